@@ -35,12 +35,29 @@ Tensor convenience:
     matmul(A, B, out=None, variant="best") -> C
     gemm(A, B, C=None, alpha=1.0, beta=0.0, variant="best") -> C
       (A, B float32; or both bfloat16 or both float16, summed in float32)
+
+Products whose stored operand is held in few bits (lowbit.py; raw entry
+points sgemm_w4*, sgemm_kv8* with the C ABI's arguments):
+    quantize_w4(W, group=128, zeros=False, scale_dtype=None) -> W4
+    dequantize_w4(W, dtype=None, out=None) -> matrix
+    gemm_w4(A, W, C=None, alpha=1.0, beta=0.0) -> C = alpha A W^T + beta C
+    KV8(K, V, Ks, Vs), KV8.empty(pages, heads, block, dim) -> cache
+    kv8_write(cache, K, V, table, lens, starts, max_new=None)
+    kv8_read(cache, table, lens, starts, rows=None, ...) -> K, V
+    kv8_attend(Q, cache, table, lens, starts, scale=None, causal=True,
+               window=0, out=None, max_new=None, workspace=None) -> O
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
+
+from . import lowbit
+from .lowbit import (KV8, SGEMM_F32, W4, KV8Batch, KV8Cache, dequantize_w4, gemm_w4, kv8_attend, kv8_read, kv8_write,
+                     quantize_w4, sgemm_kv8_attend, sgemm_kv8_attend_check_args, sgemm_kv8_attend_workspace_size,
+                     sgemm_kv8_check_args, sgemm_kv8_read, sgemm_kv8_write, sgemm_w4, sgemm_w4_check_args,
+                     sgemm_w4_dequantize, sgemm_w4_pack_check_args, sgemm_w4_quantize)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libsgemm.so")
@@ -57,6 +74,10 @@ SGEMM_ERR_ALIAS = -7
 SGEMM_ERR_OP = -8
 SGEMM_ERR_DTYPE = -9
 SGEMM_ERR_SCRATCH = -10
+SGEMM_ERR_GROUP = -11
+SGEMM_ERR_CACHE = -12
+SGEMM_ERR_HEADS = -13
+SGEMM_ERR_MASK = -14
 
 # 16-bit operand types (sgemm_lp_type).
 SGEMM_LP_BF16 = 1
@@ -84,7 +105,7 @@ VARIANTS = {"best": SGEMM_BEST, "naive": SGEMM_NAIVE, "tiled": SGEMM_TILED,
 EXPORTS = ("sgemm", "sgemm_check_args", "sgemm_ex", "sgemm_ex_check_args", "sgemm_ex_ws", "sgemm_ex_ws_check_args",
            "sgemm_ex_workspace_size", "sgemm_ex_noalloc", "sgemm_ex_noalloc_check_args",
            "sgemm_ex_noalloc_scratch_bytes", "sgemm_lp", "sgemm_lp_check_args", "sgemm_status_string", "sgemm_variant_name",
-           "sgemm_best_variant", "sgemm_mfma_tile", "sgemm_mfma_shape", "sgemm_regblock_tile")
+           "sgemm_best_variant", "sgemm_mfma_tile", "sgemm_mfma_shape", "sgemm_regblock_tile") + lowbit.EXPORTS
 
 _lib = None
 
@@ -148,6 +169,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sgemm_mfma_shape.restype = i
     lib.sgemm_regblock_tile.argtypes = [i, i, i]
     lib.sgemm_regblock_tile.restype = i
+    lowbit.declare(lib)
     if path is None:
         _lib = lib
     return lib

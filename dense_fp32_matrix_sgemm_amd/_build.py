@@ -23,8 +23,10 @@ LIB_PATH = os.path.join(LIBDIR, "libsgemm.so")
 
 ARCH = "gfx950"
 HIP_SOURCES = ["api.hip", "naive.hip", "tiled.hip", "regblock.hip", "scale.hip",
-               "mfma_nn.hip", "mfma_nt.hip", "mfma_tn.hip", "mfma_tt.hip", "lowp_bf16.hip", "lowp_f16.hip", "noalloc.hip"]
-CXX_SOURCES = ["args.cpp", "select.cpp"]
+               "mfma_nn.hip", "mfma_nt.hip", "mfma_tn.hip", "mfma_tt.hip", "lowp_bf16.hip", "lowp_f16.hip", "noalloc.hip",
+               "lowbit_api.hip", "w4_f32.hip", "w4_bf16.hip", "w4_f16.hip", "w4_pack.hip", "kv8.hip",
+               "kv8_attend_f32.hip", "kv8_attend_bf16.hip", "kv8_attend_f16.hip"]
+CXX_SOURCES = ["args.cpp", "select.cpp", "args_lowbit.cpp"]
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

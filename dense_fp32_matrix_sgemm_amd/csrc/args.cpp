@@ -121,6 +121,10 @@ extern "C" const char *sgemm_status_string(int status)
     case SGEMM_ERR_OP: return "transpose flag is neither SGEMM_OP_N nor SGEMM_OP_T";
     case SGEMM_ERR_DTYPE: return "16-bit operand type is neither SGEMM_LP_BF16 nor SGEMM_LP_F16";
     case SGEMM_ERR_SCRATCH: return "the product needs more scratch than the library's static buffer holds";
+    case SGEMM_ERR_GROUP: return "group is not a positive multiple of 32";
+    case SGEMM_ERR_CACHE: return "block, dim or alignment of the cache is not one the kernels take";
+    case SGEMM_ERR_HEADS: return "query heads are not a positive multiple of the cache's heads";
+    case SGEMM_ERR_MASK: return "causal is neither 0 nor 1, or the window is negative or without causal";
     default: return "unknown status";
     }
 }

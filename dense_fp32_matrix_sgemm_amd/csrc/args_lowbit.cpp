@@ -1,0 +1,210 @@
+// Host-side argument checks of the products whose stored operand is held in
+// few bits, and the layout of attention over the device.
+//
+// Pure C++: no HIP header and no device call, like args.cpp.
+#include <cstddef>
+#include <cstdint>
+
+#include "lowbit_plan.hpp"
+#include "sgemm.h"
+
+namespace {
+
+typedef std::int64_t i64;
+
+bool known_type(int t) { return t == SGEMM_F32 || t == SGEMM_LP_BF16 || t == SGEMM_LP_F16; }
+
+int size_of(int t) { return t == SGEMM_F32 ? 4 : 2; }
+
+i64 at_least_1(i64 x) { return x > 1 ? x : 1; }
+
+// Byte range of a rows x cols row-major extent with row stride ld (elements).
+struct Span {
+    std::uintptr_t lo, hi;
+};
+
+Span span_of(const void *p, i64 rows, i64 cols, i64 ld, i64 elem)
+{
+    const std::uintptr_t base = reinterpret_cast<std::uintptr_t>(p);
+    if (p == nullptr || rows <= 0 || cols <= 0) return {base, base};
+    const unsigned __int128 bytes =
+        (static_cast<unsigned __int128>(rows - 1) * static_cast<unsigned __int128>(ld) + static_cast<unsigned __int128>(cols)) *
+        static_cast<unsigned __int128>(elem);
+    const std::uintptr_t room = UINTPTR_MAX - base;
+    return {base, bytes > room ? UINTPTR_MAX : base + static_cast<std::uintptr_t>(bytes)};
+}
+
+bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+
+i64 groups_of(int K, int group) { return (i64(K) + group - 1) / group; }
+
+int check_group(int group) { return group <= 0 || group % 32 != 0 ? SGEMM_ERR_GROUP : SGEMM_OK; }
+
+// Leading dimensions of the W4 form itself.
+bool w4_ld_ok(int K, int group, int ldw, int lds, const void *Z, int ldz)
+{
+    const i64 g = at_least_1(groups_of(K, group));
+    return ldw >= at_least_1((i64(K) + 1) / 2) && lds >= g && (Z == nullptr || ldz >= g);
+}
+
+bool aligned16(const void *p) { return reinterpret_cast<std::uintptr_t>(p) % 16 == 0; }
+
+int check_cache_batch(const sgemm_kv8_cache *c, const sgemm_kv8_batch *b)
+{
+    if (c == nullptr || b == nullptr) return SGEMM_ERR_NULL;
+    if (c->pages < 1 || c->heads < 1 || b->seqs < 0 || b->table_ld < 0 || b->rows < 0 || b->max_new < 0) return SGEMM_ERR_DIM;
+    const bool power = c->block >= 16 && c->block <= 1024 && (c->block & (c->block - 1)) == 0;
+    if (!power || c->dim < 16 || c->dim > 256 || c->dim % 16 != 0) return SGEMM_ERR_CACHE;
+    if (!aligned16(c->K) || !aligned16(c->V)) return SGEMM_ERR_CACHE;
+    return SGEMM_OK;
+}
+
+// A rows x heads x dim operand whose rows lie apart (heads inside a row) or
+// whose heads do (rows inside a head); one row or one head needs no stride.
+bool strides_ok(int rows, int heads, int dim, int ld, int hs)
+{
+    if (rows == 0) return true;
+    if (rows == 1) return heads == 1 || hs >= dim;
+    if (heads == 1) return ld >= dim;
+    return (hs >= dim && ld >= i64(heads - 1) * hs + dim) || (ld >= dim && hs >= i64(rows - 1) * ld + dim);
+}
+
+Span rows_span(const void *p, int rows, int heads, int dim, int ld, int hs, int elem)
+{
+    const i64 last = (rows > 1 ? i64(rows - 1) * ld : 0) + (heads > 1 ? i64(heads - 1) * hs : 0) + dim;
+    return span_of(p, 1, last, last, elem);
+}
+
+bool missing_arrays(const sgemm_kv8_cache *c, const sgemm_kv8_batch *b)
+{
+    return c->K == nullptr || c->V == nullptr || c->Ks == nullptr || c->Vs == nullptr || b->lens == nullptr ||
+           b->starts == nullptr || (b->table == nullptr && b->table_ld > 0);
+}
+
+bool overlaps_cache(Span x, const sgemm_kv8_cache *c)
+{
+    const i64 ph = i64(c->pages) * c->heads, codes = i64(c->block) * c->dim;
+    return overlap(x, span_of(c->K, ph, codes, codes, 1)) || overlap(x, span_of(c->V, ph, codes, codes, 1)) ||
+           overlap(x, span_of(c->Ks, 1, ph, ph, 4)) || overlap(x, span_of(c->Vs, 1, ph, ph, 4));
+}
+
+bool overlaps_batch(Span x, const sgemm_kv8_batch *b)
+{
+    return overlap(x, span_of(b->table, b->seqs, b->table_ld, b->table_ld, 4)) || overlap(x, span_of(b->lens, 1, b->seqs, b->seqs, 4)) ||
+           overlap(x, span_of(b->starts, 1, i64(b->seqs) + 1, i64(b->seqs) + 1, 4));
+}
+
+}  // namespace
+
+extern "C" int sgemm_w4_check_args(int dtype, int stype, int M, int N, int K, int group, float alpha, const void *A,
+                                   int lda, const unsigned char *W, int ldw, const void *S, int lds,
+                                   const unsigned char *Z, int ldz, float beta, const float *C, int ldc)
+{
+    (void)beta;
+    if (!known_type(dtype) || !known_type(stype)) return SGEMM_ERR_DTYPE;
+    if (M < 0 || N < 0 || K < 0) return SGEMM_ERR_DIM;
+    if (check_group(group) != SGEMM_OK) return SGEMM_ERR_GROUP;
+    if (lda < at_least_1(K) || !w4_ld_ok(K, group, ldw, lds, Z, ldz) || ldc < at_least_1(N)) return SGEMM_ERR_LD;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (C == nullptr) return SGEMM_ERR_NULL;
+    if (K > 0 && alpha != 0.0f) {
+        if (A == nullptr || W == nullptr || S == nullptr) return SGEMM_ERR_NULL;
+        const Span c = span_of(C, M, N, ldc, 4);
+        const i64 g = groups_of(K, group);
+        if (overlap(c, span_of(A, M, K, lda, size_of(dtype))) || overlap(c, span_of(W, N, (i64(K) + 1) / 2, ldw, 1)) ||
+            overlap(c, span_of(S, N, g, lds, size_of(stype))) || overlap(c, span_of(Z, N, g, ldz, 1)))
+            return SGEMM_ERR_ALIAS;
+    }
+    return SGEMM_OK;
+}
+
+extern "C" int sgemm_w4_pack_check_args(int dtype, int stype, int N, int K, int group, const void *B, int ldb,
+                                        const unsigned char *W, int ldw, const void *S, int lds,
+                                        const unsigned char *Z, int ldz)
+{
+    if (!known_type(dtype) || !known_type(stype)) return SGEMM_ERR_DTYPE;
+    if (N < 0 || K < 0) return SGEMM_ERR_DIM;
+    if (check_group(group) != SGEMM_OK) return SGEMM_ERR_GROUP;
+    if (ldb < at_least_1(K) || !w4_ld_ok(K, group, ldw, lds, Z, ldz)) return SGEMM_ERR_LD;
+    if (N == 0 || K == 0) return SGEMM_OK;
+    if (B == nullptr || W == nullptr || S == nullptr) return SGEMM_ERR_NULL;
+    const i64 g = groups_of(K, group);
+    const Span spans[] = {span_of(B, N, K, ldb, size_of(dtype)), span_of(W, N, (i64(K) + 1) / 2, ldw, 1),
+                          span_of(S, N, g, lds, size_of(stype)), span_of(Z, N, g, ldz, 1)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(spans[i], spans[j])) return SGEMM_ERR_ALIAS;
+    return SGEMM_OK;
+}
+
+extern "C" int sgemm_kv8_check_args(const sgemm_kv8_cache *c, const sgemm_kv8_batch *b, int dtype, const void *K,
+                                    int ldk, int hsk, const void *V, int ldv, int hsv)
+{
+    if (!known_type(dtype)) return SGEMM_ERR_DTYPE;
+    const int rc = check_cache_batch(c, b);
+    if (rc != SGEMM_OK) return rc;
+    if (!strides_ok(b->rows, c->heads, c->dim, ldk, hsk) || !strides_ok(b->rows, c->heads, c->dim, ldv, hsv)) return SGEMM_ERR_LD;
+    if (b->seqs == 0 || b->rows == 0) return SGEMM_OK;
+    if (missing_arrays(c, b) || K == nullptr || V == nullptr) return SGEMM_ERR_NULL;
+    const Span k = rows_span(K, b->rows, c->heads, c->dim, ldk, hsk, size_of(dtype));
+    const Span v = rows_span(V, b->rows, c->heads, c->dim, ldv, hsv, size_of(dtype));
+    if (overlaps_cache(k, c) || overlaps_cache(v, c)) return SGEMM_ERR_ALIAS;
+    return SGEMM_OK;
+}
+
+extern "C" int sgemm_kv8_attend_check_args(const sgemm_kv8_cache *c, const sgemm_kv8_batch *b, int dtype, int heads_q,
+                                           const void *Q, int ldq, int hsq, float scale, int causal, int window,
+                                           const float *O, int ldo, int hso, const void *workspace,
+                                           std::size_t workspace_bytes)
+{
+    (void)scale;
+    if (!known_type(dtype)) return SGEMM_ERR_DTYPE;
+    const int rc = check_cache_batch(c, b);
+    if (rc != SGEMM_OK) return rc;
+    if (heads_q < 1 || heads_q % c->heads != 0) return SGEMM_ERR_HEADS;
+    if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && causal == 0)) return SGEMM_ERR_MASK;
+    if (!strides_ok(b->rows, heads_q, c->dim, ldq, hsq) || !strides_ok(b->rows, heads_q, c->dim, ldo, hso)) return SGEMM_ERR_LD;
+    if (b->seqs == 0 || b->rows == 0) return SGEMM_OK;
+    if (missing_arrays(c, b) || Q == nullptr || O == nullptr) return SGEMM_ERR_NULL;
+    const Span o = rows_span(O, b->rows, heads_q, c->dim, ldo, hso, 4);
+    const Span q = rows_span(Q, b->rows, heads_q, c->dim, ldq, hsq, size_of(dtype));
+    if (overlap(o, q) || overlaps_cache(o, c) || overlaps_batch(o, b)) return SGEMM_ERR_ALIAS;
+    if (workspace != nullptr && workspace_bytes > 0) {
+        const std::uintptr_t base = reinterpret_cast<std::uintptr_t>(workspace);
+        const Span w{base, workspace_bytes > UINTPTR_MAX - base ? UINTPTR_MAX : base + workspace_bytes};
+        if (overlap(w, o) || overlap(w, q) || overlaps_cache(w, c) || overlaps_batch(w, b)) return SGEMM_ERR_ALIAS;
+    }
+    return SGEMM_OK;
+}
+
+namespace sgemm_impl {
+
+bool kv8_read_overlaps(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int dtype, const void *K, int ldk, int hsk,
+                       const void *V, int ldv, int hsv)
+{
+    const Span k = rows_span(K, b.rows, c.heads, c.dim, ldk, hsk, size_of(dtype));
+    const Span v = rows_span(V, b.rows, c.heads, c.dim, ldv, hsv, size_of(dtype));
+    return overlap(k, v) || overlaps_batch(k, &b) || overlaps_batch(v, &b);
+}
+
+Kv8Plan plan_kv8_attend(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus)
+{
+    (void)window;
+    (void)cus;
+    Kv8Plan plan{1, 1, 1};
+    const i64 rows = i64(b.max_new < b.rows ? b.max_new : b.rows) * (heads_q / c.heads);
+    const i64 tiles = (rows + 16 * plan.mt - 1) / (16 * plan.mt);
+    plan.tiles = int(tiles < 1 ? 1 : tiles < (1 << 20) ? tiles : (1 << 20));
+    return plan;
+}
+
+}  // namespace sgemm_impl
+
+extern "C" size_t sgemm_kv8_attend_workspace_size(const sgemm_kv8_cache *c, const sgemm_kv8_batch *b, int heads_q,
+                                                  int window, int cus)
+{
+    if (check_cache_batch(c, b) != SGEMM_OK || heads_q < 1 || heads_q % c->heads != 0 || window < 0) return 0;
+    const sgemm_impl::Kv8Plan plan = sgemm_impl::plan_kv8_attend(*c, *b, heads_q, window, cus);
+    (void)plan;
+    return 0;
+}

@@ -1,0 +1,223 @@
+// The 8-bit cache of keys and values: quantising new rows into its pages
+// (sgemm_kv8_write) and reading rows back (sgemm_kv8_read).
+//
+// A page and head share one scale, a power of two: e4m3 is a floating format,
+// so the choice of power costs no precision but at its subnormal end, dividing
+// by it is exact, and a page whose scale rises while it fills keeps its older
+// codes' values exactly (again but for subnormals), however often it rises.
+//
+// Work is laid out by what shares a scale: one work-group for each sequence,
+// page that the sequence's rows reach, head, and K or V. It alone reads and
+// writes that scale and those codes, so nothing is atomic and the result does
+// not depend on timing. Both kernels are bound by memory: rows come in once
+// (a second pass over them, after the maximum is known, hits the caches).
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm.hpp"
+#include "kv8.hpp"
+#include "lowbit.hpp"
+
+namespace sgemm_impl {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Pages that n rows reach at most.
+std::int64_t pages_reached(std::int64_t n, int block) { return n < 1 ? 1 : (n + block - 2) / block + 1; }
+
+struct Grid {
+    unsigned pieces, groups;
+};
+
+// Work-groups: pieces (pages) x sequences x heads x {K, V}, the pages cut so
+// that the launch stays in range; a kernel walks the pages beyond.
+Grid grid_of(const Kv8Problem &p)
+{
+    const std::int64_t n = p.b.max_new < p.b.rows ? p.b.max_new : p.b.rows;
+    std::int64_t pieces = pages_reached(n, p.c.block);
+    const std::int64_t others = 2 * std::int64_t(p.b.seqs) * p.c.heads;
+    const std::int64_t most = (std::int64_t(1) << 23) / others;
+    if (pieces > most) pieces = most < 1 ? 1 : most;
+    const std::int64_t groups = pieces * others;
+    // Sequences x heads beyond the grid are walked too.
+    return {unsigned(pieces), unsigned(groups < (std::int64_t(1) << 23) ? groups : (std::int64_t(1) << 23))};
+}
+
+// One work-group's share: rows of sequence `seq` in one page.
+struct Piece {
+    int head, kv;
+    Kv8Sequence s;
+    std::int64_t page;  // within the sequence
+};
+
+// Calls body(piece) for every piece that falls to this work-group.
+template <class Body> __device__ inline void for_each_piece(const Kv8Problem &p, unsigned pieces, Body &&body)
+{
+    const std::int64_t all = 2 * std::int64_t(pieces) * p.b.seqs * p.c.heads;
+    for (std::int64_t id = blockIdx.x; id < all; id += gridDim.x) {
+        Piece w;
+        w.kv = int(id & 1);
+        std::int64_t rest = id >> 1;
+        w.head = int(rest % p.c.heads);
+        rest /= p.c.heads;
+        const std::int64_t first = rest % pieces;
+        w.s = kv8_sequence(p.b, int(rest / pieces));
+        if (w.s.n == 0) continue;
+        const std::int64_t from = w.s.len - w.s.n > 0 ? w.s.len - w.s.n : 0;
+        for (w.page = from / p.c.block + first; w.page * p.c.block < w.s.len; w.page += pieces) body(w);
+    }
+}
+
+// The largest |x| among the finite of eight elements, as bits.
+template <class T> __device__ inline std::uint32_t largest(const typename T::elem *x, std::uint32_t m)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const std::uint32_t a = f32_bits(to_f32<T>(x[i])) & 0x7fffffffu;
+        m = a < 0x7f800000u && a > m ? a : m;
+    }
+    return m;
+}
+
+// The smallest power of two s >= 2^-126 with amax / s <= 448 = 1.75 * 2^8; 0
+// for 0.
+__device__ inline float scale_for(std::uint32_t amax)
+{
+    if (amax == 0) return 0.0f;
+    int field = int(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return bits_f32(std::uint32_t(field < 1 ? 1 : field) << 23);
+}
+
+__device__ inline std::uint32_t to_codes(float a, float b, float c, float d)
+{
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return std::uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+}
+
+template <class T> struct Eight {
+    typename T::elem x[8];
+};
+
+template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(Kv8Problem p, unsigned pieces)
+{
+    typedef typename T::elem elem;
+    __shared__ std::uint32_t wave_max[kThreads / 64];
+    const int dim = p.c.dim, block = p.c.block, per_row = dim / 8;
+    for_each_piece(p, pieces, [&](const Piece &w) {
+        const std::int64_t start = w.s.len - w.s.n;  // position of the sequence's first row (may be below 0)
+        const std::int64_t t0 = w.page * block;
+        const std::int64_t lo = start > t0 ? start : t0, hi = w.s.len < t0 + block ? w.s.len : t0 + block;
+        const std::int64_t page = kv8_page(p.c, p.b, w.s.seq, w.page);
+        if (page < 0) return;  // the same for the whole work-group
+        const int kept = int(lo - t0), fresh = int(hi - lo) * per_row;
+        const elem *src = static_cast<const elem *>(w.kv ? p.V : p.K) + w.head * (w.kv ? p.hsv : p.hsk);
+        const std::int64_t ld = w.kv ? p.ldv : p.ldk, row0 = w.s.row0 + (lo - start);
+        std::uint8_t *codes = static_cast<std::uint8_t *>(w.kv ? p.c.V : p.c.K) + (page * p.c.heads + w.head) * block * dim;
+        float *scale = (w.kv ? p.c.Vs : p.c.Ks) + page * p.c.heads + w.head;
+        const float before = kept > 0 ? *scale : 0.0f;
+
+        std::uint32_t m = 0;
+        for (int e = threadIdx.x; e < fresh; e += kThreads) {
+            const Eight<T> v = load_any<Eight<T>>(src + (row0 + e / per_row) * ld + e % per_row * 8);
+            m = largest<T>(v.x, m);
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            const std::uint32_t o = std::uint32_t(__shfl_xor(int(m), d));
+            m = o > m ? o : m;
+        }
+        if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 64; ++i) m = wave_max[i] > m ? wave_max[i] : m;
+        const float s = __builtin_fmaxf(scale_for(m), before);
+        const float inverse = s > 0.0f ? 1.0f / s : 0.0f;
+
+        if (s != before) {
+            // The page's earlier tokens, rounded to the risen scale.
+            const float ratio = before * inverse;
+            for (int e = threadIdx.x; e < kept * per_row; e += kThreads) {
+                u32x2 *at = reinterpret_cast<u32x2 *>(codes + e * 8);
+                u32x2 v = *at;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[i]), false);
+                    const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[i]), true);
+                    v[i] = to_codes(a[0] * ratio, a[1] * ratio, b[0] * ratio, b[1] * ratio);
+                }
+                *at = v;
+            }
+        }
+        for (int e = threadIdx.x; e < fresh; e += kThreads) {
+            const Eight<T> v = load_any<Eight<T>>(src + (row0 + e / per_row) * ld + e % per_row * 8);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = to_f32<T>(v.x[i]);
+                x[i] = (f32_bits(a) & 0x7f800000u) == 0x7f800000u ? __builtin_nanf("") : a * inverse;
+            }
+            *reinterpret_cast<u32x2 *>(codes + kept * dim + e * 8) =
+                u32x2{to_codes(x[0], x[1], x[2], x[3]), to_codes(x[4], x[5], x[6], x[7])};
+        }
+        __syncthreads();  // every thread has read the scale and wave_max
+        if (threadIdx.x == 0) *scale = s;
+    });
+}
+
+template <class T> __global__ __launch_bounds__(kThreads) void kv8_read_kernel(Kv8Problem p, unsigned pieces)
+{
+    typedef typename T::elem elem;
+    const int dim = p.c.dim, block = p.c.block, per_row = dim / 8;
+    for_each_piece(p, pieces, [&](const Piece &w) {
+        const std::int64_t start = w.s.len - w.s.n, t0 = w.page * block;
+        const std::int64_t lo = start > t0 ? start : t0, hi = w.s.len < t0 + block ? w.s.len : t0 + block;
+        const std::int64_t page = kv8_page(p.c, p.b, w.s.seq, w.page);
+        const int count = int(hi - lo) * per_row;
+        elem *dst = static_cast<elem *>(w.kv ? p.V : p.K) + w.head * (w.kv ? p.hsv : p.hsk);
+        const std::int64_t ld = w.kv ? p.ldv : p.ldk, row0 = w.s.row0 + (lo - start);
+        const std::int64_t at = (page < 0 ? 0 : page) * p.c.heads + w.head;
+        const std::uint8_t *codes = static_cast<const std::uint8_t *>(w.kv ? p.c.V : p.c.K) + at * block * dim + (lo - t0) * dim;
+        const float s = page < 0 ? __builtin_nanf("") : (w.kv ? p.c.Vs : p.c.Ks)[at];
+        for (int e = threadIdx.x; e < count; e += kThreads) {
+            u32x2 v = {0, 0};
+            if (page >= 0) v = *reinterpret_cast<const u32x2 *>(codes + e * 8);
+            Eight<T> out;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[i]), false);
+                const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[i]), true);
+                out.x[4 * i] = from_f32<T>(a[0] * s);
+                out.x[4 * i + 1] = from_f32<T>(a[1] * s);
+                out.x[4 * i + 2] = from_f32<T>(b[0] * s);
+                out.x[4 * i + 3] = from_f32<T>(b[1] * s);
+            }
+            __builtin_memcpy(dst + (row0 + e / per_row) * ld + e % per_row * 8, &out, sizeof(out));
+        }
+    });
+}
+
+template <class F> hipError_t launch(const Kv8Problem &p, F f32, F bf16, F f16, hipStream_t stream)
+{
+    const Grid g = grid_of(p);
+    const F kernel = p.dtype == SGEMM_F32 ? f32 : p.dtype == SGEMM_LP_BF16 ? bf16 : f16;
+    Kv8Problem q = p;
+    unsigned pieces = g.pieces;
+    void *args[] = {&q, &pieces};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(g.groups), dim3(kThreads), args, 0, stream);
+}
+
+}  // namespace
+
+hipError_t launch_kv8_write(const Kv8Problem &p, hipStream_t stream)
+{
+    return launch(p, &kv8_write_kernel<F32>, &kv8_write_kernel<BF16>, &kv8_write_kernel<F16>, stream);
+}
+
+hipError_t launch_kv8_read(const Kv8Problem &p, hipStream_t stream)
+{
+    return launch(p, &kv8_read_kernel<F32>, &kv8_read_kernel<BF16>, &kv8_read_kernel<F16>, stream);
+}
+
+}  // namespace sgemm_impl

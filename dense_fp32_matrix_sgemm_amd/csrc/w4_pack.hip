@@ -1,0 +1,195 @@
+// Quantising a matrix to the W4 form (sgemm_w4_quantize) and reading it back
+// (sgemm_w4_dequantize). Both are bound by memory: each matrix is moved once.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "lowbit.hpp"
+
+namespace sgemm_impl {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <class T> struct Eight {
+    typename T::elem x[8];
+};
+
+// Eight elements of a row from k on as float32; zeros from the row's end on.
+template <class T> __device__ inline void load8(const typename T::elem *row, int k, int K, float *x)
+{
+    Eight<T> v;
+    if (k + 8 <= K) {
+        v = load_any<Eight<T>>(row + k);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.x[i] = k + i < K ? row[k + i] : typename T::elem(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32<T>(v.x[i]);
+}
+
+__device__ inline float store_scale(void *S, int stype, std::int64_t i, float s)
+{
+    if (stype == SGEMM_F32) {
+        static_cast<float *>(S)[i] = s;
+        return s;
+    }
+    const std::uint16_t b = stype == SGEMM_LP_BF16 ? from_f32<BF16>(s) : from_f32<F16>(s);
+    static_cast<std::uint16_t *>(S)[i] = b;
+    return stype == SGEMM_LP_BF16 ? to_f32<BF16>(b) : to_f32<F16>(b);
+}
+
+// round(x / s) with ties to even, as if the quotient were exact, for |x / s|
+// up to 16 or so: the float32 quotient may round onto or over a tie, so its
+// nearest integer is corrected by the exact remainder x - r s (one fused
+// multiply-add; next to a tie it is a multiple of x's or s's last place and
+// fits float32).
+__device__ inline float rounded_quotient(float x, float s, float inverse)
+{
+    float r = __builtin_rintf(x * inverse);
+    const float d = __builtin_fmaf(-r, s, x), half = 0.5f * s;
+    const bool odd = (int(r) & 1) != 0;
+    if (d > half || (d == half && odd)) r += 1.0f;
+    if (d < -half || (d == -half && odd)) r -= 1.0f;
+    return r;
+}
+
+// LG lanes (a power of two) share one group and take eight k each in turn.
+template <class T, int LG, bool ZP>
+__global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, int groups, std::int64_t all)
+{
+    const int part = threadIdx.x % LG;
+    for (std::int64_t id = std::int64_t(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG; id < all;
+         id += std::int64_t(gridDim.x) * (kThreads / LG)) {
+        const std::int64_t n = id / groups;
+        const int g = int(id % groups);
+        const int k0 = g * p.group, k1 = p.K - k0 < p.group ? p.K : k0 + p.group;
+        const typename T::elem *row = static_cast<const typename T::elem *>(p.B) + n * p.ldb;
+        float lo = 0.0f, hi = 0.0f, x[8];
+        bool fine = true;
+        for (int k = k0 + 8 * part; k < k1; k += 8 * LG) {
+            load8<T>(row, k, k1, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                fine = fine && (f32_bits(x[i]) & 0x7f800000u) != 0x7f800000u;
+                lo = __builtin_fminf(lo, x[i]);
+                hi = __builtin_fmaxf(hi, x[i]);
+            }
+        }
+#pragma unroll
+        for (int d = LG / 2; d > 0; d /= 2) {
+            lo = __builtin_fminf(lo, __shfl_xor(lo, d));
+            hi = __builtin_fmaxf(hi, __shfl_xor(hi, d));
+            fine = __shfl_xor(int(fine), d) != 0 && fine;
+        }
+        float s = ZP ? (hi - lo) / 15.0f : __builtin_fmaxf(hi, -lo) / 7.0f;
+        if (!fine) s = __builtin_nanf("");
+        // Every lane of the group rounds the scale; the first stores it.
+        if (p.stype == SGEMM_LP_BF16) s = to_f32<BF16>(from_f32<BF16>(s));
+        if (p.stype == SGEMM_LP_F16) s = to_f32<F16>(from_f32<F16>(s));
+        const bool flat = !(s > 0.0f) || __builtin_isinf(s);
+        // Quotients are formed on values moved away from the subnormals.
+        const float up = s < 0x1p-90f ? 0x1p90f : 1.0f, scale = s * up;
+        const float inverse = flat ? 0.0f : 1.0f / scale;
+        float z = 8.0f;
+        if (ZP && !flat) z = __builtin_fminf(rounded_quotient(-lo * up, scale, inverse), 15.0f);
+        if (part == 0) {
+            store_scale(p.S, p.stype, n * p.lds + g, s);
+            if (ZP) p.Z[n * p.ldz + g] = std::uint8_t(z);
+        }
+        for (int k = k0 + 8 * part; k < k1; k += 8 * LG) {
+            load8<T>(row, k, k1, x);
+            std::uint32_t w = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float q = z;
+                if (!flat) q += __builtin_fminf(__builtin_fmaxf(rounded_quotient(x[i] * up, scale, inverse), -15.0f), 15.0f);
+                q = __builtin_fminf(__builtin_fmaxf(q, 0.0f), 15.0f);
+                if (k + i < k1) w |= std::uint32_t(q) << (4 * i);
+            }
+            std::uint8_t *dst = p.W + n * p.ldw + k / 2;
+            if (k + 8 <= k1) {
+                __builtin_memcpy(dst, &w, 4);
+            } else {
+                for (int i = 0; k + 2 * i < k1; ++i) dst[i] = std::uint8_t(w >> (8 * i));
+            }
+        }
+    }
+}
+
+template <class T, bool ZP>
+__global__ __launch_bounds__(kThreads) void w4_dequantize_kernel(W4PackProblem p, int eights, std::int64_t all)
+{
+    for (std::int64_t id = std::int64_t(blockIdx.x) * kThreads + threadIdx.x; id < all; id += std::int64_t(gridDim.x) * kThreads) {
+        const std::int64_t n = id / eights;
+        const int k = int(id % eights) * 8, g = k / p.group;
+        const std::uint8_t *src = p.W + n * p.ldw + k / 2;
+        const int rest = p.K - k;
+        std::uint32_t w = 0;
+        if (rest >= 7) {
+            w = load_any<std::uint32_t>(src);
+        } else {
+            for (int i = 0; 2 * i < rest; ++i) w |= std::uint32_t(src[i]) << (8 * i);
+        }
+        const float s = load_scale(p.S, p.stype, n * p.lds + g);
+        const int z = ZP ? p.Z[n * p.ldz + g] & 15 : 8;
+        Eight<T> v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.x[i] = from_f32<T>(s * float(int((w >> (4 * i)) & 15u) - z));
+        typename T::elem *dst = static_cast<typename T::elem *>(p.B) + n * p.ldb + k;
+        if (rest >= 8) {
+            __builtin_memcpy(dst, &v, sizeof(v));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < rest) dst[i] = v.x[i];
+        }
+    }
+}
+
+unsigned grid_for(std::int64_t groups) { return unsigned(groups < (1 << 22) ? groups : (1 << 22)); }
+
+template <class T, int LG> hipError_t quantize(const W4PackProblem &p, hipStream_t stream)
+{
+    int groups = (p.K + p.group - 1) / p.group;
+    std::int64_t all = std::int64_t(p.N) * groups;
+    W4PackProblem q = p;
+    void *args[] = {&q, &groups, &all};
+    const void *kernel = p.Z ? reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, true>)
+                             : reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, false>);
+    return hipLaunchKernel(kernel, dim3(grid_for((all + kThreads / LG - 1) / (kThreads / LG))), dim3(kThreads), args, 0, stream);
+}
+
+template <class T> hipError_t quantize(const W4PackProblem &p, hipStream_t stream)
+{
+    if (p.group <= 32) return quantize<T, 4>(p, stream);
+    if (p.group <= 64) return quantize<T, 8>(p, stream);
+    if (p.group <= 128) return quantize<T, 16>(p, stream);
+    return quantize<T, 32>(p, stream);
+}
+
+template <class T> hipError_t dequantize(const W4PackProblem &p, hipStream_t stream)
+{
+    int eights = int((std::int64_t(p.K) + 7) / 8);
+    std::int64_t all = std::int64_t(p.N) * eights;
+    W4PackProblem q = p;
+    void *args[] = {&q, &eights, &all};
+    const void *kernel = p.Z ? reinterpret_cast<const void *>(&w4_dequantize_kernel<T, true>)
+                             : reinterpret_cast<const void *>(&w4_dequantize_kernel<T, false>);
+    return hipLaunchKernel(kernel, dim3(grid_for((all + kThreads - 1) / kThreads)), dim3(kThreads), args, 0, stream);
+}
+
+}  // namespace
+
+hipError_t launch_w4_quantize(const W4PackProblem &p, hipStream_t stream)
+{
+    return p.dtype == SGEMM_F32 ? quantize<F32>(p, stream) : p.dtype == SGEMM_LP_BF16 ? quantize<BF16>(p, stream) : quantize<F16>(p, stream);
+}
+
+hipError_t launch_w4_dequantize(const W4PackProblem &p, hipStream_t stream)
+{
+    return p.dtype == SGEMM_F32 ? dequantize<F32>(p, stream) : p.dtype == SGEMM_LP_BF16 ? dequantize<BF16>(p, stream) : dequantize<F16>(p, stream);
+}
+
+}  // namespace sgemm_impl

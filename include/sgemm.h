@@ -50,8 +50,15 @@ typedef enum sgemm_status {
     SGEMM_ERR_ALIAS = -7,    /* C's extent overlaps A's or B's                   */
     SGEMM_ERR_OP = -8,       /* transpose flag not SGEMM_OP_N or SGEMM_OP_T      */
     SGEMM_ERR_DTYPE = -9,    /* 16-bit type not SGEMM_LP_BF16 or SGEMM_LP_F16    */
-    SGEMM_ERR_SCRATCH = -10  /* sgemm_ex_noalloc: the product needs more scratch
+    SGEMM_ERR_SCRATCH = -10, /* sgemm_ex_noalloc: the product needs more scratch
                                 than the library's static buffer holds          */
+    SGEMM_ERR_GROUP = -11,   /* sgemm_w4*: group not a positive multiple of 32   */
+    SGEMM_ERR_CACHE = -12,   /* sgemm_kv8*: block, dim or alignment of the cache
+                                not one the kernels take                        */
+    SGEMM_ERR_HEADS = -13,   /* sgemm_kv8_attend: query heads not a positive
+                                multiple of the cache's heads                   */
+    SGEMM_ERR_MASK = -14     /* sgemm_kv8_attend: causal not 0 or 1, window
+                                negative, or a window without causal            */
 } sgemm_status;
 
 /* 16-bit operand types of sgemm_lp. */
@@ -59,6 +66,12 @@ typedef enum sgemm_lp_type {
     SGEMM_LP_BF16 = 1,  /* bfloat16: the upper 16 bits of an IEEE binary32     */
     SGEMM_LP_F16 = 2    /* IEEE 754 binary16                                   */
 } sgemm_lp_type;
+
+/* Element types of the entry points that take float32 operands as well as
+ * 16-bit ones (sgemm_w4*, sgemm_kv8*): SGEMM_F32 or an sgemm_lp_type. */
+typedef enum sgemm_type {
+    SGEMM_F32 = 0  /* IEEE binary32 */
+} sgemm_type;
 
 /* Transpose flags of sgemm_ex: how an operand is stored. */
 typedef enum sgemm_op {
@@ -339,6 +352,236 @@ int sgemm_lp_check_args(int dtype, int transA, int transB, int M, int N, int K,
                         const void *B, int ldb,
                         float beta,
                         const float *C, int ldc);
+
+/*
+ * ---- Products whose stored operand is held in few bits ----
+ *
+ * sgemm_w4 multiplies by a matrix held in 4 bits, sgemm_kv8_attend attends
+ * over keys and values held in 8; the other entry points make those operands
+ * and read them back. As everywhere in this library products are summed in
+ * float32 and results are float32; codes enter the matrix cores as the whole
+ * numbers (W4) or floats (KV8) they stand for, which the 16-bit types hold
+ * exactly, and scales multiply the float32 sums. float32 operands enter as
+ * three bf16 parts that add up to them exactly.
+ *
+ * The W4 form of an N x K matrix W, in groups of `group` k of a row (a
+ * positive multiple of 32; the last group of a row may be shorter):
+ *
+ *     W[n][k] = S[n][k / group] * (q[n][k] - z)
+ *
+ *   codes   q[n][k] in 0..15: byte W[n * ldw + k / 2], the low half for even
+ *           k, the high half for odd k (unused at the end of an odd K);
+ *   scales  S[n * lds + k / group], of type stype (SGEMM_F32, SGEMM_LP_BF16
+ *           or SGEMM_LP_F16);
+ *   zeros   z = Z[n * ldz + k / group], one byte of 0..15 (higher bits are
+ *           ignored); with Z == NULL every z is 8.
+ * Rows may start at any byte (codes, zeros) or element (scales).
+ */
+
+/*
+ * C = alpha * A * W^T + beta * C with A of M x K (dtype SGEMM_F32,
+ * SGEMM_LP_BF16 or SGEMM_LP_F16, row-major, lda >= max(1, K) elements), W of
+ * N x K in the W4 form and C of M x N float32.
+ *
+ * Behaviour: as sgemm_lp. Checks, in this order, before any HIP call: types
+ * (SGEMM_ERR_DTYPE), sizes, group, leading dimensions (ldw >= max(1,
+ * ceil(K / 2)); lds and, with zeros, ldz >= max(1, ceil(K / group)); ldc >=
+ * max(1, N)), then (only if M > 0 and N > 0) NULL C and, when A and W are
+ * read (K > 0 and alpha != 0), NULL A, W or S and overlap of C with A, W, S
+ * or Z. beta == 0 never reads C. One kernel is enqueued; nothing is
+ * allocated. The result is the same on every run.
+ */
+int sgemm_w4(int dtype, int stype, int M, int N, int K, int group,
+             float alpha,
+             const void *A, int lda,
+             const unsigned char *W, int ldw,
+             const void *S, int lds,
+             const unsigned char *Z, int ldz,
+             float beta,
+             float *C, int ldc,
+             void *stream);
+
+/* The host-side argument checks of sgemm_w4() alone. */
+int sgemm_w4_check_args(int dtype, int stype, int M, int N, int K, int group,
+                        float alpha,
+                        const void *A, int lda,
+                        const unsigned char *W, int ldw,
+                        const void *S, int lds,
+                        const unsigned char *Z, int ldz,
+                        float beta,
+                        const float *C, int ldc);
+
+/*
+ * Quantises the N x K matrix B (dtype, row-major, ldb >= max(1, K)) to the W4
+ * form. For each group of a row, with rounding to nearest, ties to even:
+ *   without zeros (Z == NULL)  s = max |b| / 7, q = 8 + round(b / s) in 0..15;
+ *   with zeros                 lo = min(0, b), hi = max(0, b), s = (hi - lo) /
+ *                              15, z = round(-lo / s) in 0..15,
+ *                              q = z + round(b / s) in 0..15.
+ * hi - lo and the quotient that gives s are rounded to float32 and s then to
+ * stype; the other quotients are by that stored s and rounded once. s == 0
+ * gives codes (and z) of 8. A group that holds a value that is not finite
+ * gets the scale NaN and codes of 8, so that products with it show it.
+ *
+ * Checks: types, sizes, group, leading dimensions, then (N > 0 and K > 0)
+ * NULL B, W or S and overlap of W, S or Z with B or one another.
+ */
+int sgemm_w4_quantize(int dtype, int stype, int N, int K, int group,
+                      const void *B, int ldb,
+                      unsigned char *W, int ldw,
+                      void *S, int lds,
+                      unsigned char *Z, int ldz,
+                      void *stream);
+
+/* Reads an N x K matrix in the W4 form back into B (dtype, row-major, ldb >=
+ * max(1, K)): S * (q - z) in float32, rounded to dtype. The same checks. */
+int sgemm_w4_dequantize(int dtype, int stype, int N, int K, int group,
+                        const unsigned char *W, int ldw,
+                        const void *S, int lds,
+                        const unsigned char *Z, int ldz,
+                        void *B, int ldb,
+                        void *stream);
+
+/* The host-side argument checks of sgemm_w4_quantize() and
+ * sgemm_w4_dequantize() alone. */
+int sgemm_w4_pack_check_args(int dtype, int stype, int N, int K, int group,
+                             const void *B, int ldb,
+                             const unsigned char *W, int ldw,
+                             const void *S, int lds,
+                             const unsigned char *Z, int ldz);
+
+/*
+ * A cache of keys and values in 8-bit floats (e4m3: 1 sign, 4 exponent and 3
+ * fraction bits, bias 7, largest value 448, no infinities, NaN 0x7F / 0xFF),
+ * in pages of `block` tokens, with one float32 scale for each page and head:
+ * the value at token t, component d is code[page][head][t][d] *
+ * scale[page][head].
+ */
+typedef struct sgemm_kv8_cache {
+    void *K, *V;     /* pages x heads x block x dim codes, 16-byte aligned      */
+    float *Ks, *Vs;  /* pages x heads scales                                    */
+    int pages;       /* >= 1                                                    */
+    int heads;       /* >= 1                                                    */
+    int block;       /* tokens of a page: a power of two from 16 to 1024        */
+    int dim;         /* components of a head: a multiple of 16 from 16 to 256   */
+} sgemm_kv8_cache;
+
+/*
+ * The sequences of one call. Sequence b holds lens[b] tokens, of which this
+ * call's operand (new keys and values, queries, or a copy) covers the last
+ * starts[b + 1] - starts[b]: its rows starts[b] .. starts[b + 1] - 1, in
+ * order. Token t of sequence b lives at place t % block of page
+ * table[b * table_ld + t / block].
+ *
+ * table, lens and starts are DEVICE arrays, read by the kernels alone: what
+ * they hold is not seen by the host's checks. The kernels treat it so:
+ * lens[b] < 0 is 0; starts are cut to 0 .. rows and a falling pair covers no
+ * rows; rows at positions before token 0 have no token; a page outside 0 ..
+ * pages - 1, or a token behind the table's last column, is never read or
+ * written. Rows of the operand before starts[0] or from starts[seqs] on are
+ * left as they were.
+ */
+typedef struct sgemm_kv8_batch {
+    const int *table;   /* seqs x table_ld page numbers                         */
+    const int *lens;    /* seqs                                                 */
+    const int *starts;  /* seqs + 1                                             */
+    int seqs;
+    int table_ld;       /* columns of table, >= 0                               */
+    int rows;           /* rows of the operand                                  */
+    int max_new;        /* how many rows of one sequence the launch is laid out
+                           for; more than that is right as well, but slower     */
+} sgemm_kv8_batch;
+
+/*
+ * Quantises the last rows of each sequence into its pages. K and V are rows x
+ * heads x dim (dtype; component d of head h of row r at r * ld + h * hs + d,
+ * in elements). For each page that receives rows, head, and K and V apart:
+ *   need  = the smallest power of two s >= 2^-126 with max |x| / s <= 448
+ *           over the finite new values (0 if they are all 0);
+ *   scale = need if the page holds none of the sequence's earlier tokens,
+ *           else the larger of need and the page's scale;
+ *   code  = x / scale rounded to e4m3, ties to even (NaN for a value that is
+ *           not finite); when the scale rises, the earlier tokens' codes are
+ *           rounded to the new one.
+ * With powers of two that last rounding changes only values that fall among
+ * e4m3's subnormals. A page that receives rows must belong to one sequence
+ * and appear once in its row of the table: two writers leave codes and scale
+ * of that page undefined (nothing else).
+ *
+ * Checks, in this order: dtype, sizes (pages, heads, seqs, table_ld, rows,
+ * max_new), cache (block, dim, alignment), strides (elements must not share
+ * places: heads inside a row, hs >= dim and ld >= (heads - 1) * hs + dim, or
+ * rows inside a head, ld >= dim and hs >= (rows - 1) * ld + dim), then (seqs
+ * > 0 and rows > 0) NULL pointers and overlap of the operand with the cache.
+ * One kernel is enqueued.
+ */
+int sgemm_kv8_write(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype,
+                    const void *K, int ldk, int hsk,
+                    const void *V, int ldv, int hsv,
+                    void *stream);
+
+/* The last rows of each sequence read back: code * scale in float32, rounded
+ * to dtype, into K and V (rows x heads x dim, strides as above). A row whose
+ * page is not one of the cache's reads NaN; a row before token 0 is left as
+ * it was. The same checks. */
+int sgemm_kv8_read(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype,
+                   void *K, int ldk, int hsk,
+                   void *V, int ldv, int hsv,
+                   void *stream);
+
+/* The host-side argument checks of sgemm_kv8_write() and sgemm_kv8_read()
+ * alone. */
+int sgemm_kv8_check_args(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype,
+                         const void *K, int ldk, int hsk,
+                         const void *V, int ldv, int hsv);
+
+/*
+ * Softmax attention over the cache:
+ *
+ *     O[r][h] = sum_t p_t V_t,   p = softmax over t of scale * <Q[r][h], K_t>
+ *
+ * for query heads h = 0 .. heads_q - 1, a multiple of the cache's heads;
+ * query head h reads the cache's head h / (heads_q / heads). Row r = starts[b]
+ * + i of sequence b stands at position p = lens[b] - n + i, n being the
+ * sequence's rows. It sees
+ *   causal == 0              tokens 0 .. lens[b] - 1;
+ *   causal == 1, window == 0 tokens 0 .. p;
+ *   causal == 1, window > 0  tokens p - window + 1 .. p.
+ * A row that sees no token gets zeros; one that sees a token on a page that
+ * is not the cache's gets NaN. Tokens a row does not see do not reach it, not
+ * even as NaN.
+ *
+ * Q is rows x heads_q x dim (dtype), O the same in float32 (strides as for
+ * sgemm_kv8_write). Sequences too few to fill the device are split along
+ * their tokens if `workspace` (device memory, 16-byte aligned) has at least
+ * sgemm_kv8_attend_workspace_size() bytes; else they are not. Split or not,
+ * the result is the same on every run; the two differ in their last bits.
+ * Calls that share a workspace must be ordered on one stream.
+ *
+ * Checks, in this order: dtype, sizes, cache, heads (SGEMM_ERR_HEADS), mask
+ * (SGEMM_ERR_MASK), strides, then (seqs > 0 and rows > 0) NULL pointers and
+ * overlap of O with Q, the cache or the workspace. One or two kernels are
+ * enqueued.
+ */
+int sgemm_kv8_attend(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype, int heads_q,
+                     const void *Q, int ldq, int hsq,
+                     float scale, int causal, int window,
+                     float *O, int ldo, int hso,
+                     void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/* The host-side argument checks of sgemm_kv8_attend() alone. */
+int sgemm_kv8_attend_check_args(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype, int heads_q,
+                                const void *Q, int ldq, int hsq,
+                                float scale, int causal, int window,
+                                const float *O, int ldo, int hso,
+                                const void *workspace, size_t workspace_bytes);
+
+/* Workspace bytes with which sgemm_kv8_attend splits this call's sequences on
+ * a device with `cus` compute units (cus <= 0: 256), or 0 when it would not
+ * split them (or the sizes are invalid). Pure host logic; reads no array. */
+size_t sgemm_kv8_attend_workspace_size(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int heads_q,
+                                       int window, int cus);
 
 /* Static English text for a status code ("unknown status" otherwise). */
 const char *sgemm_status_string(int status);
