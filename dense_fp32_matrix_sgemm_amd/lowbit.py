@@ -57,10 +57,16 @@ def declare(lib) -> None:
     lib.sgemm_kv8_attend_workspace_size.restype = sz
 
 
-def _lib():
-    from . import load_library
+_LIB = None
 
-    return load_library()
+
+def _lib():
+    global _LIB
+    if _LIB is None:
+        from . import load_library
+
+        _LIB = load_library()
+    return _LIB
 
 
 def sgemm_w4(*args) -> int:
@@ -108,12 +114,18 @@ def sgemm_kv8_attend_workspace_size(*args) -> int:
 
 
 # ------------------------------------------------------------ tensor helpers
+#
+# A serving program makes these calls once per layer and token, so the helpers
+# stay short: what a W4 or a KV8 holds is checked and marshalled once, when it
+# is made, and the device and stream are asked for as plain numbers.
 
+_INT32_MAX = 2**31 - 1
 
 _TYPES = None
 
 
 def _types():
+    """Type code of each element type."""
     global _TYPES
     if _TYPES is None:
         import torch
@@ -130,53 +142,59 @@ def _type_code(dtype, name):
 
 
 def _need(t, name, dim, dtypes, device=None):
-    """t, if it is a GPU tensor of `dim` dimensions and one of `dtypes` on `device`."""
+    """Checks that t is a GPU tensor of `dim` dimensions and one of `dtypes`, on `device`."""
     import torch
 
     if not isinstance(t, torch.Tensor) or t.dim() != dim:
         raise TypeError(f"{name} must be a {dim}-D torch.Tensor")
-    if dtypes is not None and t.dtype not in dtypes:
+    if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {tuple(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, is on {t.device}")
-    return t
 
 
 def _row_major(t, name):
     """Row stride of a 2-D tensor with unit column stride."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must be row-major (unit column stride)")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    if rows > 1 and ld < cols:
-        raise ValueError(f"{name}'s rows overlap (strides {tuple(t.stride())})")
-    return max(ld, 1)
+    if rows <= 1:
+        return cols or 1
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap (strides {(ld, step)})")
+    return ld or 1
 
 
 def _heads(t, name):
     """Row and head strides of a rows x heads x dim tensor with unit last stride."""
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name}'s components must be adjacent (unit last stride)")
     rows, heads, dim = t.shape
-    hs = t.stride(1) if heads > 1 else dim
-    ld = t.stride(0) if rows > 1 else max(heads * dim, 1)
+    ld, hs, step = t.stride()
+    if step != 1 and dim > 1:
+        raise ValueError(f"{name}'s components must be adjacent (unit last stride)")
+    if heads <= 1:
+        hs = dim
+    if rows <= 1:
+        ld = heads * dim or 1
+    if ld > _INT32_MAX or hs > _INT32_MAX:
+        _int32(**{f"{name}'s row stride": ld, f"{name}'s head stride": hs})
     return ld, hs
 
 
-def _launch(device, call):
-    """call(stream) with `device` current, raising on a status."""
+def _launch(index, entry, *args):
+    """entry(*args, stream) with device `index` current, on its current stream; raises on a status."""
     import torch
 
-    from . import SGEMM_OK, SgemmError
-
-    if torch.cuda.current_device() == device.index:
-        rc = call(torch.cuda.current_stream(device).cuda_stream or None)
+    if torch._C._cuda_getDevice() == index:
+        rc = entry(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            rc = call(torch.cuda.current_stream(device).cuda_stream or None)
-    if rc != SGEMM_OK:
+        with torch.cuda.device(index):
+            rc = entry(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        from . import SgemmError
+
         raise SgemmError(rc)
 
 
@@ -191,9 +209,10 @@ class W4:
     lower half of a byte first), ``scales`` (float32, bfloat16 or float16, N x
     ceil(K / group)), ``zeros`` (uint8, the same shape, or None: 8
     everywhere), and ``K`` and ``group``. Its value is
-    ``scales * (code - zeros)``. Tensors are used in place, without a copy."""
+    ``scales * (code - zeros)``. The tensors are used in place, without a
+    copy, and belong to the W4 for good (what they hold may change)."""
 
-    __slots__ = ("codes", "scales", "zeros", "K", "group")
+    __slots__ = ("_codes", "_scales", "_zeros", "_shape", "_group", "_stype", "_args", "_device")
 
     def __init__(self, codes, scales, zeros, K, group):
         import torch
@@ -202,34 +221,31 @@ class W4:
         if group <= 0 or group % 32:
             raise ValueError(f"group must be a positive multiple of 32, got {group}")
         _need(codes, "codes", 2, (torch.uint8,))
-        _need(scales, "scales", 2, tuple(_types()), codes.device)
-        groups = -(-K // group)
-        if codes.shape[1] != -(-K // 2):
+        _need(scales, "scales", 2, _types(), codes.device)
+        N, groups = codes.shape[0], -(-K // group)
+        if K < 0 or codes.shape[1] != -(-K // 2):
             raise ValueError(f"codes must have ceil(K / 2) = {-(-K // 2)} columns, has {codes.shape[1]}")
-        if tuple(scales.shape) != (codes.shape[0], groups):
-            raise ValueError(f"scales must be {codes.shape[0]} x {groups}, is {tuple(scales.shape)}")
+        if tuple(scales.shape) != (N, groups):
+            raise ValueError(f"scales must be {N} x {groups}, is {tuple(scales.shape)}")
         if zeros is not None:
             _need(zeros, "zeros", 2, (torch.uint8,), codes.device)
             if zeros.shape != scales.shape:
                 raise ValueError(f"zeros must be {tuple(scales.shape)}, is {tuple(zeros.shape)}")
-        for name, t in (("codes", codes), ("scales", scales), ("zeros", zeros)):
-            if t is not None:
-                _row_major(t, name)
-        self.codes, self.scales, self.zeros, self.K, self.group = codes, scales, zeros, K, group
+        ldw, lds = _row_major(codes, "codes"), _row_major(scales, "scales")
+        ldz = 1 if zeros is None else _row_major(zeros, "zeros")
+        _int32(N=N, K=K, group=group, ldw=ldw, lds=lds, ldz=ldz)
+        self._codes, self._scales, self._zeros, self._shape, self._group = codes, scales, zeros, (N, K), group
+        self._device, self._stype = codes.device, _types()[scales.dtype]
+        self._args = (codes.data_ptr() or None, ldw, scales.data_ptr() or None, lds,
+                      None if zeros is None else zeros.data_ptr() or None, ldz)
 
-    @property
-    def shape(self):
-        return (self.codes.shape[0], self.K)
-
-    @property
-    def device(self):
-        return self.codes.device
-
-    def _args(self):
-        z = self.zeros
-        return (self.codes.data_ptr() or None, _row_major(self.codes, "codes"), self.scales.data_ptr() or None,
-                _row_major(self.scales, "scales"), None if z is None else z.data_ptr() or None,
-                1 if z is None else _row_major(z, "zeros"))
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    zeros = property(lambda self: self._zeros)
+    shape = property(lambda self: self._shape)
+    K = property(lambda self: self._shape[1])
+    group = property(lambda self: self._group)
+    device = property(lambda self: self._device)
 
 
 def quantize_w4(W, group=128, zeros=False, scale_dtype=None):
@@ -238,21 +254,21 @@ def quantize_w4(W, group=128, zeros=False, scale_dtype=None):
     with ``zeros``, one zero point for each ``group`` elements of a row."""
     import torch
 
-    _need(W, "W", 2, tuple(_types()))
+    _need(W, "W", 2, _types())
     scale_dtype = W.dtype if scale_dtype is None else scale_dtype
-    stype = _type_code(scale_dtype, "scale_dtype")
+    _type_code(scale_dtype, "scale_dtype")
     group = int(group)
     if group <= 0 or group % 32:
         raise ValueError(f"group must be a positive multiple of 32, got {group}")
     N, K = W.shape
     ldb = _row_major(W, "W")
-    groups = -(-K // group)
-    out = W4(torch.empty((N, -(-K // 2)), dtype=torch.uint8, device=W.device),
-             torch.empty((N, groups), dtype=scale_dtype, device=W.device),
-             torch.empty((N, groups), dtype=torch.uint8, device=W.device) if zeros else None, K, group)
     _int32(N=N, K=K, group=group, ldb=ldb)
-    _launch(W.device, lambda stream: _lib().sgemm_w4_quantize(_types()[W.dtype], stype, N, K, group, W.data_ptr() or None,
-                                                              ldb, *out._args(), stream))
+    groups, device = -(-K // group), W.device
+    out = W4(torch.empty((N, -(-K // 2)), dtype=torch.uint8, device=device),
+             torch.empty((N, groups), dtype=scale_dtype, device=device),
+             torch.empty((N, groups), dtype=torch.uint8, device=device) if zeros else None, K, group)
+    _launch(device.index, _lib().sgemm_w4_quantize, _types()[W.dtype], out._stype, N, K, group, W.data_ptr() or None, ldb,
+            *out._args)
     return out
 
 
@@ -263,18 +279,21 @@ def dequantize_w4(W, dtype=None, out=None):
 
     if not isinstance(W, W4):
         raise TypeError("W must be a W4")
-    N, K = W.shape
     if out is None:
-        out = torch.empty((N, K), dtype=torch.float32 if dtype is None else dtype, device=W.device)
+        dtype = torch.float32 if dtype is None else dtype
+        _type_code(dtype, "dtype")
+        out = torch.empty(W._shape, dtype=dtype, device=W._device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out must be {dtype}, is {out.dtype}")
-    _need(out, "out", 2, tuple(_types()), W.device)
+    _need(out, "out", 2, _types(), W._device)
+    N, K = W._shape
     if tuple(out.shape) != (N, K):
         raise ValueError(f"out must be {N} x {K}, is {tuple(out.shape)}")
     ldb = _row_major(out, "out")
-    _int32(N=N, K=K, ldb=ldb)
-    _launch(W.device, lambda stream: _lib().sgemm_w4_dequantize(_types()[out.dtype], _types()[W.scales.dtype], N, K, W.group,
-                                                                *W._args(), out.data_ptr() or None, ldb, stream))
+    if ldb > _INT32_MAX:
+        _int32(ldb=ldb)
+    _launch(W._device.index, _lib().sgemm_w4_dequantize, _types()[out.dtype], W._stype, N, K, W._group, *W._args,
+            out.data_ptr() or None, ldb)
     return out
 
 
@@ -289,24 +308,24 @@ def gemm_w4(A, W, C=None, alpha=1.0, beta=0.0):
 
     if not isinstance(W, W4):
         raise TypeError("W must be a W4")
-    _need(A, "A", 2, tuple(_types()), W.device)
+    _need(A, "A", 2, _types(), W._device)
     M, K = A.shape
-    N = W.codes.shape[0]
-    if K != W.K:
-        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {W.shape}")
+    N = W._shape[0]
+    if K != W._shape[1]:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {W._shape}")
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
-        C = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        C = torch.empty((M, N), dtype=torch.float32, device=W._device)
     else:
-        _need(C, "C", 2, (torch.float32,), A.device)
+        _need(C, "C", 2, (torch.float32,), W._device)
         if tuple(C.shape) != (M, N):
             raise ValueError(f"C must be {M} x {N}, is {tuple(C.shape)}")
     lda, ldc = _row_major(A, "A"), _row_major(C, "C")
-    _int32(M=M, N=N, K=K, group=W.group, lda=lda, ldc=ldc)
-    _launch(A.device, lambda stream: _lib().sgemm_w4(_types()[A.dtype], _types()[W.scales.dtype], M, N, K, W.group,
-                                                     float(alpha), A.data_ptr() or None, lda, *W._args(), float(beta),
-                                                     C.data_ptr() or None, ldc, stream))
+    if M > _INT32_MAX or lda > _INT32_MAX or ldc > _INT32_MAX:
+        _int32(M=M, lda=lda, ldc=ldc)
+    _launch(W._device.index, _lib().sgemm_w4, _types()[A.dtype], W._stype, M, N, K, W._group, alpha, A.data_ptr() or None,
+            lda, *W._args, beta, C.data_ptr() or None, ldc)
     return C
 
 
@@ -314,10 +333,11 @@ class KV8:
     """A paged cache of keys and values in 8-bit floats: ``K`` and ``V``
     (float8_e4m3fn, pages x heads x block x dim, contiguous) and ``Ks`` and
     ``Vs`` (float32, pages x heads), one scale for each page and head. The
-    tensors are used in place. ``block`` is a power of two from 16 to 1024 and
-    ``dim`` a multiple of 16 up to 256."""
+    tensors are used in place and belong to the KV8 for good (what they hold
+    may change). ``block`` is a power of two from 16 to 1024 and ``dim`` a
+    multiple of 16 up to 256."""
 
-    __slots__ = ("K", "V", "Ks", "Vs", "_struct")
+    __slots__ = ("_tensors", "_struct", "_device", "_heads", "_dim")
 
     def __init__(self, K, V, Ks, Vs):
         import torch
@@ -331,13 +351,21 @@ class KV8:
         if not all(t.is_contiguous() for t in (K, V, Ks, Vs)):
             raise ValueError("K, V, Ks and Vs must be contiguous")
         pages, heads, block, dim = K.shape
+        if pages < 1 or heads < 1:
+            raise ValueError("a cache needs a page and a head")
         if block < 16 or block > 1024 or block & (block - 1):
             raise ValueError(f"block must be a power of two from 16 to 1024, is {block}")
         if dim < 16 or dim > 256 or dim % 16:
             raise ValueError(f"dim must be a multiple of 16 from 16 to 256, is {dim}")
         _int32(pages=pages, heads=heads)
-        self.K, self.V, self.Ks, self.Vs = K, V, Ks, Vs
+        self._tensors, self._device, self._heads, self._dim = (K, V, Ks, Vs), K.device, heads, dim
         self._struct = KV8Cache(K.data_ptr(), V.data_ptr(), Ks.data_ptr(), Vs.data_ptr(), pages, heads, block, dim)
+
+    K = property(lambda self: self._tensors[0])
+    V = property(lambda self: self._tensors[1])
+    Ks = property(lambda self: self._tensors[2])
+    Vs = property(lambda self: self._tensors[3])
+    device = property(lambda self: self._device)
 
     @staticmethod
     def empty(pages, heads, block, dim, device="cuda"):
@@ -348,37 +376,39 @@ class KV8:
                  for _ in range(2)]
         return KV8(*codes, *[torch.zeros((pages, heads), dtype=torch.float32, device=device) for _ in range(2)])
 
-    @property
-    def device(self):
-        return self.K.device
-
 
 def _batch(cache, table, lens, starts, rows, max_new):
     import torch
 
-    if not isinstance(cache, KV8):
-        raise TypeError("cache must be a KV8")
-    i32, device = (torch.int32,), cache.K.device
+    i32, device = (torch.int32,), cache._device
     _need(table, "table", 2, i32, device)
     _need(lens, "lens", 1, i32, device)
     _need(starts, "starts", 1, i32, device)
-    seqs = lens.shape[0]
-    if table.shape[0] != seqs or starts.shape[0] != seqs + 1:
-        raise ValueError(f"{seqs} lens need a table of {seqs} rows and {seqs + 1} starts, got {table.shape[0]} and {starts.shape[0]}")
+    seqs, columns = table.shape
+    if lens.shape[0] != seqs or starts.shape[0] != seqs + 1:
+        raise ValueError(f"a table of {seqs} rows needs {seqs} lens and {seqs + 1} starts, got {lens.shape[0]} and {starts.shape[0]}")
     if not (table.is_contiguous() and lens.is_contiguous() and starts.is_contiguous()):
         raise ValueError("table, lens and starts must be contiguous")
     max_new = rows if max_new is None else int(max_new)
-    _int32(rows=rows, max_new=max_new, seqs=seqs, columns=table.shape[1])
-    return KV8Batch(table.data_ptr() or None, lens.data_ptr() or None, starts.data_ptr() or None, seqs, table.shape[1], rows, max_new)
+    if not 0 <= max_new <= _INT32_MAX or rows > _INT32_MAX or seqs > _INT32_MAX or columns > _INT32_MAX:
+        _int32(rows=rows, max_new=max_new, seqs=seqs, columns=columns)
+    return KV8Batch(table.data_ptr() or None, lens.data_ptr() or None, starts.data_ptr() or None, seqs, columns, rows, max_new)
 
 
 def _operand(t, name, cache, heads, dtypes):
-    _need(t, name, 3, dtypes, cache.K.device)
-    if t.shape[2] != cache.K.shape[3] or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be rows x {heads or 'heads'} x {cache.K.shape[3]}, is {tuple(t.shape)}")
-    ld, hs = _heads(t, name)
-    _int32(**{f"{name}'s row stride": ld, f"{name}'s head stride": hs})
-    return ld, hs
+    _need(t, name, 3, dtypes, cache._device)
+    if t.shape[2] != cache._dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be rows x {heads or 'heads'} x {cache._dim}, is {tuple(t.shape)}")
+    return _heads(t, name)
+
+
+def _pair(cache, K, V):
+    """Strides of K and V, rows x heads x dim of one type."""
+    ldk, hsk = _operand(K, "K", cache, cache._heads, _types())
+    ldv, hsv = _operand(V, "V", cache, cache._heads, (K.dtype,))
+    if V.shape[0] != K.shape[0]:
+        raise ValueError(f"K and V must have the same rows, have {K.shape[0]} and {V.shape[0]}")
+    return _types()[K.dtype], K.data_ptr() or None, ldk, hsk, V.data_ptr() or None, ldv, hsv
 
 
 def kv8_write(cache, K, V, table, lens, starts, max_new=None):
@@ -394,14 +424,9 @@ def kv8_write(cache, K, V, table, lens, starts, max_new=None):
     """
     if not isinstance(cache, KV8):
         raise TypeError("cache must be a KV8")
-    heads = cache.K.shape[1]
-    ldk, hsk = _operand(K, "K", cache, heads, tuple(_types()))
-    ldv, hsv = _operand(V, "V", cache, heads, (K.dtype,))
-    if V.shape[0] != K.shape[0]:
-        raise ValueError(f"K and V must have the same rows, have {K.shape[0]} and {V.shape[0]}")
+    operand = _pair(cache, K, V)
     batch = _batch(cache, table, lens, starts, K.shape[0], max_new)
-    _launch(cache.K.device, lambda stream: _lib().sgemm_kv8_write(cache._struct, batch, _types()[K.dtype], K.data_ptr() or None,
-                                                                  ldk, hsk, V.data_ptr() or None, ldv, hsv, stream))
+    _launch(cache._device.index, _lib().sgemm_kv8_write, cache._struct, batch, *operand)
 
 
 def kv8_read(cache, table, lens, starts, rows=None, dtype=None, K=None, V=None, max_new=None):
@@ -413,22 +438,18 @@ def kv8_read(cache, table, lens, starts, rows=None, dtype=None, K=None, V=None, 
 
     if not isinstance(cache, KV8):
         raise TypeError("cache must be a KV8")
-    heads, dim = cache.K.shape[1], cache.K.shape[3]
     if (K is None) != (V is None) or (K is None and rows is None):
         raise ValueError("give rows, or both K and V")
     if K is None:
         dtype = torch.float32 if dtype is None else dtype
         _type_code(dtype, "dtype")
-        K, V = (torch.empty((int(rows), heads, dim), dtype=dtype, device=cache.K.device) for _ in range(2))
-    elif (rows is not None and K.shape[0] != rows) or (dtype is not None and K.dtype != dtype):
+        shape = (int(rows), cache._heads, cache._dim)
+        K, V = torch.empty(shape, dtype=dtype, device=cache._device), torch.empty(shape, dtype=dtype, device=cache._device)
+    operand = _pair(cache, K, V)
+    if (rows is not None and K.shape[0] != rows) or (dtype is not None and K.dtype != dtype):
         raise ValueError("K is not of the rows and dtype asked for")
-    ldk, hsk = _operand(K, "K", cache, heads, tuple(_types()))
-    ldv, hsv = _operand(V, "V", cache, heads, (K.dtype,))
-    if V.shape[0] != K.shape[0]:
-        raise ValueError(f"K and V must have the same rows, have {K.shape[0]} and {V.shape[0]}")
     batch = _batch(cache, table, lens, starts, K.shape[0], max_new)
-    _launch(cache.K.device, lambda stream: _lib().sgemm_kv8_read(cache._struct, batch, _types()[K.dtype], K.data_ptr() or None,
-                                                                 ldk, hsk, V.data_ptr() or None, ldv, hsv, stream))
+    _launch(cache._device.index, _lib().sgemm_kv8_read, cache._struct, batch, *operand)
     return K, V
 
 
@@ -450,28 +471,30 @@ def kv8_attend(Q, cache, table, lens, starts, scale=None, causal=True, window=0,
 
     if not isinstance(cache, KV8):
         raise TypeError("cache must be a KV8")
-    ldq, hsq = _operand(Q, "Q", cache, None, tuple(_types()))
+    ldq, hsq = _operand(Q, "Q", cache, None, _types())
     rows, heads_q, dim = Q.shape
     if out is None:
-        out = torch.empty((rows, heads_q, dim), dtype=torch.float32, device=Q.device)
+        out = torch.empty((rows, heads_q, dim), dtype=torch.float32, device=cache._device)
     ldo, hso = _operand(out, "out", cache, heads_q, (torch.float32,))
     if out.shape[0] != rows:
         raise ValueError(f"out must have Q's shape {tuple(Q.shape)}, is {tuple(out.shape)}")
-    window = int(window)
-    _int32(window=window, heads_q=heads_q)
+    if not 0 <= window <= _INT32_MAX or heads_q > _INT32_MAX:
+        _int32(window=window, heads_q=heads_q)
     batch = _batch(cache, table, lens, starts, rows, max_new)
     lib = _lib()
+    ws, ws_bytes = None, 0
     if workspace is None:
-        need = lib.sgemm_kv8_attend_workspace_size(cache._struct, batch, heads_q, window, _cus(Q.device))
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != Q.device or not workspace.is_contiguous():
+        ws_bytes = lib.sgemm_kv8_attend_workspace_size(cache._struct, batch, heads_q, window, _cus(cache._device))
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=cache._device)
+            ws = workspace.data_ptr()
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != cache._device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on Q's device")
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr() or None, workspace.numel() * workspace.element_size())
-    _launch(Q.device, lambda stream: lib.sgemm_kv8_attend(
-        cache._struct, batch, _types()[Q.dtype], heads_q, Q.data_ptr() or None, ldq, hsq,
-        float(dim ** -0.5 if scale is None else scale), int(bool(causal)), window, out.data_ptr() or None, ldo, hso,
-        ws, ws_bytes, stream))
+    else:
+        ws, ws_bytes = workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
+    _launch(cache._device.index, lib.sgemm_kv8_attend, cache._struct, batch, _types()[Q.dtype], heads_q, Q.data_ptr() or None,
+            ldq, hsq, dim**-0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr() or None, ldo, hso, ws,
+            ws_bytes)
     return out
 
 
