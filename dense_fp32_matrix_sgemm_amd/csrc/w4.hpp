@@ -187,46 +187,133 @@ template <> struct Bytes<2> {
     __device__ std::uint32_t at(int i) const { return std::uint32_t(w) >> (8 * i); }
 };
 
-// N 16-bit scales, likewise.
-template <int N> struct Halves {
+// N scales of type ST, likewise.
+template <class ST, int N> struct ScaleSet {
     Words<N / 2> w;
-    __device__ void load(const void *p) { w = load_any<Words<N / 2>>(p); }
-    __device__ std::uint16_t at(int i) const { return std::uint16_t(w.v[i / 2] >> (16 * (i % 2))); }
+    __device__ void load(const void *S, std::int64_t i) { w = load_any<Words<N / 2>>(static_cast<const std::uint16_t *>(S) + i); }
+    __device__ float at(int i) const { return to_f32<ST>(std::uint16_t(w.v[i / 2] >> (16 * (i % 2)))); }
 };
-template <> struct Halves<1> {
-    std::uint16_t w;
-    __device__ void load(const void *p) { w = load_any<std::uint16_t>(p); }
-    __device__ std::uint16_t at(int) const { return w; }
+template <class ST> struct ScaleSet<ST, 1> {
+    typename ST::elem w;
+    __device__ void load(const void *S, std::int64_t i) { w = load_any<typename ST::elem>(static_cast<const typename ST::elem *>(S) + i); }
+    __device__ float at(int) const { return to_f32<ST>(w); }
 };
-
-// How a kernel meets the scales. The first three: group == 32 GS, so that a
-// wave's scales (of that type) and zero points are adjacent in memory and
-// come in one load for U chunks; Any: one load each.
-enum class Scales { RunF32, RunBF16, RunF16, Any };
-
-// N scales as loaded.
-template <Scales SC, int N> struct ScaleSet {
-    typedef typename std::conditional<SC == Scales::RunBF16, BF16, F16>::type T16;
-    Halves<N> h;
-    __device__ void load(const void *S, std::int64_t i) { h.load(static_cast<const std::uint16_t *>(S) + i); }
-    __device__ float at(int i) const { return to_f32<T16>(h.at(i)); }
-};
-template <int N> struct ScaleSet<Scales::RunF32, N> {
+template <int N> struct ScaleSet<F32, N> {
     Words<N> w;
     __device__ void load(const void *S, std::int64_t i) { w = load_any<Words<N>>(static_cast<const float *>(S) + i); }
     __device__ float at(int i) const { return bits_f32(w.v[i]); }
 };
-template <int N> struct ScaleSet<Scales::Any, N> {
-    float f[N];
-    __device__ float at(int i) const { return f[i]; }
+template <> struct ScaleSet<F32, 1> {
+    float w;
+    __device__ void load(const void *S, std::int64_t i) { w = static_cast<const float *>(S)[i]; }
+    __device__ float at(int) const { return w; }
+};
+
+// The scales and zero points of N runs of 32 GS k from k0 on, for one column.
+// Run: group == 32 GS, so that they are adjacent and come in one load each;
+// otherwise group is a multiple of 32 GS and each run has its own loads.
+template <class ST, int GS, int N, bool ZP, bool Run> struct Groups {
+    static constexpr int kSets = Run ? 1 : N, kPer = Run ? N : 1;
+    ScaleSet<ST, kPer> s[kSets];
+    Bytes<kPer> z[kSets];
+    __device__ void load(const void *S, std::int64_t srow, const std::uint8_t *zrow, unsigned k0, int group)
+    {
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            const unsigned g = Run ? k0 / (32u * GS) : (k0 + i * (32u * GS)) / unsigned(group);
+            s[i].load(S, srow + g);
+            if (ZP) z[i].load(zrow + g);
+        }
+    }
+    __device__ float scale(int run) const { return Run ? s[0].at(run) : s[Run ? 0 : run].at(0); }
+    __device__ std::uint32_t zero(int run) const { return ZP ? (Run ? z[0].at(run) : z[Run ? 0 : run].at(0)) & 15u : 8u; }
+};
+
+// N scales of a runtime type, for the tile kernels: loaded as two runs of N
+// 16-bit words without a branch (for a 16-bit type the second repeats the
+// first), told apart where they are used.
+struct AnyType {};
+template <int N> struct ScaleSet<AnyType, N> {
+    Words<N / 2> a, b;
+    __device__ void load(const void *S, std::int64_t i, bool f32)
+    {
+        const char *p = static_cast<const char *>(S) + i * (f32 ? 4 : 2);
+        a = load_any<Words<N / 2>>(p);
+        b = load_any<Words<N / 2>>(p + (f32 ? 2 * N : 0));
+    }
+    __device__ float at(int i, int stype) const
+    {
+        const std::uint16_t x = std::uint16_t(a.v[i / 2] >> (16 * (i % 2)));
+        const float f = bits_f32(i < N / 2 ? a.v[i < N / 2 ? i : 0] : b.v[i < N / 2 ? 0 : i - N / 2]);
+        return stype == SGEMM_F32 ? f : stype == SGEMM_LP_BF16 ? to_f32<BF16>(x) : to_f32<F16>(x);
+    }
+};
+template <> struct ScaleSet<AnyType, 1> {
+    std::uint16_t a, b;
+    __device__ void load(const void *S, std::int64_t i, bool f32)
+    {
+        const char *p = static_cast<const char *>(S) + i * (f32 ? 4 : 2);
+        a = load_any<std::uint16_t>(p);
+        b = load_any<std::uint16_t>(p + (f32 ? 2 : 0));
+    }
+    __device__ float at(int, int stype) const
+    {
+        const float f = bits_f32(a | std::uint32_t(b) << 16);
+        return stype == SGEMM_F32 ? f : stype == SGEMM_LP_BF16 ? to_f32<BF16>(a) : to_f32<F16>(a);
+    }
+};
+
+// As Groups; past K (the last slab) the last group's stand in, A being 0 there.
+template <int GS, int N, bool ZP, bool Run> struct AnyGroups {
+    static constexpr int kSets = Run ? 1 : N, kPer = Run ? N : 1;
+    ScaleSet<AnyType, kPer> s[kSets];
+    Bytes<kPer> z[kSets];
+    __device__ void load(const W4Problem &p, std::int64_t srow, const std::uint8_t *zrow, int k0)
+    {
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            const unsigned g = Run ? unsigned(k0) / (32u * GS) : unsigned(k0 + i * (32 * GS)) / unsigned(p.group);
+            s[i].load(p.S, srow + g, p.stype == SGEMM_F32);
+            if (ZP) z[i].load(zrow + g);
+        }
+    }
+    __device__ void load_last(const W4Problem &p, std::int64_t srow, const std::uint8_t *zrow, int k0)
+    {
+        const bool f32 = p.stype == SGEMM_F32;
+        std::uint16_t a[N], b[N];
+        std::uint8_t zz[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = k0 + 32 * GS * i < p.K ? k0 + 32 * GS * i : p.K - 1;
+            ScaleSet<AnyType, 1> one;
+            one.load(p.S, srow + k / p.group, f32);
+            a[i] = one.a, b[i] = one.b;
+            zz[i] = ZP ? zrow[k / p.group] : 0;
+        }
+        if constexpr (Run && N > 1) {
+            // As the adjacent load would have left them.
+            std::uint16_t x[2 * N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                x[f32 ? 2 * i : i] = a[i];
+                if (f32) x[2 * i + 1] = b[i];
+            }
+            __builtin_memcpy(&s[0].a, x, 2 * N);
+            __builtin_memcpy(&s[0].b, x + N, 2 * N);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) s[i].a = a[i], s[i].b = b[i];
+        }
+        __builtin_memcpy(&z, zz, sizeof(zz));
+    }
+    __device__ float scale(int run, int stype) const { return Run ? s[0].at(run, stype) : s[Run ? 0 : run].at(0, stype); }
+    __device__ std::uint32_t zero(int run) const { return ZP ? (Run ? z[0].at(run) : z[Run ? 0 : run].at(0)) & 15u : 8u; }
 };
 
 // What a wave loads for U chunks of k.
-template <int NT, int GS, int U, Scales SC> struct W4Stage {
-    static constexpr int kRuns = 4 * U / GS;  // runs of 32 GS k that share a scale
+template <class ST, int NT, int GS, int U, bool ZP, bool Run> struct W4Stage {
     u32x4 w[U][NT];
-    ScaleSet<SC, kRuns> s[NT];
-    Bytes<kRuns> z[NT];
+    Groups<ST, GS, 4 * U / GS, ZP, Run> g[NT];
 };
 
 // How a product is laid out over work-groups (launch_rows).
@@ -244,15 +331,15 @@ struct W4Layout {
 // codes per chunk. The wk waves of a column tile add their sums through LDS
 // in their order, so the result does not depend on timing. GS: steps of 32 k
 // that share a scale.
-template <class T, int MT, int NT, int GS, bool ZP, int U, bool Short, Scales SC, int MaxWaves>
+template <class T, class ST, int MT, int NT, int GS, bool ZP, int U, bool Short, bool Run, int MaxWaves>
 __global__ __launch_bounds__(64 * MaxWaves) void w4_rows_kernel(W4Problem p, W4Layout l)
 {
     extern __shared__ __align__(16) char lds[];  // A: [plane][row][k] as 16-bit operands
     typedef typename T::elem elem;
-    typedef W4Stage<NT, GS, U, SC> Stage;
+    typedef W4Stage<ST, NT, GS, U, ZP, Run> Stage;
     typedef AOperand<T> Operand;
     typedef Codes<T, ZP> Code;
-    constexpr int kStep = kW4Chunk * U, kPlanes = Operand::kPlanes, kRuns = Stage::kRuns;
+    constexpr int kStep = kW4Chunk * U, kPlanes = Operand::kPlanes;
     float *const part = reinterpret_cast<float *>(lds);  // then the sums: [wave][16 MT][16 NT]
     const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -277,22 +364,7 @@ __global__ __launch_bounds__(64 * MaxWaves) void w4_rows_kernel(W4Problem p, W4L
 #pragma unroll
             for (int t = 0; t < NT; ++t) st.w[u][t] = load_any<u32x4>(wrow[t] + (k0 / 2 + 64 * u + 16 * kq));
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if constexpr (SC != Scales::Any) {
-                const unsigned g0 = k0 / (32u * GS);
-                st.s[t].load(p.S, srow[t] + g0);
-                if (ZP) st.z[t].load(zrow[t] + g0);
-            } else {
-                std::uint8_t z[(kRuns + 3) / 4 * 4] = {};
-#pragma unroll
-                for (int g = 0; g < kRuns; ++g) {
-                    const unsigned group = (k0 + g * (32 * GS)) / unsigned(p.group);
-                    st.s[t].f[g] = load_scale(p.S, p.stype, srow[t] + group);
-                    if (ZP) z[g] = zrow[t][group];
-                }
-                if (ZP) __builtin_memcpy(&st.z[t], z, sizeof(st.z[t]));
-            }
-        }
+        for (int t = 0; t < NT; ++t) st.g[t].load(p.S, srow[t], zrow[t], k0, p.group);
     };
 
     for (std::int64_t m0 = std::int64_t(blockIdx.y) * (16 * MT); m0 < p.M; m0 += std::int64_t(gridDim.y) * (16 * MT)) {
@@ -324,7 +396,7 @@ __global__ __launch_bounds__(64 * MaxWaves) void w4_rows_kernel(W4Problem p, W4L
                     for (int s = 0; s < GS; ++s) {
                         Frag wf[NT];
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) wf[t] = Code(ZP ? st.z[t].at(run) & 15u : 8u)(w[t][g * GS + s]);
+                        for (int t = 0; t < NT; ++t) wf[t] = Code(st.g[t].zero(run))(w[t][g * GS + s]);
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             const Operand a = operand(k0 + 128 * u + 32 * (g * GS + s), i);
@@ -334,7 +406,7 @@ __global__ __launch_bounds__(64 * MaxWaves) void w4_rows_kernel(W4Problem p, W4L
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const float s = st.s[t].at(run) * Code::kUnit;
+                        const float s = st.g[t].scale(run) * Code::kUnit;
 #pragma unroll
                         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -387,7 +459,7 @@ __global__ __launch_bounds__(64 * MaxWaves) void w4_rows_kernel(W4Problem p, W4L
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w |= at + i < bytes ? std::uint32_t(wrow[t][at + i]) << (8 * i) : 0u;
                     wf[t] = Code(ZP ? zrow[t][group] & 15u : 8u)(w);
-                    s[t] = load_scale(p.S, p.stype, srow[t] + group) * Code::kUnit;
+                    s[t] = to_f32<ST>(static_cast<const typename ST::elem *>(p.S)[srow[t] + group]) * Code::kUnit;
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -425,7 +497,7 @@ __global__ __launch_bounds__(64 * MaxWaves) void w4_rows_kernel(W4Problem p, W4L
     }
 }
 
-template <class T, int MT, int NT, int GS, bool ZP, Scales SC> hipError_t launch_rows(const W4Problem &p, hipStream_t stream)
+template <class T, class ST, int MT, int NT, int GS, bool ZP, bool Run> hipError_t launch_rows(const W4Problem &p, hipStream_t stream)
 {
     constexpr int U = MT * NT <= 2 && sizeof(typename T::elem) == 2 ? 2 : 1, kStep = kW4Chunk * U, kWaves = MT * NT <= 2 ? 16 : 8;
     constexpr std::int64_t kLds = 160 * 1024;
@@ -453,8 +525,8 @@ template <class T, int MT, int NT, int GS, bool ZP, Scales SC> hipError_t launch
     const std::size_t sums = std::size_t(waves) * MT * NT * 1024;
     if (shared < sums) shared = sums;
     tiles_n = (tiles_n + l.wn - 1) / l.wn;
-    const void *kernel = steps > 0 ? reinterpret_cast<const void *>(&w4_rows_kernel<T, MT, NT, GS, ZP, U, false, SC, kWaves>)
-                                   : reinterpret_cast<const void *>(&w4_rows_kernel<T, MT, NT, 1, ZP, U, true, Scales::Any, kWaves>);
+    const void *kernel = steps > 0 ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, MT, NT, GS, ZP, U, false, Run, kWaves>)
+                                   : reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, MT, NT, 1, ZP, U, true, false, kWaves>);
     if (shared > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
         if (e != hipSuccess) return e;
@@ -479,32 +551,310 @@ template <class T, int MT, int NT, int GS, bool ZP, Scales SC> hipError_t launch
     return hipSuccess;
 }
 
-template <class T, int GS, bool ZP, Scales SC> hipError_t launch_shape(const W4Problem &p, hipStream_t stream)
+// Products with more rows, on v_mfma_f32_32x32x16: each wave a tile of 32 MT
+// rows by 32 NT columns. A's rows of 128 k at a time (a slab) lie in LDS, the
+// next slab's in registers while this one is multiplied; each wave's codes go
+// from memory straight to its registers and are converted once for all rows.
+// WN > 1: WN waves divide the columns and share the slab (two buffers, one
+// barrier a slab). WN == 1: WK waves divide K, each with a buffer of its own
+// and no barrier, and add their sums through LDS in their order: for products
+// with too few tiles to fill the device.
+//
+// Within a slab the loops run over groups, then row tiles, then k: a group's
+// sum of one row tile is complete, scaled and added to the result before the
+// next begins, so that it takes 16 NT registers and not another result tile.
+// Lane 32 h + c supplies column (row) c; which k it supplies in a step is free
+// as long as both operands agree and stay inside a group: k = 16 GS h + 8 j of
+// the group in step j, so that a lane's codes of a group are adjacent.
+//
+// The matrix cores bound it: what shares their time is the conversion (7
+// cycles a code and column, so tall tiles) and the reads of A from LDS (4
+// cycles a row and 64 k for four waves against MT NT matrix instructions, so
+// wide ones).
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+template <class T> __device__ inline f32x16 mfma32(const Frag &a, const Frag &b, f32x16 c)
 {
-    if (p.M <= 16) return launch_rows<T, 1, 1, GS, ZP, SC>(p, stream);
-    return p.M <= 32 ? launch_rows<T, 2, 1, GS, ZP, SC>(p, stream) : launch_rows<T, 4, 1, GS, ZP, SC>(p, stream);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c, 0, 0, 0);
+}
+template <> __device__ inline f32x16 mfma32<F16>(const Frag &a, const Frag &b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), c, 0, 0, 0);
 }
 
-template <class T, int GS, bool ZP> hipError_t launch_run(const W4Problem &p, hipStream_t stream)
+constexpr int kTilePitch = 2 * kW4Chunk + 16;  // bytes of a row of A's slab in LDS: 8 rows meet in no bank
+
+template <class T, int MT, int NT, int WN, int WK> constexpr int tile_lds()
 {
-    return p.stype == SGEMM_F32       ? launch_shape<T, GS, ZP, Scales::RunF32>(p, stream)
-           : p.stype == SGEMM_LP_BF16 ? launch_shape<T, GS, ZP, Scales::RunBF16>(p, stream)
-                                      : launch_shape<T, GS, ZP, Scales::RunF16>(p, stream);
+    const int slabs = (WN > 1 ? 2 : WK) * AOperand<T>::kPlanes * 32 * MT * kTilePitch, sums = WK > 1 ? WK * MT * NT * 4096 : 0;
+    return slabs > sums ? slabs : sums;
 }
 
-template <class T, bool ZP> hipError_t launch_group(const W4Problem &p, hipStream_t stream)
+template <class T, int MT, int NT, int GS, bool ZP, bool Run, int WN, int WK>
+__global__ __launch_bounds__(64 * WN * WK, WN > 1 && AOperand<T>::kPlanes == 1 ? 2 : 1) void w4_tile_kernel(W4Problem p, int tiles_m)
+{
+    static_assert(WN == 1 || WK == 1, "waves divide the columns or K");
+    extern __shared__ __align__(16) char lds[];  // [buffer][plane][row][k]
+    typedef typename T::elem elem;
+    typedef AOperand<T> Operand;
+    typedef Codes<T, ZP> Code;
+    constexpr int kPlanes = Operand::kPlanes, BM = 32 * MT, BN = 32 * NT * WN, kPieces = BM * 16 / (64 * WN);
+    constexpr int kBuffer = kPlanes * BM * kTilePitch;
+    const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = WN > 1 ? wave : 0, wk = WN > 1 ? 0 : wave;
+    const std::int64_t m0 = std::int64_t(blockIdx.x % unsigned(tiles_m)) * BM;
+    const std::int64_t c0 = std::int64_t(blockIdx.x / unsigned(tiles_m)) * BN, n0 = c0 + wn * (32 * NT);
+    const int bytes = p.K / 2 + p.K % 2;
+
+    const std::uint8_t *wrow[NT], *zrow[NT];
+    std::int64_t srow[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        // Columns (and rows) past the last read it again; they are not stored.
+        const std::int64_t n = n0 + 32 * t + c < p.N ? n0 + 32 * t + c : p.N - 1;
+        wrow[t] = p.W + n * p.ldw;
+        srow[t] = n * p.lds;
+        zrow[t] = ZP ? p.Z + n * p.ldz : nullptr;
+    }
+    // A's slab in pieces of 8 k: a thread takes piece t % 16 of rows t / 16, t / 16 + 4 WN, ...
+    const int piece = threadIdx.x & 15, prow = (WN > 1 ? threadIdx.x : lane) >> 4;
+    const elem *arow[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const std::int64_t r = m0 + prow + 4 * WN * i < p.M ? m0 + prow + 4 * WN * i : p.M - 1;
+        arow[i] = static_cast<const elem *>(p.A) + r * p.lda;
+    }
+    struct Eight {
+        elem x[8];
+    };
+    Eight araw[kPieces];
+    std::uint32_t w[NT][16];  // a lane's codes: word 2 GS g + j holds k = 32 GS g + 16 GS h + 8 j
+    AnyGroups<GS, 4 / GS, ZP, Run> groups[NT];
+    f32x16 out[MT][NT] = {};
+
+    auto load = [&](int k0, auto tail) {
+        constexpr bool Tail = decltype(tail)::value;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            if constexpr (Tail) {
+                load_a<T>(arow[i], k0 + 8 * piece, p.K, araw[i].x);
+            } else {
+                araw[i] = load_any<Eight>(arow[i] + k0 + 8 * piece);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int g = 0; g < 4 / GS; ++g) {
+                const int at = k0 / 2 + 16 * GS * g + 8 * GS * h;
+                if constexpr (Tail) {
+#pragma unroll
+                    for (int j = 0; j < 2 * GS; ++j) {
+                        std::uint32_t x = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x |= at + 4 * j + i < bytes ? std::uint32_t(wrow[t][at + 4 * j + i]) << (8 * i) : 0u;
+                        w[t][2 * GS * g + j] = x;
+                    }
+                } else {
+                    const Words<2 * GS> x = load_any<Words<2 * GS>>(wrow[t] + at);
+#pragma unroll
+                    for (int j = 0; j < 2 * GS; ++j) w[t][2 * GS * g + j] = x.v[j];
+                }
+            }
+            if constexpr (Tail) {
+                groups[t].load_last(p, srow[t], zrow[t], k0);
+            } else {
+                groups[t].load(p, srow[t], zrow[t], k0);
+            }
+        }
+    };
+    auto hold = [&](char *buffer) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            Operand a;
+            a.set(araw[i].x);
+#pragma unroll
+            for (int f = 0; f < kPlanes; ++f)
+                *reinterpret_cast<u32x4 *>(buffer + (f * BM + prow + 4 * WN * i) * kTilePitch + 16 * piece) = a.f[f].v;
+        }
+    };
+
+    const int slabs = (p.K + kW4Chunk - 1) / kW4Chunk, whole = p.K / kW4Chunk;
+    const int first = int(std::int64_t(slabs) * wk / WK), end = int(std::int64_t(slabs) * (wk + 1) / WK);
+    char *const own = lds + wk * kBuffer;
+    if (first < end) {
+        if (first < whole) {
+            load(first * kW4Chunk, std::false_type{});
+        } else {
+            load(first * kW4Chunk, std::true_type{});
+        }
+        hold(own);
+    }
+    for (int s = first; s < end; ++s) {
+        if (WN > 1) __syncthreads();  // this slab is in LDS; the one before has been read
+        const char *const buffer = own + (WN > 1 ? (s - first) % 2 * kBuffer : 0) + c * kTilePitch + 32 * GS * h;
+        // The slab's operands and scales, then (their registers free) the next slab's loads.
+        Frag b[NT][8];
+        float scale[NT][4 / GS];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int g = 0; g < 4 / GS; ++g) {
+                scale[t][g] = groups[t].scale(g, p.stype) * Code::kUnit;
+#pragma unroll
+                for (int j = 0; j < 2 * GS; ++j) b[t][2 * GS * g + j] = Code(groups[t].zero(g))(w[t][2 * GS * g + j]);
+            }
+        if (s + 1 < end) {
+            if (s + 1 < whole) {
+                load((s + 1) * kW4Chunk, std::false_type{});
+            } else {
+                load((s + 1) * kW4Chunk, std::true_type{});
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4 / GS; ++g)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                f32x16 acc[NT];
+#pragma unroll
+                for (int j = 0; j < 2 * GS; ++j) {
+#pragma unroll
+                    for (int f = kPlanes - 1; f >= 0; --f) {
+                        Frag a;
+                        a.v = *reinterpret_cast<const u32x4 *>(buffer + (f * BM + 32 * i) * kTilePitch + 64 * GS * g + 16 * j);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            acc[t] = mfma32<T>(a, b[t][2 * GS * g + j], j == 0 && f == kPlanes - 1 ? f32x16{} : acc[t]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) out[i][t][r] += scale[t][g] * acc[t][r];
+                if (GS < 4) {
+                    // Without a fence the compiler keeps many short groups' sums at once and spills.
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(out[i][t]));
+                }
+            }
+        if (s + 1 < end) hold(own + (WN > 1 ? (s + 1 - first) % 2 * kBuffer : 0));
+    }
+    // D: lane 32 h + c, register r: row 8 (r / 4) + 4 h + r % 4, column c.
+    auto store = [&](std::int64_t m, std::int64_t n, float x) {
+        float *dst = p.C + m * p.ldc + n;
+        *dst = p.beta == 0.0f ? p.alpha * x : __builtin_fmaf(p.alpha, x, p.beta * *dst);
+    };
+    if constexpr (WK > 1) {
+        float *const part = reinterpret_cast<float *>(lds);  // [wave][row][column]
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    part[(wk * BM + 32 * i + 8 * (r / 4) + 4 * h + r % 4) * BN + 32 * t + c] = out[i][t][r];
+        __syncthreads();
+        for (int e = threadIdx.x; e < BM * BN; e += 64 * WK) {
+            const std::int64_t m = m0 + e / BN, n = c0 + e % BN;
+            if (m >= p.M || n >= p.N) continue;
+            float sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < WK; ++x) sum += part[x * BM * BN + e];
+            store(m, n, sum);
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const std::int64_t n = n0 + 32 * t + c;
+            if (n >= p.N) continue;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const std::int64_t m = m0 + 32 * i + 8 * (r / 4) + 4 * h + r % 4;
+                    if (m < p.M) store(m, n, out[i][t][r]);
+                }
+        }
+    }
+}
+
+template <class T, int MT, int NT, int GS, bool ZP, bool Run, int WN, int WK>
+hipError_t launch_tile_shape(const W4Problem &p, hipStream_t stream)
+{
+    constexpr int BM = 32 * MT, BN = 32 * NT * WN, kLds = tile_lds<T, MT, NT, WN, WK>();
+    static_assert(kLds <= 160 * 1024, "fits the LDS");
+    const void *kernel = reinterpret_cast<const void *>(&w4_tile_kernel<T, MT, NT, GS, ZP, Run, WN, WK>);
+    if (kLds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        if (e != hipSuccess) return e;
+    }
+    // Bands of rows and columns keep the launch under 2^32 work-items.
+    constexpr std::int64_t kBand = 2048;
+    for (std::int64_t r0 = 0; r0 < p.M; r0 += kBand * BM)
+        for (std::int64_t c0 = 0; c0 < p.N; c0 += kBand * BN) {
+            W4Problem q = p;
+            q.M = int(p.M - r0 < kBand * BM ? p.M - r0 : kBand * BM);
+            q.N = int(p.N - c0 < kBand * BN ? p.N - c0 : kBand * BN);
+            q.A = static_cast<const char *>(p.A) + r0 * p.lda * std::int64_t(sizeof(typename T::elem));
+            q.W = p.W + c0 * p.ldw;
+            q.S = static_cast<const char *>(p.S) + c0 * p.lds * (p.stype == SGEMM_F32 ? 4 : 2);
+            if (p.Z) q.Z = p.Z + c0 * p.ldz;
+            q.C = p.C + r0 * p.ldc + c0;
+            int tiles_m = (q.M + BM - 1) / BM;
+            const int tiles_n = (q.N + BN - 1) / BN;
+            void *args[] = {&q, &tiles_m};
+            const hipError_t e = hipLaunchKernel(kernel, dim3(unsigned(tiles_m) * unsigned(tiles_n)), dim3(64 * WN * WK), args, kLds, stream);
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
+}
+
+template <class T, int GS, bool ZP, bool Run> hipError_t launch_tile(const W4Problem &p, hipStream_t stream)
+{
+    // The largest tile that still gives every compute unit one; with fewer
+    // tiles the waves divide K. float32 rows take three times the LDS.
+    constexpr bool wide = AOperand<T>::kPlanes == 1;
+    const auto tiles = [&](int bm, int bn) { return (std::int64_t(p.M) + bm - 1) / bm * ((std::int64_t(p.N) + bn - 1) / bn); };
+    if (tiles(64, 256) >= p.cus) return launch_tile_shape<T, 2, 2, GS, ZP, Run, 4, 1>(p, stream);
+    if constexpr (wide) {
+        if (tiles(64, 64) >= 2 * p.cus) return launch_tile_shape<T, 2, 2, GS, ZP, Run, 1, 4>(p, stream);
+        if (p.M > 32) return launch_tile_shape<T, 2, 1, GS, ZP, Run, 1, 8>(p, stream);
+        return launch_tile_shape<T, 1, 1, GS, ZP, Run, 1, 8>(p, stream);
+    } else {
+        return launch_tile_shape<T, 1, 1, GS, ZP, Run, 1, 4>(p, stream);
+    }
+}
+
+template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_shape(const W4Problem &p, hipStream_t stream)
+{
+    // Up to 8 rows (16 in float32, whose parts fill the tile kernel's LDS) the
+    // rows kernel is faster: 8192 x 8192 bf16, 8 rows 17.0 us against 17.7, 16
+    // rows 22.1 against 18.4; float32, 16 rows 32.8 against 41.5.
+    if (p.M <= (AOperand<T>::kPlanes == 1 ? 8 : 16)) return launch_rows<T, ST, 1, 1, GS, ZP, Run>(p, stream);
+    return launch_tile<T, GS, ZP, Run>(p, stream);
+}
+
+template <class T, class ST, bool ZP> hipError_t launch_group(const W4Problem &p, hipStream_t stream)
 {
     switch (p.group) {
-    case 32: return launch_run<T, 1, ZP>(p, stream);
-    case 64: return launch_run<T, 2, ZP>(p, stream);
-    case 128: return launch_run<T, 4, ZP>(p, stream);
+    case 32: return launch_shape<T, ST, 1, ZP, true>(p, stream);
+    case 64: return launch_shape<T, ST, 2, ZP, true>(p, stream);
+    case 128: return launch_shape<T, ST, 4, ZP, true>(p, stream);
     }
-    return p.group % 128 == 0 ? launch_shape<T, 4, ZP, Scales::Any>(p, stream) : launch_shape<T, 1, ZP, Scales::Any>(p, stream);
+    return p.group % 128 == 0 ? launch_shape<T, ST, 4, ZP, false>(p, stream) : launch_shape<T, ST, 1, ZP, false>(p, stream);
+}
+
+template <class T, class ST> hipError_t launch_zeros(const W4Problem &p, hipStream_t stream)
+{
+    return p.Z ? launch_group<T, ST, true>(p, stream) : launch_group<T, ST, false>(p, stream);
 }
 
 template <class T> hipError_t launch_w4(const W4Problem &p, hipStream_t stream)
 {
-    return p.Z ? launch_group<T, true>(p, stream) : launch_group<T, false>(p, stream);
+    return p.stype == SGEMM_F32       ? launch_zeros<T, F32>(p, stream)
+           : p.stype == SGEMM_LP_BF16 ? launch_zeros<T, BF16>(p, stream)
+                                      : launch_zeros<T, F16>(p, stream);
 }
 
 }  // namespace
