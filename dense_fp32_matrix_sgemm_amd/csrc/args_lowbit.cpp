@@ -189,12 +189,34 @@ bool kv8_read_overlaps(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int d
 
 Kv8Plan plan_kv8_attend(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus)
 {
-    (void)window;
-    (void)cus;
-    Kv8Plan plan{1, 1, 1};
-    const i64 rows = i64(b.max_new < b.rows ? b.max_new : b.rows) * (heads_q / c.heads);
-    const i64 tiles = (rows + 16 * plan.mt - 1) / (16 * plan.mt);
-    plan.tiles = int(tiles < 1 ? 1 : tiles < (1 << 20) ? tiles : (1 << 20));
+    cus = cus <= 0 ? 256 : cus < 4096 ? cus : 4096;
+    const i64 new_rows = b.max_new < b.rows ? b.max_new : b.rows, rows = at_least_1(new_rows * (heads_q / c.heads));
+    const i64 heads = i64(b.seqs) * c.heads;  // of all sequences
+    const auto tiles_of = [&](i64 tile) { return (rows + tile - 1) / tile; };
+    // A launch covers at most 2^22 work-groups at once; kernels walk the rest.
+    const i64 most = at_least_1((i64(1) << 22) / c.heads);
+    const auto cut = [&](i64 tiles) { return int(tiles < most ? tiles : most); };
+
+    Kv8Plan plan;
+    plan.splits = 1;
+    // Waves take row tiles of their own once that gives half the compute units a work-group.
+    const int most_mt = c.dim > 128 ? 1 : 2;  // longer heads have no registers for two
+    plan.rows = rows >= 64 * most_mt && (heads >= cus || 2 * tiles_of(64 * most_mt) * heads >= cus);
+    plan.mt = plan.rows || rows > 16 ? most_mt : 1;
+    if (plan.rows) {
+        plan.tiles = cut(tiles_of(64 * most_mt));
+        return plan;
+    }
+    plan.tiles = cut(tiles_of(16 * plan.mt));
+    // Else four work-groups a compute unit, each with at least 256 of the
+    // tokens that the longest sequence can have.
+    const i64 units = heads < 8 * i64(cus) ? heads * plan.tiles : heads;
+    i64 tokens = i64(b.table_ld) * c.block;
+    if (window > 0 && tokens > window + new_rows) tokens = window + new_rows;
+    i64 splits = units > 0 ? (4 * i64(cus) + units - 1) / units : 1;
+    if (splits > tokens / 256) splits = tokens / 256;
+    if (splits > 64) splits = 64;
+    plan.splits = int(splits < 1 ? 1 : splits);
     return plan;
 }
 
@@ -204,7 +226,10 @@ extern "C" size_t sgemm_kv8_attend_workspace_size(const sgemm_kv8_cache *c, cons
                                                   int window, int cus)
 {
     if (check_cache_batch(c, b) != SGEMM_OK || heads_q < 1 || heads_q % c->heads != 0 || window < 0) return 0;
+    if (b->seqs == 0 || b->rows == 0) return 0;
     const sgemm_impl::Kv8Plan plan = sgemm_impl::plan_kv8_attend(*c, *b, heads_q, window, cus);
-    (void)plan;
-    return 0;
+    if (plan.splits == 1) return 0;
+    // For each row of each split: the sums of its components, maximum and sum of the softmax.
+    return std::size_t(b->seqs) * std::size_t(c->heads) * std::size_t(plan.tiles) * std::size_t(plan.splits) * std::size_t(16 * plan.mt) *
+           std::size_t(c->dim + 4) * 4;
 }

@@ -28,6 +28,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "kv8.hpp"
 #include "lowbit.hpp"
 
@@ -113,44 +115,110 @@ template <> struct QOperand<F32> {
 // The bytes of a word that are e4m3 NaN, as 0x80 in each such byte.
 __device__ inline std::uint32_t nan_codes(std::uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// DC: a head of up to 32 DC components; MT: groups of 16 rows a wave holds.
-// A work-group's four waves take the tokens of one row tile in turns of 32
-// and add their sums through LDS in the waves' order.
-template <class T, int DC, int MT>
-__global__ __launch_bounds__(64 * kAttendWaves) void kv8_attend_kernel(Kv8AttendProblem p)
+// Eight weights p * scale, p >= 0, as three bf16 parts that add up to them
+// exactly (split3 without its care for infinities: a weight that is not
+// finite makes its whole row NaN in any case).
+__device__ inline void split_weights(const float *w, Frag &hi, Frag &mid, Frag &lo)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float h[2], m[2], l[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float x = w[2 * i + j];
+            h[j] = bits_f32(f32_bits(x) & 0xffff0000u);
+            const float r = x - h[j];
+            m[j] = bits_f32(f32_bits(r) & 0xffff0000u);
+            l[j] = r - m[j];
+        }
+        hi.v[i] = pack_hi(h[0], h[1]);
+        mid.v[i] = pack_hi(m[0], m[1]);
+        lo.v[i] = pack_hi(l[0], l[1]);
+    }
+}
+
+// The factor that brings a sum with maximum m to maximum top.
+__device__ inline float rescale(float m, float top) { return m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top); }
+
+// What the rows of one tile see: row `row` of a sequence (row / R th new row,
+// query head row % R of the group) sees `count` tokens from `from` on.
+struct Kv8Seen {
+    std::int64_t first, len, nameable;  // position of new row 0, tokens, tokens that the table can name
+    int R, causal, window;
+    __device__ void operator()(std::int64_t row, int &from, int &count) const
+    {
+        const std::int64_t pos = first + row / R;
+        std::int64_t hi = causal ? pos + 1 : len, lo = window > 0 ? pos + 1 - window : 0;
+        if (hi > nameable) hi = nameable;
+        lo = lo < 0 ? 0 : lo;
+        hi = hi < lo ? lo : hi;
+        from = int(lo);
+        count = int(hi - lo);
+    }
+};
+
+// Waves a SIMD has registers for: two, but for the longest heads and for two
+// groups of float32 rows (three parts of Q each).
+template <class T> constexpr int kv8_waves_per_simd(int DC, int MT) { return DC > 4 || (DC == 4 && MT == 2 && sizeof(typename T::elem) == 4) ? 1 : 2; }
+
+// DC: a head of up to 32 DC components; Full: of exactly that many. MT: groups
+// of 16 rows a wave holds. Rows: the four waves of a work-group take row tiles
+// of their own (prompts: the same keys and values pass through the compute
+// unit's cache for all four). Otherwise they take the tokens of one row tile
+// in turns of 32 and add their sums through LDS in the waves' order, and
+// `splits` work-groups share the tile's tokens: each leaves its sums in the
+// workspace and kv8_join_kernel adds them.
+//
+// Keys of the next 32 tokens are loaded into the registers of the last ones
+// as soon as their scores are formed, values likewise after their product:
+// each has half a turn to arrive. No load is conditional (that would make the
+// compiler wait for all of them): pages that may not be read are replaced by
+// page 0 and their scores by NaN.
+template <class T, int DC, bool Full, int MT, bool Rows>
+__global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) void kv8_attend_kernel(Kv8AttendProblem p)
 {
     constexpr int PD = 32 * DC, kRows = 16 * MT, kDTiles = 2 * DC, kLd = PD + 4;
     __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows];
-    __shared__ __align__(16) float sm_o[kRows * kLd];
+    __shared__ __align__(16) float sm_o[Rows ? 4 : kRows * kLd];
     typedef typename T::elem elem;
     const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int dim = p.c.dim, block = p.c.block, R = p.heads_q / p.c.heads;
+    const int dim = Full ? PD : p.c.dim, R = p.heads_q / p.c.heads;
+    const int shift = 31 - __builtin_clz(unsigned(p.c.block)), block = 1 << shift;
 
     unsigned id = blockIdx.x;
+    const int split = int(id % unsigned(p.plan.splits));
+    id /= unsigned(p.plan.splits);
     const int tile0 = int(id % unsigned(p.plan.tiles));
     id /= unsigned(p.plan.tiles);
     const int head = int(id % unsigned(p.c.heads));
-    for (unsigned seq = id / unsigned(p.c.heads); seq < unsigned(p.b.seqs); seq += gridDim.x / (unsigned(p.plan.tiles) * unsigned(p.c.heads))) {
+    const unsigned seqs_at_once = gridDim.x / (unsigned(p.plan.splits) * unsigned(p.plan.tiles) * unsigned(p.c.heads));
+    const float factor = p.scale * kLog2e;
+    const std::uint8_t *const codes_k = static_cast<const std::uint8_t *>(p.c.K), *const codes_v = static_cast<const std::uint8_t *>(p.c.V);
+    // Lanes past the head's components read its first ones: keys are then
+    // zeroed, values give components that are not stored.
+    const int k_at = c * dim, v_at = 4 * kq * dim + (Full || c * 2 * DC < dim ? c * 2 * DC : 0);
+
+    for (unsigned seq = id / unsigned(p.c.heads); seq < unsigned(p.b.seqs); seq += seqs_at_once) {
         const Kv8Sequence s = kv8_sequence(p.b, int(seq));
         const std::int64_t all_rows = s.n * R;
         // Tokens the table cannot name: every row of the sequence is NaN.
-        const std::int64_t nameable = std::int64_t(p.b.table_ld) * block;
+        const std::int64_t nameable = std::int64_t(p.b.table_ld) << shift;
         const bool short_table = s.len > nameable;
-        for (std::int64_t row0 = std::int64_t(tile0) * kRows; row0 < all_rows; row0 += std::int64_t(p.plan.tiles) * kRows) {
+        const Kv8Seen seen{s.len - s.n, s.len, nameable, R, p.causal, p.window};
+        const int *const table = p.b.table + std::int64_t(seq) * p.b.table_ld;
+        for (std::int64_t tile = tile0;; tile += p.plan.tiles) {
+            const std::int64_t row0 = Rows ? (tile * kAttendWaves + wave) * kRows : tile * kRows;
+            if ((Rows ? tile * kAttendWaves * kRows : row0) >= all_rows) break;
+            // Tiles beyond those the grid (and the workspace) was laid out for are not split.
+            const bool whole = p.plan.splits == 1 || tile >= p.plan.tiles;
+            if (whole && split > 0) break;
+            if (Rows && row0 >= all_rows) continue;  // no barrier below when Rows
+
             // Each lane's rows: what they see, and their operands. Rows past
             // the last repeat it; what they give is not stored.
             int lo_t[MT], n_t[MT];  // first token seen, tokens seen
             QOperand<T> q[MT][DC];
-            auto seen = [&](std::int64_t row, int &from, int &count) {
-                const std::int64_t pos = s.len - s.n + row / R;
-                std::int64_t hi = p.causal ? pos + 1 : s.len, lo = p.window > 0 ? pos + 1 - p.window : 0;
-                if (hi > nameable) hi = nameable;
-                lo = lo < 0 ? 0 : lo;
-                hi = hi < lo ? lo : hi;
-                from = int(lo);
-                count = int(hi - lo);
-            };
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 std::int64_t row = row0 + 16 * t + c;
@@ -158,156 +226,210 @@ __global__ __launch_bounds__(64 * kAttendWaves) void kv8_attend_kernel(Kv8Attend
                 seen(row, lo_t[t], n_t[t]);
                 const elem *src = static_cast<const elem *>(p.Q) + (s.row0 + row / R) * p.ldq + (head * R + row % R) * p.hsq;
 #pragma unroll
-                for (int i = 0; i < DC; ++i) q[t][i].load(src + (kq * DC + i) * 8, (kq * DC + i) * 8 < dim);
+                for (int i = 0; i < DC; ++i) q[t][i].load(src + (kq * DC + i) * 8, Full || (kq * DC + i) * 8 < dim);
             }
             int first_lo, first_n, last_lo, last_n;
-            const std::int64_t last = row0 + kRows < all_rows ? row0 + kRows - 1 : all_rows - 1;
             seen(row0, first_lo, first_n);
-            seen(last, last_lo, last_n);
-            const int begin = first_lo & ~31, end = last_lo + last_n;   // tokens some row sees
-            const int open = last_lo, close = first_lo + first_n;       // tokens every row sees
+            seen(row0 + kRows < all_rows ? row0 + kRows - 1 : all_rows - 1, last_lo, last_n);
+            // Turns of 32 tokens: begin .. end sees some row; inner .. outer every row in full.
+            int begin = first_lo >> 5, end = (last_lo + last_n + 31) >> 5, inner = (last_lo + 31) >> 5, outer = (first_lo + first_n) >> 5;
+            const int limit = last_lo + last_n;
+            if (!whole) {
+                const int turns = end - begin, b = begin;
+                begin = b + int(std::int64_t(turns) * split / p.plan.splits);
+                end = b + int(std::int64_t(turns) * (split + 1) / p.plan.splits);
+            }
 
             f32x4 o[MT][kDTiles] = {};
             float m[MT], l[MT];
 #pragma unroll
             for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = 0.0f;
 
-            for (int t0 = begin + 32 * wave; t0 < end; t0 += 32 * kAttendWaves) {
-                u32x2 k[2][DC];
-                std::uint32_t v[8][DC / 2];
-                float ks[2], vs[2];
-                const std::uint8_t *vrow[2];
+            // The page of a half turn, and its offset in codes; NaN scales where it may not be read.
+            struct Half {
+                const std::uint8_t *k, *v;
+                float ks, vs;
+            };
+            auto half_at = [&](int t) {
+                const int page = t < limit ? table[t >> shift] : 0;  // limit <= nameable
+                const bool good = unsigned(page) < unsigned(p.c.pages);
+                const std::int64_t at = std::int64_t(good ? page : 0) * p.c.heads + head;
+                const std::int64_t byte0 = ((at << shift) + (t & (block - 1))) * dim;
+                Half h{codes_k + byte0, codes_v + byte0, p.c.Ks[at], p.c.Vs[at]};
+                if (!good) h.ks = h.vs = __builtin_nanf("");
+                return h;
+            };
+            u32x2 k[2][DC];
+            std::uint32_t v[8][DC / 2];
+            auto load_keys = [&](const Half (&h)[2]) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int t = t0 + 16 * h;
-                    std::int64_t page = -1;
-                    if (t < end) page = kv8_page(p.c, p.b, int(seq), t / block);
-                    ks[h] = vs[h] = t < end ? __builtin_nanf("") : 0.0f;
-                    const std::int64_t at = (page < 0 ? 0 : page) * p.c.heads + head;
-                    const std::int64_t byte0 = (at * block + (t & (block - 1))) * dim;
-                    if (page >= 0) ks[h] = p.c.Ks[at], vs[h] = p.c.Vs[at];
-                    const std::uint8_t *kr = static_cast<const std::uint8_t *>(p.c.K) + byte0 + c * dim + kq * 8 * DC;
-                    vrow[h] = page < 0 ? nullptr : static_cast<const std::uint8_t *>(p.c.V) + byte0;
-                    const std::uint8_t *vr = static_cast<const std::uint8_t *>(p.c.V) + byte0 + 4 * kq * dim + c * 2 * DC;
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int i = 0; i < DC; ++i) {
-                        k[h][i] = u32x2{0, 0};
-                        if (page >= 0 && (kq * DC + i) * 8 < dim) k[h][i] = *reinterpret_cast<const u32x2 *>(kr + 8 * i);
+                        const int d = (kq * DC + i) * 8;
+                        const bool there = Full || d < dim;
+                        k[x][i] = *reinterpret_cast<const u32x2 *>(h[x].k + k_at + (there ? d : 0));
+                        if (!Full) k[x][i] = there ? k[x][i] : u32x2{0, 0};
                     }
+            };
+            auto load_values = [&](const Half (&h)[2]) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-#pragma unroll
-                        for (int i = 0; i < DC / 2; ++i) v[4 * h + r][i] = 0;
-                        if (page >= 0 && c * 2 * DC < dim) __builtin_memcpy(v[4 * h + r], vr + r * dim, 2 * DC);
-                    }
-                }
-                const bool cut = t0 < open || t0 + 32 > close;  // some row does not see all 32
-                bool poisoned = false;
-                if (cut) {
-                    // NaN codes must not reach rows that do not see them (0 * NaN):
-                    // they leave the product and are put back below.
-                    std::uint32_t any = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-#pragma unroll
-                        for (int i = 0; i < DC / 2; ++i) {
-                            const std::uint32_t n = nan_codes(v[e][i]);
-                            any |= n;
-                            v[e][i] &= ~((n >> 7) * 0xffu);
-                        }
-                    poisoned = __ballot(any != 0) != 0;
-                }
+                for (int e = 0; e < 8; ++e) __builtin_memcpy(v[e], h[e / 4].v + v_at + (e % 4) * dim, 2 * DC);
+            };
 
-                Frag ph[MT], pm[MT], pl[MT];
+            // Turns from .. to, this wave's among them; Cut: some row does not see all of a turn.
+            auto turns = [&](int from, int to, auto cut_) {
+                constexpr bool Cut = decltype(cut_)::value;
+                constexpr int kStride = Rows ? 1 : kAttendWaves;
+                int turn = from + (Rows ? 0 : (wave - from) & (kAttendWaves - 1));
+                if (turn >= to) return;
+                Half now[2] = {half_at(32 * turn), half_at(32 * turn + 16)};
+                load_keys(now);
+                load_values(now);
+                for (; turn < to; turn += kStride) {
+                    const int t0 = 32 * turn, tn = turn + kStride < to ? 32 * (turn + kStride) : t0;
+                    const Half next[2] = {half_at(tn), half_at(tn + 16)};
+                    float z[MT][8];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    float z[8];
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        f32x4 acc = {};
+                        for (int t = 0; t < MT; ++t) {
+                            f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < DC; ++i) acc = q[t][i].scores(k[h][i], acc);
-                        const float f = ks[h] * (p.scale * kLog2e);
+                            for (int i = 0; i < DC; ++i) acc = q[t][i].scores(k[x][i], acc);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) z[4 * h + r] = acc[r] * f;
+                            for (int r = 0; r < 4; ++r) z[t][4 * x + r] = acc[r] * (now[x].ks * factor);
+                        }
+                    load_keys(next);
+                    bool poisoned = false;
+                    if (Cut) {
+                        // NaN codes must not reach rows that do not see them (0 * NaN):
+                        // they leave the product and are put back below.
+                        std::uint32_t any = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+#pragma unroll
+                            for (int i = 0; i < DC / 2; ++i) {
+                                const std::uint32_t nan = nan_codes(v[e][i]);
+                                any |= nan;
+                                v[e][i] &= ~((nan >> 7) * 0xffu);
+                            }
+                        poisoned = __ballot(any != 0) != 0;
                     }
-                    if (cut) {
+                    Frag ph[MT], pm[MT], pl[MT];
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        if (Cut) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const unsigned j = unsigned(t0 + 16 * (e / 4) + 4 * kq + e % 4 - lo_t[t]);
+                                z[t][e] = j < unsigned(n_t[t]) ? z[t][e] : -__builtin_inff();
+                            }
+                        }
+                        float top = __builtin_fmaxf(z[t][0], z[t][1]);
+#pragma unroll
+                        for (int e = 2; e < 8; ++e) top = __builtin_fmaxf(top, z[t][e]);
+                        top = column_max(top);
+                        if (__ballot(top > m[t]) != 0) {
+                            const float risen = __builtin_fmaxf(m[t], top), a = rescale(m[t], risen);
+                            m[t] = risen;
+                            l[t] *= a;
+#pragma unroll
+                            for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
+                        }
+                        const float base = m[t] == -__builtin_inff() ? 0.0f : m[t];
+                        float w[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const unsigned j = unsigned(t0 + 16 * (e / 4) + 4 * kq + e % 4 - lo_t[t]);
-                            z[e] = j < unsigned(n_t[t]) ? z[e] : -__builtin_inff();
+                            const float pe = __builtin_amdgcn_exp2f(z[t][e] - base);
+                            l[t] += pe;
+                            w[e] = pe * now[e / 4].vs;
+                            if (Cut) w[e] = z[t][e] == -__builtin_inff() ? 0.0f : w[e];
                         }
-                    }
-                    float top = z[0];
-#pragma unroll
-                    for (int e = 1; e < 8; ++e) top = __builtin_fmaxf(top, z[e]);
-                    top = column_max(top);
-                    if (__ballot(top > m[t]) != 0) {
-                        const float risen = __builtin_fmaxf(m[t], top);
-                        const float a = m[t] == risen ? 1.0f : __builtin_amdgcn_exp2f(m[t] - risen);
-                        m[t] = risen;
-                        l[t] *= a;
-#pragma unroll
-                        for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
-                    }
-                    const float base = m[t] == -__builtin_inff() ? 0.0f : m[t];
-                    float w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float pe = __builtin_amdgcn_exp2f(z[e] - base);
-                        l[t] += pe;
-                        w[e] = pe * vs[e / 4];
-                        if (cut) w[e] = z[e] == -__builtin_inff() ? 0.0f : w[e];
-                    }
-                    split3(w, ph[t], pm[t], pl[t]);
-                }
-#pragma unroll
-                for (int i = 0; i < DC / 2; ++i) {
-                    Frag f[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const std::uint32_t a = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x05010400u);
-                        const std::uint32_t b = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x07030602u);
-                        f[0].v[e] = codes_bf16(a, false);
-                        f[1].v[e] = codes_bf16(a, true);
-                        f[2].v[e] = codes_bf16(b, false);
-                        f[3].v[e] = codes_bf16(b, true);
+                        split_weights(w, ph[t], pm[t], pl[t]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int i = 0; i < DC / 2; ++i) {
+                        Frag f[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const std::uint32_t a = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x05010400u);
+                            const std::uint32_t b = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x07030602u);
+                            f[0].v[e] = codes_bf16(a, false);
+                            f[1].v[e] = codes_bf16(a, true);
+                            f[2].v[e] = codes_bf16(b, false);
+                            f[3].v[e] = codes_bf16(b, true);
+                        }
 #pragma unroll
                         for (int t = 0; t < MT; ++t)
-                            o[t][4 * i + j] = mfma_bf16(f[j], ph[t], mfma_bf16(f[j], pm[t], mfma_bf16(f[j], pl[t], o[t][4 * i + j])));
-                }
-                if (poisoned) {
-                    for (int u = 0; u < 32; ++u) {
-                        const std::uint8_t *row = vrow[u / 16];
-                        if (row == nullptr) continue;
 #pragma unroll
-                        for (int x = 0; x < 4 * kDTiles; ++x) {
-                            const int d = kq * 8 * DC + x;  // component of register x / kDTiles of d-tile x % kDTiles
-                            if (d >= dim || (row[(u % 16) * dim + d] & 0x7f) != 0x7f) continue;
+                            for (int j = 0; j < 4; ++j) {
+                                f32x4 &acc = o[t][4 * i + j];
+                                acc = mfma_bf16(f[j], ph[t], mfma_bf16(f[j], pm[t], mfma_bf16(f[j], pl[t], acc)));
+                            }
+                    }
+                    if (Cut && poisoned) {
+                        for (int u = 0; u < 32; ++u) {
+                            const float vs = u < 16 ? now[0].vs : now[1].vs;
+                            if (vs != vs) continue;  // not read
+                            const std::uint8_t *row = (u < 16 ? now[0].v : now[1].v) + (u % 16) * dim;
 #pragma unroll
-                            for (int t = 0; t < MT; ++t)
-                                if (unsigned(t0 + u - lo_t[t]) < unsigned(n_t[t])) o[t][x % kDTiles][x / kDTiles] = __builtin_nanf("");
+                            for (int x = 0; x < 4 * kDTiles; ++x) {
+                                const int d = kq * 8 * DC + x;  // component of register x / kDTiles of d-tile x % kDTiles
+                                if (d >= dim || (row[d] & 0x7f) != 0x7f) continue;
+#pragma unroll
+                                for (int t = 0; t < MT; ++t)
+                                    if (unsigned(t0 + u - lo_t[t]) < unsigned(n_t[t])) o[t][x % kDTiles][x / kDTiles] = __builtin_nanf("");
+                            }
                         }
                     }
+                    load_values(next);
+                    now[0] = next[0];
+                    now[1] = next[1];
                 }
+            };
+            if (inner < outer) {
+                const int a = inner < end ? (inner > begin ? inner : begin) : end, b = outer < end ? (outer > a ? outer : a) : end;
+                turns(begin, a, std::true_type{});
+                turns(a, b, std::false_type{});
+                turns(b, end, std::true_type{});
+            } else {
+                turns(begin, end, std::true_type{});
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) l[t] = column_sum(l[t]);
+
+            if constexpr (Rows) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const std::int64_t row = row0 + 16 * t + c;
+                    if (row >= all_rows) continue;
+                    float inverse = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+                    if (short_table) inverse = __builtin_nanf("");
+                    float *dst = p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + kq * 8 * DC;
+#pragma unroll
+                    for (int x = 0; x < 4 * kDTiles; x += 4) {
+                        if (!Full && kq * 8 * DC + x >= dim) continue;
+                        f32x4 y;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) y[j] = o[t][(x + j) % kDTiles][x / kDTiles] * inverse;
+                        __builtin_memcpy(dst + x, &y, sizeof(y));
+                    }
+                }
+                continue;
             }
 
             // The waves' sums: all onto the largest maximum.
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                l[t] = column_sum(l[t]);
+            for (int t = 0; t < MT; ++t)
                 if (kq == 0) sm_m[wave][16 * t + c] = m[t], sm_l[wave][16 * t + c] = l[t];
-            }
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 float top = sm_m[0][16 * t + c];
 #pragma unroll
                 for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][16 * t + c]);
-                const float a = m[t] == top ? 1.0f : __builtin_amdgcn_exp2f(m[t] - top);
+                const float a = rescale(m[t], top);
 #pragma unroll
                 for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
             }
@@ -326,42 +448,96 @@ __global__ __launch_bounds__(64 * kAttendWaves) void kv8_attend_kernel(Kv8Attend
                 }
                 __syncthreads();
             }
-            const std::int64_t rows = all_rows - row0 < kRows ? all_rows - row0 : kRows;
-            for (int e = threadIdx.x; e < int(rows) * dim; e += 64 * kAttendWaves) {
-                const int i = e / dim, d = e % dim;
+            const int rows = int(all_rows - row0 < kRows ? all_rows - row0 : kRows);
+            // A thread keeps one component quad of every 4 * 64 / (PD / 4)-th row.
+            constexpr int kQuads = PD / 4, kStep = 64 * kAttendWaves / kQuads;
+            const int d = int(threadIdx.x) % kQuads * 4;
+            for (int i = threadIdx.x / kQuads; i < rows; i += kStep) {
                 float top = sm_m[0][i], sum = 0.0f;
 #pragma unroll
                 for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][i]);
 #pragma unroll
-                for (int w = 0; w < kAttendWaves; ++w)
-                    sum += sm_l[w][i] * (sm_m[w][i] == top ? 1.0f : __builtin_amdgcn_exp2f(sm_m[w][i] - top));
-                float x = sm_o[i * kLd + d];
-                x = sum == 0.0f ? 0.0f : x / sum;
-                if (short_table) x = __builtin_nanf("");
-                const std::int64_t row = row0 + i;
-                p.O[(s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + d] = x;
+                for (int w = 0; w < kAttendWaves; ++w) sum += sm_l[w][i] * rescale(sm_m[w][i], top);
+                if (!Full && d >= dim) continue;
+                f32x4 x = *reinterpret_cast<const f32x4 *>(&sm_o[i * kLd + d]);
+                if (whole) {
+                    const std::int64_t row = row0 + i;
+                    x = sum == 0.0f ? f32x4{0, 0, 0, 0} : x / sum;
+                    if (short_table) x = x * __builtin_nanf("");
+                    __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + d, &x, sizeof(x));
+                } else {
+                    const std::int64_t at = (((std::int64_t(seq) * p.c.heads + head) * p.plan.tiles + tile) * p.plan.splits + split) * kRows + i;
+                    *reinterpret_cast<f32x4 *>(p.ws + at * (dim + 4) + d) = x;
+                    if (d == 0) p.ws[at * (dim + 4) + dim] = top, p.ws[at * (dim + 4) + dim + 1] = sum;
+                }
             }
             __syncthreads();
         }
     }
 }
 
-template <class T, int DC, int MT> hipError_t launch_attend_shape(const Kv8AttendProblem &p, hipStream_t stream)
+// Adds the sums that the splits of a row tile left in the workspace, in their
+// order: one wave for each row.
+template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendProblem p)
 {
-    const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads;
-    std::int64_t seqs = (std::int64_t(1) << 23) / per_seq;
+    constexpr int kRows = 16 * MT;
+    const int lane = threadIdx.x & 63, R = p.heads_q / p.c.heads, dim = p.c.dim, splits = p.plan.splits;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned unit = blockIdx.x / (kRows / 4), i = blockIdx.x % (kRows / 4) * 4 + unsigned(wave);
+    const int tile = int(unit % unsigned(p.plan.tiles)), head = int(unit / unsigned(p.plan.tiles) % unsigned(p.c.heads));
+    const int seq = int(unit / unsigned(p.plan.tiles) / unsigned(p.c.heads));
+    const Kv8Sequence s = kv8_sequence(p.b, seq);
+    const std::int64_t row = std::int64_t(tile) * kRows + i;
+    if (row >= s.n * R) return;
+    const float *const part = p.ws + (std::int64_t(unit) * splits * kRows + i) * (dim + 4);
+    const std::int64_t pitch = std::int64_t(kRows) * (dim + 4);
+    float top = -__builtin_inff();
+    for (int x = 0; x < splits; ++x) top = __builtin_fmaxf(top, part[x * pitch + dim]);
+    f32x4 y = {0, 0, 0, 0};
+    float sum = 0.0f;
+    for (int x = 0; x < splits; ++x) {
+        const float l = part[x * pitch + dim + 1];
+        const float a = rescale(part[x * pitch + dim], top);
+        if (l == 0.0f) continue;  // saw nothing
+        sum += l * a;
+        if (4 * lane < dim) y += *reinterpret_cast<const f32x4 *>(part + x * pitch + 4 * lane) * a;
+    }
+    if (4 * lane >= dim) return;
+    y = sum == 0.0f ? f32x4{0, 0, 0, 0} : y / sum;
+    if (s.len > std::int64_t(p.b.table_ld) * p.c.block) y = y * __builtin_nanf("");
+    __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + 4 * lane, &y, sizeof(y));
+}
+
+template <class T, int DC, bool Full, int MT, bool Rows> hipError_t launch_attend_kernel(const Kv8AttendProblem &p, hipStream_t stream)
+{
+    const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads * p.plan.splits;
+    std::int64_t seqs = (std::int64_t(1) << 23) / per_seq;  // splits > 1: all of them (plan_kv8_attend)
     seqs = seqs < 1 ? 1 : seqs < p.b.seqs ? seqs : p.b.seqs;
     Kv8AttendProblem q = p;
     void *args[] = {&q};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&kv8_attend_kernel<T, DC, MT>), dim3(unsigned(per_seq * seqs)),
-                           dim3(64 * kAttendWaves), args, 0, stream);
+    hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&kv8_attend_kernel<T, DC, Full, MT, Rows>), dim3(unsigned(per_seq * seqs)),
+                                   dim3(64 * kAttendWaves), args, 0, stream);
+    if (e != hipSuccess || p.plan.splits == 1) return e;
+    const unsigned units = unsigned(p.plan.tiles) * unsigned(p.c.heads) * unsigned(p.b.seqs);
+    return hipLaunchKernel(reinterpret_cast<const void *>(&kv8_join_kernel<MT>), dim3(units * (4 * MT)), dim3(256), args, 0, stream);
+}
+
+template <class T, int DC, bool Full> hipError_t launch_attend_shape(const Kv8AttendProblem &p, hipStream_t stream)
+{
+    constexpr int kMost = DC > 4 ? 1 : 2;  // plan_kv8_attend gives no more
+    if (p.plan.rows) return launch_attend_kernel<T, DC, Full, kMost, true>(p, stream);
+    return p.plan.mt == 1 ? launch_attend_kernel<T, DC, Full, 1, false>(p, stream) : launch_attend_kernel<T, DC, Full, kMost, false>(p, stream);
 }
 
 template <class T> hipError_t launch_attend(const Kv8AttendProblem &p, hipStream_t stream)
 {
-    if (p.c.dim <= 64) return launch_attend_shape<T, 2, 1>(p, stream);
-    if (p.c.dim <= 128) return launch_attend_shape<T, 4, 1>(p, stream);
-    return launch_attend_shape<T, 8, 1>(p, stream);
+    switch (p.c.dim) {
+    case 64: return launch_attend_shape<T, 2, true>(p, stream);
+    case 128: return launch_attend_shape<T, 4, true>(p, stream);
+    case 256: return launch_attend_shape<T, 8, true>(p, stream);
+    }
+    if (p.c.dim < 64) return launch_attend_shape<T, 2, false>(p, stream);
+    return p.c.dim < 128 ? launch_attend_shape<T, 4, false>(p, stream) : launch_attend_shape<T, 8, false>(p, stream);
 }
 
 }  // namespace

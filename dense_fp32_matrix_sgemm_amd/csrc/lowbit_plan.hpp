@@ -9,7 +9,8 @@ namespace sgemm_impl {
 // (args_lowbit.cpp), so that the workspace's size needs no device.
 struct Kv8Plan {
     int mt;        // groups of 16 rows a wave holds
-    int tiles;     // row tiles of 16 * mt rows per sequence and head the grid covers at once
+    int rows;      // 1: a work-group's waves take row tiles of their own; 0: the tokens of one row tile
+    int tiles;     // row tiles (of one wave, or four when rows) per sequence and head the grid covers at once
     int splits;    // work-groups that share a row tile's tokens
 };
 Kv8Plan plan_kv8_attend(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus);
