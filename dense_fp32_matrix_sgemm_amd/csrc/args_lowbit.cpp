@@ -199,21 +199,25 @@ Kv8Plan plan_kv8_attend(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int 
 
     Kv8Plan plan;
     plan.splits = 1;
-    // Waves take row tiles of their own once that gives half the compute units a work-group.
+    // Waves take row tiles of their own once that gives every compute unit a work-group
+    // (8 sequences of 64 rows behind 2048 tokens, at half of that: 118 us against 66).
     const int most_mt = c.dim > 128 ? 1 : 2;  // longer heads have no registers for two
-    plan.rows = rows >= 64 * most_mt && (heads >= cus || 2 * tiles_of(64 * most_mt) * heads >= cus);
+    plan.rows = rows >= 64 * most_mt && (heads >= cus || tiles_of(64 * most_mt) * heads >= cus);
     plan.mt = plan.rows || rows > 16 ? most_mt : 1;
     if (plan.rows) {
         plan.tiles = cut(tiles_of(64 * most_mt));
         return plan;
     }
     plan.tiles = cut(tiles_of(16 * plan.mt));
-    // Else four work-groups a compute unit, each with at least 256 of the
-    // tokens that the longest sequence can have.
+    // Else as many work-groups as the compute units hold at once (their
+    // registers allow 4, 3 or 1 by the head's length: 32 sequences of 8192
+    // tokens and 128 components in 3 splits 92 us, in 4 104), each with at
+    // least 256 of the tokens that the longest sequence can have.
+    const int resident = c.dim <= 64 ? 4 : c.dim <= 128 ? 3 : 1;
     const i64 units = heads < 8 * i64(cus) ? heads * plan.tiles : heads;
     i64 tokens = i64(b.table_ld) * c.block;
     if (window > 0 && tokens > window + new_rows) tokens = window + new_rows;
-    i64 splits = units > 0 ? (4 * i64(cus) + units - 1) / units : 1;
+    i64 splits = units > 0 ? (resident * i64(cus) + units - 1) / units : 1;
     if (splits > tokens / 256) splits = tokens / 256;
     if (splits > 64) splits = 64;
     plan.splits = int(splits < 1 ? 1 : splits);

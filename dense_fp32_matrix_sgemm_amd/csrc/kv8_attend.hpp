@@ -491,17 +491,28 @@ template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Atte
     if (row >= s.n * R) return;
     const float *const part = p.ws + (std::int64_t(unit) * splits * kRows + i) * (dim + 4);
     const std::int64_t pitch = std::int64_t(kRows) * (dim + 4);
-    float top = -__builtin_inff();
-    for (int x = 0; x < splits; ++x) top = __builtin_fmaxf(top, part[x * pitch + dim]);
+    // Lane x: split x's maximum and sum (at most 64 splits).
+    float m = -__builtin_inff(), l = 0.0f;
+    if (lane < splits) m = part[lane * pitch + dim], l = part[lane * pitch + dim + 1];
+    float top = m;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    // A split that saw nothing weighs nothing, and its components were left as sums of nothing: zeros.
+    const float a = l == 0.0f ? 0.0f : rescale(m, top);
+    float sum = l * a;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
     f32x4 y = {0, 0, 0, 0};
-    float sum = 0.0f;
-    for (int x = 0; x < splits; ++x) {
-        const float l = part[x * pitch + dim + 1];
-        const float a = rescale(part[x * pitch + dim], top);
-        if (l == 0.0f) continue;  // saw nothing
-        sum += l * a;
-        if (4 * lane < dim) y += *reinterpret_cast<const f32x4 *>(part + x * pitch + 4 * lane) * a;
+    const float *const at = part + (4 * lane < dim ? 4 * lane : 0);
+    int x = 0;
+    for (; x + 4 <= splits; x += 4) {
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const f32x4 *>(at + (x + i) * pitch);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y += v[i] * __shfl(a, x + i);
     }
+    for (; x < splits; ++x) y += *reinterpret_cast<const f32x4 *>(at + x * pitch) * __shfl(a, x);
     if (4 * lane >= dim) return;
     y = sum == 0.0f ? f32x4{0, 0, 0, 0} : y / sum;
     if (s.len > std::int64_t(p.b.table_ld) * p.c.block) y = y * __builtin_nanf("");
