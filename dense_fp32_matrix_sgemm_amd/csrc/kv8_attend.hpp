@@ -112,6 +112,14 @@ template <> struct QOperand<F32> {
     }
 };
 
+// An element that all lanes read, of an array that no kernel writes meanwhile:
+// through the constant address space it becomes a scalar load, which no wait
+// for a vector load holds up.
+template <class V> __device__ inline V uniform_load(const V *p, std::int64_t i)
+{
+    return reinterpret_cast<const __attribute__((address_space(4))) V *>(reinterpret_cast<std::uintptr_t>(p))[i];
+}
+
 // The bytes of a word that are e4m3 NaN, as 0x80 in each such byte.
 __device__ inline std::uint32_t nan_codes(std::uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
@@ -251,11 +259,12 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                 float ks, vs;
             };
             auto half_at = [&](int t) {
-                const int page = t < limit ? table[t >> shift] : 0;  // limit <= nameable
+                // Past the tokens seen (limit <= nameable) any page of the table will do; none is named by an empty one.
+                const int page = uniform_load(table, (t < limit ? t : limit - 1) >> shift);
                 const bool good = unsigned(page) < unsigned(p.c.pages);
                 const std::int64_t at = std::int64_t(good ? page : 0) * p.c.heads + head;
                 const std::int64_t byte0 = ((at << shift) + (t & (block - 1))) * dim;
-                Half h{codes_k + byte0, codes_v + byte0, p.c.Ks[at], p.c.Vs[at]};
+                Half h{codes_k + byte0, codes_v + byte0, uniform_load(p.c.Ks, at), uniform_load(p.c.Vs, at)};
                 if (!good) h.ks = h.vs = __builtin_nanf("");
                 return h;
             };
