@@ -28,24 +28,25 @@ constexpr int kThreads = 256;
 std::int64_t pages_reached(std::int64_t n, int block) { return n < 1 ? 1 : (n + block - 2) / block + 1; }
 
 struct Grid {
-    unsigned pieces, groups;
+    unsigned pieces, seqs;  // pages of a sequence, and sequences, that the launch covers at once
 };
 
-// Work-groups: pieces (pages) x sequences x heads x {K, V}, the pages cut so
-// that the launch stays in range; a kernel walks the pages beyond.
+// Work-groups: sequences x pieces (pages) x heads x {K, V}; kernels walk the
+// pages and sequences beyond.
 Grid grid_of(const Kv8Problem &p)
 {
-    const std::int64_t n = p.b.max_new < p.b.rows ? p.b.max_new : p.b.rows;
-    std::int64_t pieces = pages_reached(n, p.c.block);
-    const std::int64_t others = 2 * std::int64_t(p.b.seqs) * p.c.heads;
-    const std::int64_t most = (std::int64_t(1) << 23) / others;
-    if (pieces > most) pieces = most < 1 ? 1 : most;
-    const std::int64_t groups = pieces * others;
-    // Sequences x heads beyond the grid are walked too.
-    return {unsigned(pieces), unsigned(groups < (std::int64_t(1) << 23) ? groups : (std::int64_t(1) << 23))};
+    const std::int64_t n = p.b.max_new < p.b.rows ? p.b.max_new : p.b.rows, most = std::int64_t(1) << 23;
+    const std::int64_t heads = 2 * std::int64_t(p.c.heads);
+    std::int64_t pieces = pages_reached(n, p.c.block), room = most / heads;
+    room = room < 1 ? 1 : room;
+    if (pieces > room) pieces = room;
+    std::int64_t seqs = most / (pieces * heads);
+    seqs = seqs < 1 ? 1 : seqs < p.b.seqs ? seqs : p.b.seqs;
+    return {unsigned(pieces), unsigned(seqs)};
 }
 
-// One work-group's share: rows of sequence `seq` in one page.
+// One work-group's share: rows of one sequence in one page, for one head of K
+// or V.
 struct Piece {
     int head, kv;
     Kv8Sequence s;
@@ -53,22 +54,39 @@ struct Piece {
 };
 
 // Calls body(piece) for every piece that falls to this work-group.
-template <class Body> __device__ inline void for_each_piece(const Kv8Problem &p, unsigned pieces, Body &&body)
+template <class Body> __device__ inline void for_each_piece(const Kv8Problem &p, const Grid &g, Body &&body)
 {
-    const std::int64_t all = 2 * std::int64_t(pieces) * p.b.seqs * p.c.heads;
-    for (std::int64_t id = blockIdx.x; id < all; id += gridDim.x) {
-        Piece w;
-        w.kv = int(id & 1);
-        std::int64_t rest = id >> 1;
-        w.head = int(rest % p.c.heads);
-        rest /= p.c.heads;
-        const std::int64_t first = rest % pieces;
-        w.s = kv8_sequence(p.b, int(rest / pieces));
+    unsigned id = blockIdx.x;
+    Piece w;
+    w.kv = int(id & 1);
+    id >>= 1;
+    w.head = int(id % unsigned(p.c.heads));
+    id /= unsigned(p.c.heads);
+    const unsigned first = id % g.pieces;
+    const int shift = 31 - __builtin_clz(unsigned(p.c.block));
+    for (unsigned seq = id / g.pieces; seq < unsigned(p.b.seqs); seq += g.seqs) {
+        w.s = kv8_sequence(p.b, int(seq));
         if (w.s.n == 0) continue;
         const std::int64_t from = w.s.len - w.s.n > 0 ? w.s.len - w.s.n : 0;
-        for (w.page = from / p.c.block + first; w.page * p.c.block < w.s.len; w.page += pieces) body(w);
+        for (w.page = (from >> shift) + first; w.page << shift < w.s.len; w.page += g.pieces) body(w);
     }
 }
+
+// A work-group's threads over rows of dim / 8 pieces of 8 elements: each keeps
+// its piece and goes from row to row.
+struct Lanes {
+    int row, step, at;  // first row, rows between, first element
+    __device__ explicit Lanes(int dim)
+    {
+        const int per_row = dim / 8;
+        step = kThreads / per_row;
+        row = int(threadIdx.x) / per_row;
+        at = int(threadIdx.x) % per_row * 8;
+        if (row >= step) row = 1 << 30;  // threads left over
+    }
+};
+
+constexpr int kHeld = 4;  // pieces a thread has in flight
 
 // The largest |x| among the finite of eight elements, as bits.
 template <class T> __device__ inline std::uint32_t largest(const typename T::elem *x, std::uint32_t m)
@@ -100,29 +118,36 @@ template <class T> struct Eight {
     typename T::elem x[8];
 };
 
-template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(Kv8Problem p, unsigned pieces)
+template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(Kv8Problem p, Grid g)
 {
     typedef typename T::elem elem;
     __shared__ std::uint32_t wave_max[kThreads / 64];
-    const int dim = p.c.dim, block = p.c.block, per_row = dim / 8;
-    for_each_piece(p, pieces, [&](const Piece &w) {
+    const int dim = p.c.dim, block = p.c.block;
+    const Lanes lanes(dim);
+    for_each_piece(p, g, [&](const Piece &w) {
         const std::int64_t start = w.s.len - w.s.n;  // position of the sequence's first row (may be below 0)
         const std::int64_t t0 = w.page * block;
         const std::int64_t lo = start > t0 ? start : t0, hi = w.s.len < t0 + block ? w.s.len : t0 + block;
         const std::int64_t page = kv8_page(p.c, p.b, w.s.seq, w.page);
         if (page < 0) return;  // the same for the whole work-group
-        const int kept = int(lo - t0), fresh = int(hi - lo) * per_row;
-        const elem *src = static_cast<const elem *>(w.kv ? p.V : p.K) + w.head * (w.kv ? p.hsv : p.hsk);
-        const std::int64_t ld = w.kv ? p.ldv : p.ldk, row0 = w.s.row0 + (lo - start);
-        std::uint8_t *codes = static_cast<std::uint8_t *>(w.kv ? p.c.V : p.c.K) + (page * p.c.heads + w.head) * block * dim;
+        const int kept = int(lo - t0), fresh = int(hi - lo);
+        const std::int64_t ld = w.kv ? p.ldv : p.ldk;
+        const elem *src = static_cast<const elem *>(w.kv ? p.V : p.K) + (w.s.row0 + (lo - start)) * ld +
+                          w.head * (w.kv ? p.hsv : p.hsk) + lanes.at;
+        std::uint8_t *codes = static_cast<std::uint8_t *>(w.kv ? p.c.V : p.c.K) + (page * p.c.heads + w.head) * block * dim + lanes.at;
         float *scale = (w.kv ? p.c.Vs : p.c.Ks) + page * p.c.heads + w.head;
         const float before = kept > 0 ? *scale : 0.0f;
 
+        // The first pieces stay in registers; further ones are read again below.
+        Eight<T> held[kHeld];
         std::uint32_t m = 0;
-        for (int e = threadIdx.x; e < fresh; e += kThreads) {
-            const Eight<T> v = load_any<Eight<T>>(src + (row0 + e / per_row) * ld + e % per_row * 8);
-            m = largest<T>(v.x, m);
-        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (lanes.row + i * lanes.step < fresh) held[i] = load_any<Eight<T>>(src + (lanes.row + i * lanes.step) * ld);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (lanes.row + i * lanes.step < fresh) m = largest<T>(held[i].x, m);
+        for (int r = lanes.row + kHeld * lanes.step; r < fresh; r += lanes.step) m = largest<T>(load_any<Eight<T>>(src + r * ld).x, m);
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) {
             const std::uint32_t o = std::uint32_t(__shfl_xor(int(m), d));
@@ -138,8 +163,8 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(
         if (s != before) {
             // The page's earlier tokens, rounded to the risen scale.
             const float ratio = before * inverse;
-            for (int e = threadIdx.x; e < kept * per_row; e += kThreads) {
-                u32x2 *at = reinterpret_cast<u32x2 *>(codes + e * 8);
+            for (int r = lanes.row; r < kept; r += lanes.step) {
+                u32x2 *at = reinterpret_cast<u32x2 *>(codes + r * dim);
                 u32x2 v = *at;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -150,62 +175,72 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(
                 *at = v;
             }
         }
-        for (int e = threadIdx.x; e < fresh; e += kThreads) {
-            const Eight<T> v = load_any<Eight<T>>(src + (row0 + e / per_row) * ld + e % per_row * 8);
+        auto store = [&](const Eight<T> &v, int r) {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float a = to_f32<T>(v.x[i]);
                 x[i] = (f32_bits(a) & 0x7f800000u) == 0x7f800000u ? __builtin_nanf("") : a * inverse;
             }
-            *reinterpret_cast<u32x2 *>(codes + kept * dim + e * 8) =
-                u32x2{to_codes(x[0], x[1], x[2], x[3]), to_codes(x[4], x[5], x[6], x[7])};
-        }
+            *reinterpret_cast<u32x2 *>(codes + (kept + r) * dim) = u32x2{to_codes(x[0], x[1], x[2], x[3]), to_codes(x[4], x[5], x[6], x[7])};
+        };
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (lanes.row + i * lanes.step < fresh) store(held[i], lanes.row + i * lanes.step);
+        for (int r = lanes.row + kHeld * lanes.step; r < fresh; r += lanes.step) store(load_any<Eight<T>>(src + r * ld), r);
         __syncthreads();  // every thread has read the scale and wave_max
         if (threadIdx.x == 0) *scale = s;
     });
 }
 
-template <class T> __global__ __launch_bounds__(kThreads) void kv8_read_kernel(Kv8Problem p, unsigned pieces)
+template <class T> __global__ __launch_bounds__(kThreads) void kv8_read_kernel(Kv8Problem p, Grid g)
 {
     typedef typename T::elem elem;
-    const int dim = p.c.dim, block = p.c.block, per_row = dim / 8;
-    for_each_piece(p, pieces, [&](const Piece &w) {
+    const int dim = p.c.dim, block = p.c.block;
+    const Lanes lanes(dim);
+    for_each_piece(p, g, [&](const Piece &w) {
         const std::int64_t start = w.s.len - w.s.n, t0 = w.page * block;
         const std::int64_t lo = start > t0 ? start : t0, hi = w.s.len < t0 + block ? w.s.len : t0 + block;
         const std::int64_t page = kv8_page(p.c, p.b, w.s.seq, w.page);
-        const int count = int(hi - lo) * per_row;
-        elem *dst = static_cast<elem *>(w.kv ? p.V : p.K) + w.head * (w.kv ? p.hsv : p.hsk);
-        const std::int64_t ld = w.kv ? p.ldv : p.ldk, row0 = w.s.row0 + (lo - start);
+        const int count = int(hi - lo);
+        const std::int64_t ld = w.kv ? p.ldv : p.ldk;
+        elem *dst = static_cast<elem *>(w.kv ? p.V : p.K) + (w.s.row0 + (lo - start)) * ld + w.head * (w.kv ? p.hsv : p.hsk) + lanes.at;
+        // A page that is not the cache's is not read; its rows are NaN.
         const std::int64_t at = (page < 0 ? 0 : page) * p.c.heads + w.head;
-        const std::uint8_t *codes = static_cast<const std::uint8_t *>(w.kv ? p.c.V : p.c.K) + at * block * dim + (lo - t0) * dim;
+        const std::uint8_t *codes = static_cast<const std::uint8_t *>(w.kv ? p.c.V : p.c.K) + at * block * dim + (lo - t0) * dim + lanes.at;
         const float s = page < 0 ? __builtin_nanf("") : (w.kv ? p.c.Vs : p.c.Ks)[at];
-        for (int e = threadIdx.x; e < count; e += kThreads) {
-            u32x2 v = {0, 0};
-            if (page >= 0) v = *reinterpret_cast<const u32x2 *>(codes + e * 8);
-            Eight<T> out;
+        for (int r0 = lanes.row; r0 < count; r0 += kHeld * lanes.step) {
+            u32x2 v[kHeld];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[i]), false);
-                const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[i]), true);
-                out.x[4 * i] = from_f32<T>(a[0] * s);
-                out.x[4 * i + 1] = from_f32<T>(a[1] * s);
-                out.x[4 * i + 2] = from_f32<T>(b[0] * s);
-                out.x[4 * i + 3] = from_f32<T>(b[1] * s);
+            for (int j = 0; j < kHeld; ++j)
+                if (r0 + j * lanes.step < count) v[j] = *reinterpret_cast<const u32x2 *>(codes + (r0 + j * lanes.step) * dim);
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) {
+                if (r0 + j * lanes.step >= count) continue;
+                Eight<T> out;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[j][i]), false);
+                    const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(int(v[j][i]), true);
+                    out.x[4 * i] = from_f32<T>(a[0] * s);
+                    out.x[4 * i + 1] = from_f32<T>(a[1] * s);
+                    out.x[4 * i + 2] = from_f32<T>(b[0] * s);
+                    out.x[4 * i + 3] = from_f32<T>(b[1] * s);
+                }
+                __builtin_memcpy(dst + (r0 + j * lanes.step) * ld, &out, sizeof(out));
             }
-            __builtin_memcpy(dst + (row0 + e / per_row) * ld + e % per_row * 8, &out, sizeof(out));
         }
     });
 }
 
 template <class F> hipError_t launch(const Kv8Problem &p, F f32, F bf16, F f16, hipStream_t stream)
 {
-    const Grid g = grid_of(p);
     const F kernel = p.dtype == SGEMM_F32 ? f32 : p.dtype == SGEMM_LP_BF16 ? bf16 : f16;
     Kv8Problem q = p;
-    unsigned pieces = g.pieces;
-    void *args[] = {&q, &pieces};
-    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(g.groups), dim3(kThreads), args, 0, stream);
+    Grid g = grid_of(p);
+    void *args[] = {&q, &g};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(2u * unsigned(p.c.heads) * g.pieces * g.seqs), dim3(kThreads), args, 0,
+                           stream);
 }
 
 }  // namespace

@@ -56,12 +56,13 @@ __device__ inline float rounded_quotient(float x, float s, float inverse)
 }
 
 // LG lanes (a power of two) share one group and take eight k each in turn.
-template <class T, int LG, bool ZP>
-__global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, int groups, std::int64_t all)
+// Once: group == 8 LG, so that a lane's eight stay in registers between the
+// search for the extremes and the rounding. `all` groups, fewer than 2^31.
+template <class T, int LG, bool ZP, bool Once>
+__global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, unsigned groups, unsigned all)
 {
     const int part = threadIdx.x % LG;
-    for (std::int64_t id = std::int64_t(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG; id < all;
-         id += std::int64_t(gridDim.x) * (kThreads / LG)) {
+    for (unsigned id = blockIdx.x * (kThreads / LG) + threadIdx.x / LG; id < all; id += gridDim.x * (kThreads / LG)) {
         const std::int64_t n = id / groups;
         const int g = int(id % groups);
         const int k0 = g * p.group, k1 = p.K - k0 < p.group ? p.K : k0 + p.group;
@@ -76,6 +77,7 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
                 lo = __builtin_fminf(lo, x[i]);
                 hi = __builtin_fmaxf(hi, x[i]);
             }
+            if (Once) break;
         }
 #pragma unroll
         for (int d = LG / 2; d > 0; d /= 2) {
@@ -99,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
             if (ZP) p.Z[n * p.ldz + g] = std::uint8_t(z);
         }
         for (int k = k0 + 8 * part; k < k1; k += 8 * LG) {
-            load8<T>(row, k, k1, x);
+            if (!Once) load8<T>(row, k, k1, x);
             std::uint32_t w = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -114,51 +116,94 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
             } else {
                 for (int i = 0; k + 2 * i < k1; ++i) dst[i] = std::uint8_t(w >> (8 * i));
             }
+            if (Once) break;
         }
     }
 }
+
+constexpr int kEights = 4;  // eights of codes that a thread has in flight
 
 template <class T, bool ZP>
-__global__ __launch_bounds__(kThreads) void w4_dequantize_kernel(W4PackProblem p, int eights, std::int64_t all)
+__global__ __launch_bounds__(kThreads) void w4_dequantize_kernel(W4PackProblem p, unsigned eights, unsigned all)
 {
-    for (std::int64_t id = std::int64_t(blockIdx.x) * kThreads + threadIdx.x; id < all; id += std::int64_t(gridDim.x) * kThreads) {
-        const std::int64_t n = id / eights;
-        const int k = int(id % eights) * 8, g = k / p.group;
-        const std::uint8_t *src = p.W + n * p.ldw + k / 2;
-        const int rest = p.K - k;
-        std::uint32_t w = 0;
-        if (rest >= 7) {
-            w = load_any<std::uint32_t>(src);
-        } else {
-            for (int i = 0; 2 * i < rest; ++i) w |= std::uint32_t(src[i]) << (8 * i);
+    for (unsigned first = blockIdx.x * (kEights * kThreads) + threadIdx.x; first < all; first += gridDim.x * (kEights * kThreads)) {
+        std::uint32_t w[kEights];
+        float s[kEights];
+        int z[kEights], rest[kEights];
+        typename T::elem *dst[kEights];
+#pragma unroll
+        for (int j = 0; j < kEights; ++j) {
+            const unsigned id = first + j * kThreads < all ? first + j * kThreads : all - 1;  // past the last: that one again
+            const std::int64_t n = id / eights;
+            const int k = int(id % eights) * 8, g = int(unsigned(k) / unsigned(p.group));
+            const std::uint8_t *src = p.W + n * p.ldw + k / 2;
+            rest[j] = p.K - k;
+            if (rest[j] >= 7) {
+                w[j] = load_any<std::uint32_t>(src);
+            } else {
+                w[j] = 0;
+                for (int i = 0; 2 * i < rest[j]; ++i) w[j] |= std::uint32_t(src[i]) << (8 * i);
+            }
+            s[j] = load_scale(p.S, p.stype, n * p.lds + g);
+            z[j] = ZP ? p.Z[n * p.ldz + g] & 15 : 8;
+            dst[j] = static_cast<typename T::elem *>(p.B) + n * p.ldb + k;
         }
-        const float s = load_scale(p.S, p.stype, n * p.lds + g);
-        const int z = ZP ? p.Z[n * p.ldz + g] & 15 : 8;
-        Eight<T> v;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.x[i] = from_f32<T>(s * float(int((w >> (4 * i)) & 15u) - z));
-        typename T::elem *dst = static_cast<typename T::elem *>(p.B) + n * p.ldb + k;
-        if (rest >= 8) {
-            __builtin_memcpy(dst, &v, sizeof(v));
-        } else {
+        for (int j = 0; j < kEights; ++j) {
+            if (first + j * kThreads >= all) continue;
+            Eight<T> v;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < rest) dst[i] = v.x[i];
+            for (int i = 0; i < 8; ++i) v.x[i] = from_f32<T>(s[j] * float(int((w[j] >> (4 * i)) & 15u) - z[j]));
+            if (rest[j] >= 8) {
+                __builtin_memcpy(dst[j], &v, sizeof(v));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < rest[j]) dst[j][i] = v.x[i];
+            }
         }
     }
 }
 
-unsigned grid_for(std::int64_t groups) { return unsigned(groups < (1 << 22) ? groups : (1 << 22)); }
+// Runs launch(part) over bands of rows of fewer than 2^30 pieces each, `per_row`
+// of them a row.
+template <class Launch> hipError_t for_each_rows(const W4PackProblem &p, std::int64_t per_row, Launch &&launch)
+{
+    std::int64_t rows = (std::int64_t(1) << 30) / per_row;
+    rows = rows < 1 ? 1 : rows;
+    const int bsize = p.dtype == SGEMM_F32 ? 4 : 2, ssize = p.stype == SGEMM_F32 ? 4 : 2;
+    for (std::int64_t n0 = 0; n0 < p.N; n0 += rows) {
+        W4PackProblem q = p;
+        q.N = int(p.N - n0 < rows ? p.N - n0 : rows);
+        q.B = static_cast<char *>(p.B) + n0 * p.ldb * bsize;
+        q.W = p.W + n0 * p.ldw;
+        q.S = static_cast<char *>(p.S) + n0 * p.lds * ssize;
+        if (p.Z) q.Z = p.Z + n0 * p.ldz;
+        const hipError_t e = launch(q);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+unsigned grid_for(std::int64_t pieces, int each)
+{
+    const std::int64_t n = (pieces + each - 1) / each;
+    return unsigned(n < (1 << 22) ? n : (1 << 22));
+}
 
 template <class T, int LG> hipError_t quantize(const W4PackProblem &p, hipStream_t stream)
 {
-    int groups = (p.K + p.group - 1) / p.group;
-    std::int64_t all = std::int64_t(p.N) * groups;
-    W4PackProblem q = p;
-    void *args[] = {&q, &groups, &all};
-    const void *kernel = p.Z ? reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, true>)
-                             : reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, false>);
-    return hipLaunchKernel(kernel, dim3(grid_for((all + kThreads / LG - 1) / (kThreads / LG))), dim3(kThreads), args, 0, stream);
+    unsigned groups = unsigned((std::int64_t(p.K) + p.group - 1) / p.group);
+    const bool once = p.group == 8 * LG;
+    const void *kernel = p.Z ? once ? reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, true, true>)
+                                    : reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, true, false>)
+                         : once ? reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, false, true>)
+                                : reinterpret_cast<const void *>(&w4_quantize_kernel<T, LG, false, false>);
+    return for_each_rows(p, groups, [&](W4PackProblem &q) {
+        unsigned all = unsigned(q.N) * groups;
+        void *args[] = {&q, &groups, &all};
+        return hipLaunchKernel(kernel, dim3(grid_for(all, kThreads / LG)), dim3(kThreads), args, 0, stream);
+    });
 }
 
 template <class T> hipError_t quantize(const W4PackProblem &p, hipStream_t stream)
@@ -171,13 +216,14 @@ template <class T> hipError_t quantize(const W4PackProblem &p, hipStream_t strea
 
 template <class T> hipError_t dequantize(const W4PackProblem &p, hipStream_t stream)
 {
-    int eights = int((std::int64_t(p.K) + 7) / 8);
-    std::int64_t all = std::int64_t(p.N) * eights;
-    W4PackProblem q = p;
-    void *args[] = {&q, &eights, &all};
+    unsigned eights = unsigned((std::int64_t(p.K) + 7) / 8);
     const void *kernel = p.Z ? reinterpret_cast<const void *>(&w4_dequantize_kernel<T, true>)
                              : reinterpret_cast<const void *>(&w4_dequantize_kernel<T, false>);
-    return hipLaunchKernel(kernel, dim3(grid_for((all + kThreads - 1) / kThreads)), dim3(kThreads), args, 0, stream);
+    return for_each_rows(p, eights, [&](W4PackProblem &q) {
+        unsigned all = unsigned(q.N) * eights;
+        void *args[] = {&q, &eights, &all};
+        return hipLaunchKernel(kernel, dim3(grid_for(all, kEights * kThreads)), dim3(kThreads), args, 0, stream);
+    });
 }
 
 }  // namespace
