@@ -41,18 +41,28 @@ __device__ inline float store_scale(void *S, int stype, std::int64_t i, float s)
 }
 
 // round(x / s) with ties to even, as if the quotient were exact, for |x / s|
-// up to 16 or so: the float32 quotient may round onto or over a tie, so its
-// nearest integer is corrected by the exact remainder x - r s (one fused
-// multiply-add; next to a tie it is a multiple of x's or s's last place and
-// fits float32).
-__device__ inline float rounded_quotient(float x, float s, float inverse)
+// up to 32 or so, of N values: the float32 quotient may round onto or over a
+// tie, so its nearest integer r is held against the exact remainder x - r s
+// (one fused multiply-add; next to a tie it is a multiple of x's or s's last
+// place and fits float32). Only a remainder of half of s or more needs the
+// correction, which is rare and left to a branch.
+template <int N> __device__ inline void rounded_quotients(const float *x, float s, float inverse, float *r)
 {
-    float r = __builtin_rintf(x * inverse);
-    const float d = __builtin_fmaf(-r, s, x), half = 0.5f * s;
-    const bool odd = (int(r) & 1) != 0;
-    if (d > half || (d == half && odd)) r += 1.0f;
-    if (d < -half || (d == -half && odd)) r -= 1.0f;
-    return r;
+    const float half = 0.5f * s;
+    float d[N], worst = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        r[i] = __builtin_rintf(x[i] * inverse);
+        d[i] = __builtin_fmaf(-r[i], s, x[i]);
+        worst = __builtin_fmaxf(worst, __builtin_fabsf(d[i]));
+    }
+    if (worst < half) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool odd = (int(r[i]) & 1) != 0;
+        if (d[i] > half || (d[i] == half && odd)) r[i] += 1.0f;
+        else if (d[i] < -half || (d[i] == -half && odd)) r[i] -= 1.0f;
+    }
 }
 
 // LG lanes (a power of two) share one group and take eight k each in turn.
@@ -95,21 +105,25 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
         const float up = s < 0x1p-90f ? 0x1p90f : 1.0f, scale = s * up;
         const float inverse = flat ? 0.0f : 1.0f / scale;
         float z = 8.0f;
-        if (ZP && !flat) z = __builtin_fminf(rounded_quotient(-lo * up, scale, inverse), 15.0f);
+        if (ZP && !flat) {
+            const float low = -lo * up;
+            rounded_quotients<1>(&low, scale, inverse, &z);
+            z = __builtin_fminf(z, 15.0f);
+        }
         if (part == 0) {
             store_scale(p.S, p.stype, n * p.lds + g, s);
             if (ZP) p.Z[n * p.ldz + g] = std::uint8_t(z);
         }
         for (int k = k0 + 8 * part; k < k1; k += 8 * LG) {
             if (!Once) load8<T>(row, k, k1, x);
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = flat ? 0.0f : x[i] * up;
+            rounded_quotients<8>(x, scale, inverse, q);
             std::uint32_t w = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float q = z;
-                if (!flat) q += __builtin_fminf(__builtin_fmaxf(rounded_quotient(x[i] * up, scale, inverse), -15.0f), 15.0f);
-                q = __builtin_fminf(__builtin_fmaxf(q, 0.0f), 15.0f);
-                if (k + i < k1) w |= std::uint32_t(q) << (4 * i);
-            }
+            for (int i = 0; i < 8; ++i) w |= std::uint32_t(__builtin_amdgcn_fmed3f(flat ? 8.0f : q[i] + z, 0.0f, 15.0f)) << (4 * i);
+            if (k + 8 > k1) w &= (1u << (4 * (k1 - k))) - 1u;  // past the row's end: 0
             std::uint8_t *dst = p.W + n * p.ldw + k / 2;
             if (k + 8 <= k1) {
                 __builtin_memcpy(dst, &w, 4);
