@@ -149,20 +149,21 @@ __device__ inline void split_weights(const float *w, Frag &hi, Frag &mid, Frag &
 __device__ inline float rescale(float m, float top) { return m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top); }
 
 // What the rows of one tile see: row `row` of a sequence (row / R th new row,
-// query head row % R of the group) sees `count` tokens from `from` on.
+// query head row % R of the group) sees `count` tokens from `from` on, of
+// those that the table can name (from + count <= nameable).
 struct Kv8Seen {
     std::int64_t first, len, nameable;  // position of new row 0, tokens, tokens that the table can name
     int R, causal, window;
+    __device__ std::int64_t behind(std::int64_t row) const { return causal ? first + row / R + 1 : len; }
     __device__ void operator()(std::int64_t row, int &from, int &count) const
     {
-        const std::int64_t pos = first + row / R;
-        std::int64_t hi = causal ? pos + 1 : len, lo = window > 0 ? pos + 1 - window : 0;
-        if (hi > nameable) hi = nameable;
-        lo = lo < 0 ? 0 : lo;
-        hi = hi < lo ? lo : hi;
+        const std::int64_t end = behind(row), begin = window > 0 ? end - window : 0;
+        const std::int64_t hi = end < 0 ? 0 : end < nameable ? end : nameable, lo = begin < 0 ? 0 : begin < hi ? begin : hi;
         from = int(lo);
         count = int(hi - lo);
     }
+    // The last token seen lies behind the table's last column: the row is NaN.
+    __device__ bool beyond(std::int64_t row) const { return behind(row) > nameable; }
 };
 
 // Waves a SIMD has registers for: two, but for the longest heads and for two
@@ -210,10 +211,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
     for (unsigned seq = id / unsigned(p.c.heads); seq < unsigned(p.b.seqs); seq += seqs_at_once) {
         const Kv8Sequence s = kv8_sequence(p.b, int(seq));
         const std::int64_t all_rows = s.n * R;
-        // Tokens the table cannot name: every row of the sequence is NaN.
-        const std::int64_t nameable = std::int64_t(p.b.table_ld) << shift;
-        const bool short_table = s.len > nameable;
-        const Kv8Seen seen{s.len - s.n, s.len, nameable, R, p.causal, p.window};
+        const Kv8Seen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, R, p.causal, p.window};
         const int *const table = p.b.table + std::int64_t(seq) * p.b.table_ld;
         for (std::int64_t tile = tile0;; tile += p.plan.tiles) {
             const std::int64_t row0 = Rows ? (tile * kAttendWaves + wave) * kRows : tile * kRows;
@@ -240,8 +238,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
             seen(row0, first_lo, first_n);
             seen(row0 + kRows < all_rows ? row0 + kRows - 1 : all_rows - 1, last_lo, last_n);
             // Turns of 32 tokens: begin .. end sees some row; inner .. outer every row in full.
-            int begin = first_lo >> 5, end = (last_lo + last_n + 31) >> 5, inner = (last_lo + 31) >> 5, outer = (first_lo + first_n) >> 5;
+            // (Positions reach 2^31 - 1, so that rounding up needs the sign bit.)
             const int limit = last_lo + last_n;
+            int begin = first_lo >> 5, end = int((unsigned(limit) + 31u) >> 5);
+            const int inner = int((unsigned(last_lo) + 31u) >> 5), outer = (first_lo + first_n) >> 5;
             if (!whole) {
                 const int turns = end - begin, b = begin;
                 begin = b + int(std::int64_t(turns) * split / p.plan.splits);
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                     const std::int64_t row = row0 + 16 * t + c;
                     if (row >= all_rows) continue;
                     float inverse = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
-                    if (short_table) inverse = __builtin_nanf("");
+                    if (seen.beyond(row)) inverse = __builtin_nanf("");
                     float *dst = p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + kq * 8 * DC;
 #pragma unroll
                     for (int x = 0; x < 4 * kDTiles; x += 4) {
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                 if (whole) {
                     const std::int64_t row = row0 + i;
                     x = sum == 0.0f ? f32x4{0, 0, 0, 0} : x / sum;
-                    if (short_table) x = x * __builtin_nanf("");
+                    if (seen.beyond(row)) x = x * __builtin_nanf("");
                     __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + d, &x, sizeof(x));
                 } else {
                     const std::int64_t at = (((std::int64_t(seq) * p.c.heads + head) * p.plan.tiles + tile) * p.plan.splits + split) * kRows + i;
@@ -524,7 +524,8 @@ template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Atte
     for (; x < splits; ++x) y += *reinterpret_cast<const f32x4 *>(at + x * pitch) * __shfl(a, x);
     if (4 * lane >= dim) return;
     y = sum == 0.0f ? f32x4{0, 0, 0, 0} : y / sum;
-    if (s.len > std::int64_t(p.b.table_ld) * p.c.block) y = y * __builtin_nanf("");
+    const Kv8Seen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) * p.c.block, R, p.causal, p.window};
+    if (seen.beyond(row)) y = y * __builtin_nanf("");
     __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + 4 * lane, &y, sizeof(y));
 }
 

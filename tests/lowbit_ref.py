@@ -157,14 +157,14 @@ class Cache:
             n, length = max(0, end - first), max(0, int(lens[b]))
             if n == 0:
                 continue
-            cut = length > table.shape[1] * self.block
-            K, V = (self.tokens(table, b, length, i) for i in range(2)) if not cut else (None, None)
+            named = table.shape[1] * self.block  # a row that sees a token behind them is NaN
+            K, V = (self.tokens(table, b, min(length, named), i) for i in range(2))
             for i in range(n):
                 p = length - n + i
                 hi = min(length, p + 1) if causal else length
                 lo = max(0, p + 1 - window) if window else 0
                 for h in range(heads_q):
-                    if cut:
+                    if hi > named:
                         continue  # NaN
                     if hi <= lo:
                         O[first + i, h] = 0.0

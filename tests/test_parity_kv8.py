@@ -286,3 +286,53 @@ def test_two_runs_are_the_same():
     first = sg.kv8_attend(Q, cache, *args, max_new=2)
     for _ in range(3):
         assert torch.equal(sg.kv8_attend(Q, cache, *args, max_new=2), first)
+
+
+@pytest.mark.parametrize("ratio,columns", [(1, 1), (1, 2), (2, 3), (70, 3), (70, 4), (3, 7)])
+@pytest.mark.parametrize("window", [0, 5, 40])
+def test_rows_past_a_short_table(window, ratio, columns):
+    # Lengths behind the table's last column: rows that see only its tokens are
+    # as ever, the others NaN, rows before token 0 zero; nothing behind is read.
+    block, dim = 16, 64
+    case = Case(12, [16 * columns] * 4, [9, 3, 8, 2], 1, block, dim)
+    case.lens = np.array([16 * columns + 3, 16 * columns + 200, 6, 2**31 - 1], np.int32)
+    cache, args = case.device(), case.args()
+    Q = case.normal(ratio, "bf16")
+    for max_new in (1, 9):
+        O, bound = case.ref.attend(Q.double().numpy(), case.table, case.lens, case.starts, 0.2, True, window)
+        assert np.isfinite(O[:6]).all() and np.isnan(O[6:12]).all() and (O[12:14] == 0).all() and np.isnan(O[20:]).all()
+        got = sg.kv8_attend(Q.cuda(), cache, *args, scale=0.2, window=window, max_new=max_new).cpu().double().numpy()
+        close(got, O, bound, f"columns {columns} window {window} max_new {max_new}")
+
+
+def test_splits_past_a_short_table():
+    # The same where sequences are split over work-groups and joined.
+    case = Case(13, [4096, 4096], [4, 3], 1, 64, 128)
+    case.lens = np.array([4098, 5000], np.int32)
+    cache, args = case.device(), case.args()
+    Q = case.normal(2, "bf16")
+    for window in (0, 100, 3000):
+        O, bound = case.ref.attend(Q.double().numpy(), case.table, case.lens, case.starts, 0.2, True, window)
+        assert np.isfinite(O[:2]).all() and np.isnan(O[2:]).all()
+        close(sg.kv8_attend(Q.cuda(), cache, *args, scale=0.2, window=window, max_new=4).cpu().double().numpy(), O, bound, f"window {window}")
+
+
+def test_positions_up_to_31_bits():
+    # The last tokens of a sequence of 2^31 - 1, whose table repeats a few pages, through a window.
+    block, dim, n, window = 1024, 16, 20, 50
+    case = Case(14, [2 * block - 1], [n], 1, block, dim, spare=0)
+    cache = case.device()
+    K, V, Q = (case.normal(1, "f32") for _ in range(3))
+    case.ref.write([K.double().numpy(), V.double().numpy()], case.table, case.lens, case.starts)
+    O, bound = case.ref.attend(Q.double().numpy(), case.table, case.lens, case.starts, 0.3, True, window)
+    table = torch.full((1, 2**21), -1, dtype=torch.int32)
+    table[0, -2:] = torch.from_numpy(case.table[0])
+    args = [table.cuda(), torch.tensor([2**31 - 1], dtype=torch.int32).cuda(), torch.from_numpy(case.starts).cuda()]
+    sg.kv8_write(cache, K.cuda(), V.cuda(), *args)
+    same_cache(cache, case.ref, "last tokens")
+    for max_new in (1, n):
+        got = sg.kv8_attend(Q.cuda(), cache, *args, scale=0.3, window=window, max_new=max_new).cpu().double().numpy()
+        close(got, O, bound, f"last tokens, max_new {max_new}")
+    outs = sg.kv8_read(cache, *args, rows=n)
+    for i in range(2):
+        assert np.array_equal(outs[i].cpu().double().numpy(), case.ref.tokens(case.table, 0, 2 * block - 1, i)[-n:])
