@@ -263,7 +263,8 @@ template <> struct ScaleSet<AnyType, 1> {
     }
 };
 
-// As Groups; past K (the last slab) the last group's stand in, A being 0 there.
+// As Groups; past K (the last slab) scales are 0, as A is (a last group's
+// infinite scale would make NaN of it).
 template <int GS, int N, bool ZP, bool Run> struct AnyGroups {
     static constexpr int kSets = Run ? 1 : N, kPer = Run ? N : 1;
     ScaleSet<AnyType, kPer> s[kSets];
@@ -284,10 +285,11 @@ template <int GS, int N, bool ZP, bool Run> struct AnyGroups {
         std::uint8_t zz[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int k = k0 + 32 * GS * i < p.K ? k0 + 32 * GS * i : p.K - 1;
+            const bool past = k0 + 32 * GS * i >= p.K;
+            const int k = past ? p.K - 1 : k0 + 32 * GS * i;
             ScaleSet<AnyType, 1> one;
             one.load(p.S, srow + k / p.group, f32);
-            a[i] = one.a, b[i] = one.b;
+            a[i] = past ? 0 : one.a, b[i] = past ? 0 : one.b;
             zz[i] = ZP ? zrow[k / p.group] : 0;
         }
         if constexpr (Run && N > 1) {

@@ -154,6 +154,18 @@ def test_infinities_nan_and_zero_groups(M, zeros, dtype):
     assert np.isnan(C[1]).all() and np.isfinite(C[2:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M", [4, 40])
+def test_infinite_and_nan_scales_of_a_short_last_group(M, dtype):
+    # K ends 8 into its last group (and inside a slab of 128): only real products see its scale.
+    A, W, dense = operands(10, M, 40, 136, 32, dtype, "f32", False)
+    W.codes[:, -4:] = 0x99
+    W.scales[0, -1], W.scales[1, -1] = float("inf"), float("nan")
+    A[:, -8:] = A[:, -8:].abs() + 1
+    C = sg.gemm_w4(A.cuda(), W).cpu()
+    assert (C[:, 0] == float("inf")).all() and torch.isnan(C[:, 1]).all() and torch.isfinite(C[:, 2:]).all()
+
+
 def test_two_runs_are_the_same():
     for M in (1, 9, 77, 300):
         A, W, _ = operands(M, M, 333, 2000, 64, "bf16", "bf16", True)
