@@ -38,6 +38,10 @@ bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi 
 
 i64 groups_of(int K, int group) { return (i64(K) + group - 1) / group; }
 
+// Limits that keep the kernels' indexes (k + a few hundred; work-items of a
+// launch) in 32 bits.
+constexpr int kMostK = 1 << 30, kMostHeads = 1 << 16;
+
 int check_group(int group) { return group <= 0 || group % 32 != 0 ? SGEMM_ERR_GROUP : SGEMM_OK; }
 
 // Leading dimensions of the W4 form itself.
@@ -52,7 +56,7 @@ bool aligned16(const void *p) { return reinterpret_cast<std::uintptr_t>(p) % 16 
 int check_cache_batch(const sgemm_kv8_cache *c, const sgemm_kv8_batch *b)
 {
     if (c == nullptr || b == nullptr) return SGEMM_ERR_NULL;
-    if (c->pages < 1 || c->heads < 1 || b->seqs < 0 || b->table_ld < 0 || b->rows < 0 || b->max_new < 0) return SGEMM_ERR_DIM;
+    if (c->pages < 1 || c->heads < 1 || c->heads > kMostHeads || b->seqs < 0 || b->table_ld < 0 || b->rows < 0 || b->max_new < 0) return SGEMM_ERR_DIM;
     const bool power = c->block >= 16 && c->block <= 1024 && (c->block & (c->block - 1)) == 0;
     if (!power || c->dim < 16 || c->dim > 256 || c->dim % 16 != 0) return SGEMM_ERR_CACHE;
     if (!aligned16(c->K) || !aligned16(c->V)) return SGEMM_ERR_CACHE;
@@ -102,7 +106,7 @@ extern "C" int sgemm_w4_check_args(int dtype, int stype, int M, int N, int K, in
 {
     (void)beta;
     if (!known_type(dtype) || !known_type(stype)) return SGEMM_ERR_DTYPE;
-    if (M < 0 || N < 0 || K < 0) return SGEMM_ERR_DIM;
+    if (M < 0 || N < 0 || K < 0 || K > kMostK) return SGEMM_ERR_DIM;
     if (check_group(group) != SGEMM_OK) return SGEMM_ERR_GROUP;
     if (lda < at_least_1(K) || !w4_ld_ok(K, group, ldw, lds, Z, ldz) || ldc < at_least_1(N)) return SGEMM_ERR_LD;
     if (M == 0 || N == 0) return SGEMM_OK;
@@ -123,7 +127,7 @@ extern "C" int sgemm_w4_pack_check_args(int dtype, int stype, int N, int K, int 
                                         const unsigned char *Z, int ldz)
 {
     if (!known_type(dtype) || !known_type(stype)) return SGEMM_ERR_DTYPE;
-    if (N < 0 || K < 0) return SGEMM_ERR_DIM;
+    if (N < 0 || K < 0 || K > kMostK) return SGEMM_ERR_DIM;
     if (check_group(group) != SGEMM_OK) return SGEMM_ERR_GROUP;
     if (ldb < at_least_1(K) || !w4_ld_ok(K, group, ldw, lds, Z, ldz)) return SGEMM_ERR_LD;
     if (N == 0 || K == 0) return SGEMM_OK;

@@ -365,7 +365,8 @@ int sgemm_lp_check_args(int dtype, int transA, int transB, int M, int N, int K,
  * three bf16 parts that add up to them exactly.
  *
  * The W4 form of an N x K matrix W, in groups of `group` k of a row (a
- * positive multiple of 32; the last group of a row may be shorter):
+ * positive multiple of 32; the last group of a row may be shorter; K at most
+ * 2^30):
  *
  *     W[n][k] = S[n][k / group] * (q[n][k] - z)
  *
@@ -388,8 +389,14 @@ int sgemm_lp_check_args(int dtype, int transA, int transB, int M, int N, int K,
  * ceil(K / 2)); lds and, with zeros, ldz >= max(1, ceil(K / group)); ldc >=
  * max(1, N)), then (only if M > 0 and N > 0) NULL C and, when A and W are
  * read (K > 0 and alpha != 0), NULL A, W or S and overlap of C with A, W, S
- * or Z. beta == 0 never reads C. One kernel is enqueued; nothing is
- * allocated. The result is the same on every run.
+ * or Z. beta == 0 never reads C. One kernel is enqueued (several for more
+ * columns or rows than one launch takes, from 131072 on); nothing is
+ * allocated. The result is the same on every run, and within 1e-5 * (|alpha|
+ * sum_k |A[m][k]| |W[n][k]| + |beta c|) + 1e-6 of the exact value. A group's
+ * products with the whole numbers q - z are summed before its scale
+ * multiplies them, so that sum |A[m][k] (q - z)| over a group has to stay
+ * within float32's range, and float32 elements of A below 2^-110 may lose
+ * bits.
  */
 int sgemm_w4(int dtype, int stype, int M, int N, int K, int group,
              float alpha,
@@ -461,7 +468,7 @@ typedef struct sgemm_kv8_cache {
     void *K, *V;     /* pages x heads x block x dim codes, 16-byte aligned      */
     float *Ks, *Vs;  /* pages x heads scales                                    */
     int pages;       /* >= 1                                                    */
-    int heads;       /* >= 1                                                    */
+    int heads;       /* 1 to 65536                                              */
     int block;       /* tokens of a page: a power of two from 16 to 1024        */
     int dim;         /* components of a head: a multiple of 16 from 16 to 256   */
 } sgemm_kv8_cache;

@@ -34,7 +34,8 @@ W4_CASES = [
     (w4(K=0, A=None, W=None, S=None), sg.SGEMM_OK), (w4(alpha=0.0, A=None, W=None, S=None), sg.SGEMM_OK),
     (w4(C=A + 4 * 399), sg.SGEMM_ERR_ALIAS), (w4(C=A + 4 * 400), sg.SGEMM_OK), (w4(C=W + 296), sg.SGEMM_ERR_ALIAS),
     (w4(C=S + 92), sg.SGEMM_ERR_ALIAS), (w4(C=Z + 20), sg.SGEMM_ERR_ALIAS), (w4(C=Z + 24), sg.SGEMM_OK),
-    (w4(M=2**31 - 1, N=2**31 - 1, K=2**31 - 1, lda=2**31 - 1, ldw=2**31 - 1, lds=2**31 - 1, ldz=2**31 - 1, ldc=2**31 - 1), sg.SGEMM_ERR_ALIAS),
+    (w4(K=2**30 + 1, lda=2**31 - 1, ldw=2**31 - 1, lds=2**31 - 1, ldz=2**31 - 1), sg.SGEMM_ERR_DIM),
+    (w4(M=2**31 - 1, N=2**31 - 1, K=2**30, lda=2**31 - 1, ldw=2**31 - 1, lds=2**31 - 1, ldz=2**31 - 1, ldc=2**31 - 1), sg.SGEMM_ERR_ALIAS),
 ]
 
 
@@ -51,6 +52,7 @@ def pack(dtype=F, stype=F, N=6, K=100, group=32, B=A, ldb=100, W=W, ldw=50, S=S,
 
 PACK_CASES = [
     (pack(), sg.SGEMM_OK), (pack(dtype=9), sg.SGEMM_ERR_DTYPE), (pack(N=-1), sg.SGEMM_ERR_DIM), (pack(K=-1), sg.SGEMM_ERR_DIM),
+    (pack(K=2**30 + 1, ldb=2**31 - 1, ldw=2**31 - 1, lds=2**31 - 1, ldz=2**31 - 1), sg.SGEMM_ERR_DIM),
     (pack(group=31), sg.SGEMM_ERR_GROUP), (pack(ldb=99), sg.SGEMM_ERR_LD), (pack(ldw=49), sg.SGEMM_ERR_LD),
     (pack(lds=3), sg.SGEMM_ERR_LD), (pack(ldz=3), sg.SGEMM_ERR_LD), (pack(Z=None, ldz=0), sg.SGEMM_OK),
     (pack(N=0, B=None, W=None, S=None), sg.SGEMM_OK), (pack(K=0, B=None, W=None, S=None), sg.SGEMM_OK),
@@ -82,7 +84,7 @@ def batch(table=TAB, lens=LEN, starts=ST, seqs=3, table_ld=4, rows=5, max_new=2)
 CACHE_CASES = [
     (cache(), batch(), sg.SGEMM_OK),
     (cache(pages=0), batch(), sg.SGEMM_ERR_DIM), (cache(heads=0), batch(), sg.SGEMM_ERR_DIM),
-    (cache(), batch(seqs=-1), sg.SGEMM_ERR_DIM), (cache(), batch(table_ld=-1), sg.SGEMM_ERR_DIM),
+    (cache(heads=65537), batch(), sg.SGEMM_ERR_DIM), (cache(), batch(seqs=-1), sg.SGEMM_ERR_DIM), (cache(), batch(table_ld=-1), sg.SGEMM_ERR_DIM),
     (cache(), batch(rows=-1), sg.SGEMM_ERR_DIM), (cache(), batch(max_new=-1), sg.SGEMM_ERR_DIM),
     (cache(block=8), batch(), sg.SGEMM_ERR_CACHE), (cache(block=48), batch(), sg.SGEMM_ERR_CACHE), (cache(block=2048), batch(), sg.SGEMM_ERR_CACHE),
     (cache(dim=0), batch(), sg.SGEMM_ERR_CACHE), (cache(dim=72), batch(), sg.SGEMM_ERR_CACHE), (cache(dim=272), batch(), sg.SGEMM_ERR_CACHE),
