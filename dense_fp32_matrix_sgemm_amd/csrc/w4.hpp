@@ -26,7 +26,8 @@
 namespace sgemm_impl {
 namespace {
 
-constexpr int kW4Chunk = 128;  // k that a wave takes at a time: 16 bytes of codes a lane
+constexpr int kW4Chunk = 128;    // k that a wave takes at a time: 16 bytes of codes a lane
+constexpr int kRowsWaves = 16;   // waves of a work-group of the rows kernel at most
 
 // (x & m) | c in one v_and_or_b32: with two constants that takes one of them
 // in a vector register, which the compiler does not do by itself.
@@ -313,222 +314,179 @@ template <int GS, int N, bool ZP, bool Run> struct AnyGroups {
 };
 
 // What a wave loads for U chunks of k.
-template <class ST, int NT, int GS, int U, bool ZP, bool Run> struct W4Stage {
-    u32x4 w[U][NT];
-    Groups<ST, GS, 4 * U / GS, ZP, Run> g[NT];
+template <class ST, int GS, int U, bool ZP, bool Run> struct W4Stage {
+    u32x4 w[U];
+    Groups<ST, GS, 4 * U / GS, ZP, Run> g;
 };
 
 // How a product is laid out over work-groups (launch_rows).
 struct W4Layout {
     int wn, wk;  // waves along N and along K
     int slabs;   // runs of K whose A is held in LDS, one after the other
-    int rows;    // rows of A held, at most 16 MT
     int pitch;   // bytes from one held row to the next: 16 more than a multiple of 128, so that 16 rows meet in no bank
 };
 
-// One work-group: 16 MT rows of C by 16 NT wn columns. A slab of A's rows
-// lies in LDS as matrix operands, read by every wave; the codes go from
-// memory to registers once: each wave takes a run of the slab's k for its 16
-// NT columns in steps of U chunks of 128, each lane 16 bytes of one column's
-// codes per chunk. The wk waves of a column tile add their sums through LDS
-// in their order, so the result does not depend on timing. GS: steps of 32 k
-// that share a scale.
-template <class T, class ST, int MT, int NT, int GS, bool ZP, int U, bool Short, bool Run, int MaxWaves>
-__global__ __launch_bounds__(64 * MaxWaves) void w4_rows_kernel(W4Problem p, W4Layout l)
+// Up to 16 rows of A. One work-group: all rows of C by 16 wn columns. A slab
+// of A's rows lies in LDS as matrix operands, read by every wave; the codes
+// go from memory to registers once: each wave takes a run of the slab's k for
+// its 16 columns in steps of U chunks of 128, each lane 16 bytes of one
+// column's codes per chunk. The wk waves of a column tile add their sums
+// through LDS in their order, so the result does not depend on timing. GS:
+// steps of 32 k that share a scale.
+//
+// Memory bounds it: 1 row of bf16 by 16384 x 4096 with zero points (35 MB)
+// takes 12.4 us on the device, 2.8 TB/s; 8 rows by 8192 x 8192 17.0. Of the
+// 12.4 us the loads alone take 8.7 and A's way to LDS 1, neither of which
+// more loads in flight shortened (A or codes, one to three steps further
+// ahead: 13.9 to 16.7 us).
+template <class T, class ST, int GS, bool ZP, int U, bool Short, bool Run>
+__global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W4Layout l)
 {
     extern __shared__ __align__(16) char lds[];  // A: [plane][row][k] as 16-bit operands
     typedef typename T::elem elem;
-    typedef W4Stage<ST, NT, GS, U, ZP, Run> Stage;
+    typedef W4Stage<ST, GS, U, ZP, Run> Stage;
     typedef AOperand<T> Operand;
     typedef Codes<T, ZP> Code;
     constexpr int kStep = kW4Chunk * U, kPlanes = Operand::kPlanes;
-    float *const part = reinterpret_cast<float *>(lds);  // then the sums: [wave][16 MT][16 NT]
+    float *const part = reinterpret_cast<float *>(lds);  // then the sums: [wave][row][column]
     const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wk = wave % l.wk, wn = wave / l.wk, cols = 16 * NT * l.wn;
-    const std::int64_t c0 = std::int64_t(blockIdx.x) * cols, n0 = c0 + wn * (16 * NT);
+    const int wk = wave % l.wk, wn = wave / l.wk, cols = 16 * l.wn, rows = p.M;
+    const std::int64_t c0 = std::int64_t(blockIdx.x) * cols;
     const int bytes = p.K / 2 + p.K % 2;
 
-    const std::uint8_t *wrow[NT], *zrow[NT];
-    std::int64_t srow[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        // Columns past the last read it again; their sums are not stored.
-        const std::int64_t n = n0 + 16 * t + c < p.N ? n0 + 16 * t + c : p.N - 1;
-        wrow[t] = p.W + n * p.ldw;
-        srow[t] = n * p.lds;
-        zrow[t] = ZP ? p.Z + n * p.ldz : nullptr;
-    }
+    // Columns past the last read it again; their sums are not stored.
+    const std::int64_t n = c0 + wn * 16 + c < p.N ? c0 + wn * 16 + c : p.N - 1, srow = n * p.lds;
+    const std::uint8_t *const wrow = p.W + n * p.ldw, *const zrow = ZP ? p.Z + n * p.ldz : nullptr;
 
     auto load = [&](Stage &st, unsigned k0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) st.w[u][t] = load_any<u32x4>(wrow[t] + (k0 / 2 + 64 * u + 16 * kq));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) st.g[t].load(p.S, srow[t], zrow[t], k0, p.group);
+        for (int u = 0; u < U; ++u) st.w[u] = load_any<u32x4>(wrow + (k0 / 2 + 64 * u + 16 * kq));
+        st.g.load(p.S, srow, zrow, k0, p.group);
     };
 
-    for (std::int64_t m0 = std::int64_t(blockIdx.y) * (16 * MT); m0 < p.M; m0 += std::int64_t(gridDim.y) * (16 * MT)) {
-        const int rows = p.M - m0 < l.rows ? int(p.M - m0) : l.rows;
-        const char *arow[kPlanes][MT];  // rows past the last repeat it; their sums are not stored
+    const char *arow[kPlanes];  // rows past the last repeat it; their sums are not stored
 #pragma unroll
-        for (int f = 0; f < kPlanes; ++f)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) arow[f][i] = lds + (f * l.rows + (16 * i + c < rows ? 16 * i + c : rows - 1)) * l.pitch + 16 * kq;
-        f32x4 out[MT][NT] = {};
+    for (int f = 0; f < kPlanes; ++f) arow[f] = lds + (f * rows + (c < rows ? c : rows - 1)) * l.pitch + 16 * kq;
+    f32x4 out = {0, 0, 0, 0};
 
-        auto operand = [&](int k, int i) {  // A's operand of the step of 32 that starts at k of the slab
+    auto operand = [&](int k) {  // A's operand of the step of 32 that starts at k of the slab
+        Operand a;
+#pragma unroll
+        for (int f = 0; f < kPlanes; ++f) a.f[f].v = *reinterpret_cast<const u32x4 *>(arow[f] + 2 * k);
+        return a;
+    };
+    auto multiply = [&](const Stage &st, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const u32x4 w = steps_of_codes(st.w[u]);
+#pragma unroll
+            for (int g = 0; g < 4 / GS; ++g) {
+                const int run = u * (4 / GS) + g;
+                f32x4 acc;
+#pragma unroll
+                for (int s = 0; s < GS; ++s) {
+                    const Frag wf = Code(st.g.zero(run))(w[g * GS + s]);
+                    acc = operand(k0 + 128 * u + 32 * (g * GS + s)).times(wf, s == 0 ? f32x4{0, 0, 0, 0} : acc);
+                }
+                const float s = st.g.scale(run) * Code::kUnit;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) out[r] += s * acc[r];
+            }
+        }
+    };
+
+    // Slabs share K's whole steps evenly; the last has the rest of K as well.
+    const int k_steps = p.K / kStep, base = k_steps / l.slabs, extra = k_steps % l.slabs;
+    int slab0 = 0;
+    for (int j = 0; j < l.slabs; ++j) {
+        const int all = Short ? 0 : base + (j < extra), slab_k = j + 1 < l.slabs ? all * kStep : p.K - slab0;
+        // This wave's run of the slab's whole steps: at least one unless
+        // Short. The first loads are on their way while A goes to LDS.
+        const int s0 = wk * all / l.wk, steps = (wk + 1) * all / l.wk - s0;
+        Stage st;
+        if constexpr (!Short) load(st, slab0 + s0 * kStep);
+
+        if (j > 0) __syncthreads();  // the last slab has been read
+        const int eights = (slab_k + 31) / 32 * 4;
+        for (int e = threadIdx.x; e < rows * eights; e += blockDim.x) {
+            const int r = e / eights, at = e % eights;
+            elem x[8];
+            load_a<T>(static_cast<const elem *>(p.A) + r * p.lda + slab0, 8 * at, slab_k, x);
             Operand a;
+            a.set(x);
 #pragma unroll
-            for (int f = 0; f < kPlanes; ++f) a.f[f].v = *reinterpret_cast<const u32x4 *>(arow[f][i] + 2 * k);
-            return a;
-        };
-        auto multiply = [&](const Stage &st, int k0) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                u32x4 w[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) w[t] = steps_of_codes(st.w[u][t]);
-#pragma unroll
-                for (int g = 0; g < 4 / GS; ++g) {
-                    const int run = u * (4 / GS) + g;
-                    f32x4 acc[MT][NT];
-#pragma unroll
-                    for (int s = 0; s < GS; ++s) {
-                        Frag wf[NT];
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) wf[t] = Code(st.g[t].zero(run))(w[t][g * GS + s]);
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            const Operand a = operand(k0 + 128 * u + 32 * (g * GS + s), i);
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) acc[i][t] = a.times(wf[t], s == 0 ? f32x4{0, 0, 0, 0} : acc[i][t]);
-                        }
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const float s = st.g[t].scale(run) * Code::kUnit;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) out[i][t][r] += s * acc[i][t][r];
-                    }
-                }
-            }
-        };
-
-        // Slabs share K's whole steps evenly; the last has the rest of K as well.
-        const int k_steps = p.K / kStep, base = k_steps / l.slabs, extra = k_steps % l.slabs;
-        int slab0 = 0;
-        for (int j = 0; j < l.slabs; ++j) {
-            const int all = Short ? 0 : base + (j < extra), slab_k = j + 1 < l.slabs ? all * kStep : p.K - slab0;
-            // This wave's run of the slab's whole steps: at least one unless
-            // Short. The first loads are on their way while A goes to LDS.
-            const int s0 = wk * all / l.wk, steps = (wk + 1) * all / l.wk - s0;
-            Stage st;
-            if constexpr (!Short) load(st, slab0 + s0 * kStep);
-
-            if (j > 0 || m0 >= 16 * MT) __syncthreads();  // the last slab (or sums) in LDS has been read
-            const int eights = (slab_k + 31) / 32 * 4;
-            for (int e = threadIdx.x; e < rows * eights; e += blockDim.x) {
-                const int r = e / eights, at = e % eights;
-                elem x[8];
-                load_a<T>(static_cast<const elem *>(p.A) + (m0 + r) * p.lda + slab0, 8 * at, slab_k, x);
-                Operand a;
-                a.set(x);
-#pragma unroll
-                for (int f = 0; f < kPlanes; ++f) *reinterpret_cast<u32x4 *>(lds + (f * l.rows + r) * l.pitch + 16 * at) = a.f[f].v;
-            }
-            __syncthreads();
-
-            if constexpr (!Short) {
-                for (int i = 0; i + 1 < steps; ++i) {
-                    multiply(st, (s0 + i) * kStep);
-                    load(st, slab0 + (s0 + i + 1) * kStep);
-                }
-                multiply(st, (s0 + steps - 1) * kStep);
-            }
-            // What is left of the slab, 32 k at a time in turns, the codes
-            // guarded (A is 0 past K).
-            for (int k0 = all * kStep + 32 * wk; k0 < slab_k; k0 += 32 * l.wk) {
-                const int group = (slab0 + k0) / p.group, at = (slab0 + k0) / 2 + 4 * kq;
-                Frag wf[NT];
-                float s[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    std::uint32_t w = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w |= at + i < bytes ? std::uint32_t(wrow[t][at + i]) << (8 * i) : 0u;
-                    wf[t] = Code(ZP ? zrow[t][group] & 15u : 8u)(w);
-                    s[t] = to_f32<ST>(static_cast<const typename ST::elem *>(p.S)[srow[t] + group]) * Code::kUnit;
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const Operand a = operand(k0, i);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const f32x4 acc = a.times(wf[t], f32x4{0, 0, 0, 0});
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) out[i][t][r] += s[t] * acc[r];
-                    }
-                }
-            }
-            slab0 += slab_k;
+            for (int f = 0; f < kPlanes; ++f) *reinterpret_cast<u32x4 *>(lds + (f * rows + r) * l.pitch + 16 * at) = a.f[f].v;
         }
+        __syncthreads();
 
-        // D of the matrix instruction: lane 16 q + c, register r: row 4 q + r, column c.
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    part[(wave * (16 * MT) + 16 * i + 4 * kq + r) * (16 * NT) + 16 * t + c] = out[i][t][r];
-        __syncthreads();
-        for (int e = threadIdx.x; e < rows * cols; e += blockDim.x) {
-            const int i = e / cols, j = e % cols;
-            if (c0 + j >= p.N) continue;
-            const float *src = part + (j / (16 * NT) * l.wk * (16 * MT) + i) * (16 * NT) + j % (16 * NT);
-            float sum = 0.0f;
-            for (int w = 0; w < l.wk; ++w) sum += src[w * (256 * MT * NT)];
-            float *dst = p.C + (m0 + i) * p.ldc + c0 + j;
-            *dst = p.beta == 0.0f ? p.alpha * sum : __builtin_fmaf(p.alpha, sum, p.beta * *dst);
+        if constexpr (!Short) {
+            for (int i = 0; i + 1 < steps; ++i) {
+                multiply(st, (s0 + i) * kStep);
+                load(st, slab0 + (s0 + i + 1) * kStep);
+            }
+            multiply(st, (s0 + steps - 1) * kStep);
         }
+        // What is left of the slab, 32 k at a time in turns, the codes
+        // guarded (A is 0 past K).
+        for (int k0 = all * kStep + 32 * wk; k0 < slab_k; k0 += 32 * l.wk) {
+            const int group = (slab0 + k0) / p.group, at = (slab0 + k0) / 2 + 4 * kq;
+            std::uint32_t w = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w |= at + i < bytes ? std::uint32_t(wrow[at + i]) << (8 * i) : 0u;
+            const Frag wf = Code(ZP ? zrow[group] & 15u : 8u)(w);
+            const float s = to_f32<ST>(static_cast<const typename ST::elem *>(p.S)[srow + group]) * Code::kUnit;
+            const f32x4 acc = operand(k0).times(wf, f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[r] += s * acc[r];
+        }
+        slab0 += slab_k;
+    }
+
+    // D of the matrix instruction: lane 16 q + c, register r: row 4 q + r, column c.
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) part[(wave * 16 + 4 * kq + r) * 16 + c] = out[r];
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * cols; e += blockDim.x) {
+        const int i = e / cols, j = e % cols;
+        if (c0 + j >= p.N) continue;
+        const float *src = part + (j / 16 * l.wk * 16 + i) * 16 + j % 16;
+        float sum = 0.0f;
+        for (int w = 0; w < l.wk; ++w) sum += src[w * 256];
+        float *dst = p.C + i * p.ldc + c0 + j;
+        *dst = p.beta == 0.0f ? p.alpha * sum : __builtin_fmaf(p.alpha, sum, p.beta * *dst);
     }
 }
 
-template <class T, class ST, int MT, int NT, int GS, bool ZP, bool Run> hipError_t launch_rows(const W4Problem &p, hipStream_t stream)
+template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_rows(const W4Problem &p, hipStream_t stream)
 {
-    constexpr int U = MT * NT <= 2 && sizeof(typename T::elem) == 2 ? 2 : 1, kStep = kW4Chunk * U, kWaves = MT * NT <= 2 ? 16 : 8;
+    constexpr int U = sizeof(typename T::elem) == 2 ? 2 : 1, kStep = kW4Chunk * U;
     constexpr std::int64_t kLds = 160 * 1024;
-    const std::int64_t tiles_m = (std::int64_t(p.M) + 16 * MT - 1) / (16 * MT);
     W4Layout l;
-    l.rows = p.M < 16 * MT ? p.M : 16 * MT;
     // Waves along K while there are too few columns to fill the device.
-    std::int64_t tiles_n = (std::int64_t(p.N) + 16 * NT - 1) / (16 * NT);
+    std::int64_t tiles_n = (std::int64_t(p.N) + 15) / 16;
     l.wn = 1;
     while (l.wn < 4 && tiles_n >= 2 * l.wn * std::int64_t(p.cus)) l.wn *= 2;
     // K in as few slabs as the LDS holds, of even length, each with a whole
-    // step for every wave. (A slab of one step and the rest always fits: 64
-    // float32 rows take 100 KB of it.)
+    // step for every wave. (A slab of one step and the rest always fits: 16
+    // float32 rows take 25 KB of it.)
     const int steps = p.K / kStep, rest = p.K % kStep;
     const auto held = [&](std::int64_t slab_steps) {
         l.pitch = int((2 * (slab_steps * kStep + (rest + 31) / 32 * 32) + 127) / 128 * 128 + 16);
-        return AOperand<T>::kPlanes * l.rows * std::int64_t(l.pitch);
+        return AOperand<T>::kPlanes * p.M * std::int64_t(l.pitch);
     };
     l.slabs = 1;
     while (l.slabs < steps && held((std::int64_t(steps) + l.slabs - 1) / l.slabs) > kLds) ++l.slabs;
     std::size_t shared = std::size_t(held((std::int64_t(steps) + l.slabs - 1) / l.slabs));
     l.wk = 1;
-    while (2 * l.wk * l.wn <= kWaves && 2 * l.wk <= steps / l.slabs) l.wk *= 2;
-    const int waves = l.wn * l.wk, width = 16 * NT * l.wn;
-    const std::size_t sums = std::size_t(waves) * MT * NT * 1024;
+    while (2 * l.wk * l.wn <= kRowsWaves && 2 * l.wk <= steps / l.slabs) l.wk *= 2;
+    const int waves = l.wn * l.wk, width = 16 * l.wn;
+    const std::size_t sums = std::size_t(waves) * 1024;
     if (shared < sums) shared = sums;
     tiles_n = (tiles_n + l.wn - 1) / l.wn;
-    const void *kernel = steps > 0 ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, MT, NT, GS, ZP, U, false, Run, kWaves>)
-                                   : reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, MT, NT, 1, ZP, U, true, false, kWaves>);
+    const void *kernel = steps > 0 ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, GS, ZP, U, false, Run>)
+                                   : reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, 1, ZP, U, true, false>);
     if (shared > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
         if (e != hipSuccess) return e;
@@ -537,17 +495,14 @@ template <class T, class ST, int MT, int NT, int GS, bool ZP, bool Run> hipError
     constexpr std::int64_t kBand = std::int64_t(1) << 21;
     for (std::int64_t t0 = 0; t0 < tiles_n; t0 += kBand) {
         const std::int64_t n0 = t0 * width, tn = tiles_n - t0 < kBand ? tiles_n - t0 : kBand;
-        std::int64_t tm = (std::int64_t(1) << 22) / tn / waves;
-        tm = tm < 1 ? 1 : tm < 65535 ? tm : 65535;
         W4Problem q = p;
         q.N = int(p.N - n0 < kBand * width ? p.N - n0 : kBand * width);
         q.W = p.W + n0 * p.ldw;
         q.S = static_cast<const char *>(p.S) + n0 * p.lds * (p.stype == SGEMM_F32 ? 4 : 2);
         if (p.Z) q.Z = p.Z + n0 * p.ldz;
         q.C = p.C + n0;
-        const dim3 grid(unsigned(tn), unsigned(tiles_m < tm ? tiles_m : tm));
         void *args[] = {&q, &l};
-        const hipError_t e = hipLaunchKernel(kernel, grid, dim3(64 * waves), args, shared, stream);
+        const hipError_t e = hipLaunchKernel(kernel, dim3(unsigned(tn)), dim3(64 * waves), args, shared, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -833,7 +788,7 @@ template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_shape(
     // Up to 8 rows (16 in float32, whose parts fill the tile kernel's LDS) the
     // rows kernel is faster: 8192 x 8192 bf16, 8 rows 17.0 us against 17.7, 16
     // rows 22.1 against 18.4; float32, 16 rows 32.8 against 41.5.
-    if (p.M <= (AOperand<T>::kPlanes == 1 ? 8 : 16)) return launch_rows<T, ST, 1, 1, GS, ZP, Run>(p, stream);
+    if (p.M <= (AOperand<T>::kPlanes == 1 ? 8 : 16)) return launch_rows<T, ST, GS, ZP, Run>(p, stream);
     return launch_tile<T, GS, ZP, Run>(p, stream);
 }
 
