@@ -313,10 +313,14 @@ template <int GS, int N, bool ZP, bool Run> struct AnyGroups {
     __device__ std::uint32_t zero(int run) const { return ZP ? (Run ? z[0].at(run) : z[Run ? 0 : run].at(0)) & 15u : 8u; }
 };
 
-// What a wave loads for U chunks of k.
-template <class ST, int GS, int U, bool ZP, bool Run> struct W4Stage {
+// What a wave loads for U chunks of k; Held: A comes from LDS.
+template <class T> struct Eight {
+    typename T::elem x[8];
+};
+template <class T, class ST, int GS, int U, bool ZP, bool Run, bool Held> struct W4Stage {
     u32x4 w[U];
     Groups<ST, GS, 4 * U / GS, ZP, Run> g;
+    Eight<T> a[Held ? 1 : 4 * U];  // Held: not used
 };
 
 // How a product is laid out over work-groups (launch_rows).
@@ -326,25 +330,29 @@ struct W4Layout {
     int pitch;   // bytes from one held row to the next: 16 more than a multiple of 128, so that 16 rows meet in no bank
 };
 
-// Up to 16 rows of A. One work-group: all rows of C by 16 wn columns. A slab
-// of A's rows lies in LDS as matrix operands, read by every wave; the codes
-// go from memory to registers once: each wave takes a run of the slab's k for
-// its 16 columns in steps of U chunks of 128, each lane 16 bytes of one
-// column's codes per chunk. The wk waves of a column tile add their sums
-// through LDS in their order, so the result does not depend on timing. GS:
-// steps of 32 k that share a scale.
+// Up to 16 rows of A. One work-group: all rows of C by 16 wn columns. The
+// codes go from memory to registers once: each wave takes a run of K for its
+// 16 columns in steps of U chunks of 128, each lane 16 bytes of one column's
+// codes per chunk. The wk waves of a column tile add their sums through LDS
+// in their order, so the result does not depend on timing. GS: steps of 32 k
+// that share a scale.
+//
+// Held: a slab of A's rows lies in LDS as matrix operands, read by every wave
+// (and the runs are the slab's). Otherwise A comes straight to registers,
+// eight elements of a row for each lane and matrix instruction: no barriers,
+// but more loads in all. launch_rows chooses.
 //
 // Memory bounds it: 1 row of bf16 by 16384 x 4096 with zero points (35 MB)
-// takes 12.4 us on the device, 2.8 TB/s; 8 rows by 8192 x 8192 17.0. Of the
-// 12.4 us the loads alone take 8.7 and A's way to LDS 1, neither of which
-// more loads in flight shortened (A or codes, one to three steps further
-// ahead: 13.9 to 16.7 us).
-template <class T, class ST, int GS, bool ZP, int U, bool Short, bool Run>
+// takes 12.4 us on the device, 2.8 TB/s; 8 rows by 8192 x 8192 (34 MB) 15.8.
+// Of the 12.4 us the loads alone take 8.7 and A's way to LDS 1, neither of
+// which more loads in flight shortened (A or codes, one to three steps
+// further ahead: 13.9 to 16.7 us).
+template <class T, class ST, int GS, bool ZP, int U, bool Short, bool Run, bool Held>
 __global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W4Layout l)
 {
     extern __shared__ __align__(16) char lds[];  // A: [plane][row][k] as 16-bit operands
     typedef typename T::elem elem;
-    typedef W4Stage<ST, GS, U, ZP, Run> Stage;
+    typedef W4Stage<T, ST, GS, U, ZP, Run, Held> Stage;
     typedef AOperand<T> Operand;
     typedef Codes<T, ZP> Code;
     constexpr int kStep = kW4Chunk * U, kPlanes = Operand::kPlanes;
@@ -359,21 +367,29 @@ __global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W
     const std::int64_t n = c0 + wn * 16 + c < p.N ? c0 + wn * 16 + c : p.N - 1, srow = n * p.lds;
     const std::uint8_t *const wrow = p.W + n * p.ldw, *const zrow = ZP ? p.Z + n * p.ldz : nullptr;
 
+    // Likewise rows past the last.
+    const int my_row = c < rows ? c : rows - 1;
+    const elem *const arow = static_cast<const elem *>(p.A) + my_row * p.lda;
+
     auto load = [&](Stage &st, unsigned k0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) st.w[u] = load_any<u32x4>(wrow + (k0 / 2 + 64 * u + 16 * kq));
+        if constexpr (!Held) {
+#pragma unroll
+            for (int s = 0; s < 4 * U; ++s) st.a[s] = load_any<Eight<T>>(arow + (k0 + 32 * s + 8 * kq));
+        }
         st.g.load(p.S, srow, zrow, k0, p.group);
     };
 
-    const char *arow[kPlanes];  // rows past the last repeat it; their sums are not stored
+    const char *held[kPlanes];
 #pragma unroll
-    for (int f = 0; f < kPlanes; ++f) arow[f] = lds + (f * rows + (c < rows ? c : rows - 1)) * l.pitch + 16 * kq;
+    for (int f = 0; f < kPlanes; ++f) held[f] = lds + (f * rows + my_row) * l.pitch + 16 * kq;
     f32x4 out = {0, 0, 0, 0};
 
-    auto operand = [&](int k) {  // A's operand of the step of 32 that starts at k of the slab
+    auto operand = [&](int k) {  // A's operand of the step of 32 that starts at k of the held slab
         Operand a;
 #pragma unroll
-        for (int f = 0; f < kPlanes; ++f) a.f[f].v = *reinterpret_cast<const u32x4 *>(arow[f] + 2 * k);
+        for (int f = 0; f < kPlanes; ++f) a.f[f].v = *reinterpret_cast<const u32x4 *>(held[f] + 2 * k);
         return a;
     };
     auto multiply = [&](const Stage &st, int k0) {
@@ -387,7 +403,13 @@ __global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W
 #pragma unroll
                 for (int s = 0; s < GS; ++s) {
                     const Frag wf = Code(st.g.zero(run))(w[g * GS + s]);
-                    acc = operand(k0 + 128 * u + 32 * (g * GS + s)).times(wf, s == 0 ? f32x4{0, 0, 0, 0} : acc);
+                    Operand a;
+                    if constexpr (Held) {
+                        a = operand(k0 + 128 * u + 32 * (g * GS + s));
+                    } else {
+                        a.set(st.a[4 * u + g * GS + s].x);
+                    }
+                    acc = a.times(wf, s == 0 ? f32x4{0, 0, 0, 0} : acc);
                 }
                 const float s = st.g.scale(run) * Code::kUnit;
 #pragma unroll
@@ -407,18 +429,20 @@ __global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W
         Stage st;
         if constexpr (!Short) load(st, slab0 + s0 * kStep);
 
-        if (j > 0) __syncthreads();  // the last slab has been read
-        const int eights = (slab_k + 31) / 32 * 4;
-        for (int e = threadIdx.x; e < rows * eights; e += blockDim.x) {
-            const int r = e / eights, at = e % eights;
-            elem x[8];
-            load_a<T>(static_cast<const elem *>(p.A) + r * p.lda + slab0, 8 * at, slab_k, x);
-            Operand a;
-            a.set(x);
+        if constexpr (Held) {
+            if (j > 0) __syncthreads();  // the last slab has been read
+            const int eights = (slab_k + 31) / 32 * 4;
+            for (int e = threadIdx.x; e < rows * eights; e += blockDim.x) {
+                const int r = e / eights, at = e % eights;
+                elem x[8];
+                load_a<T>(static_cast<const elem *>(p.A) + r * p.lda + slab0, 8 * at, slab_k, x);
+                Operand a;
+                a.set(x);
 #pragma unroll
-            for (int f = 0; f < kPlanes; ++f) *reinterpret_cast<u32x4 *>(lds + (f * rows + r) * l.pitch + 16 * at) = a.f[f].v;
+                for (int f = 0; f < kPlanes; ++f) *reinterpret_cast<u32x4 *>(lds + (f * rows + r) * l.pitch + 16 * at) = a.f[f].v;
+            }
+            __syncthreads();
         }
-        __syncthreads();
 
         if constexpr (!Short) {
             for (int i = 0; i + 1 < steps; ++i) {
@@ -436,7 +460,15 @@ __global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W
             for (int i = 0; i < 4; ++i) w |= at + i < bytes ? std::uint32_t(wrow[at + i]) << (8 * i) : 0u;
             const Frag wf = Code(ZP ? zrow[group] & 15u : 8u)(w);
             const float s = to_f32<ST>(static_cast<const typename ST::elem *>(p.S)[srow + group]) * Code::kUnit;
-            const f32x4 acc = operand(k0).times(wf, f32x4{0, 0, 0, 0});
+            Operand a;
+            if constexpr (Held) {
+                a = operand(k0);
+            } else {
+                elem x[8];
+                load_a<T>(arow, slab0 + k0 + 8 * kq, p.K, x);
+                a.set(x);
+            }
+            const f32x4 acc = a.times(wf, f32x4{0, 0, 0, 0});
 #pragma unroll
             for (int r = 0; r < 4; ++r) out[r] += s * acc[r];
         }
@@ -472,21 +504,28 @@ template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_rows(c
     // step for every wave. (A slab of one step and the rest always fits: 16
     // float32 rows take 25 KB of it.)
     const int steps = p.K / kStep, rest = p.K % kStep;
-    const auto held = [&](std::int64_t slab_steps) {
-        l.pitch = int((2 * (slab_steps * kStep + (rest + 31) / 32 * 32) + 127) / 128 * 128 + 16);
-        return AOperand<T>::kPlanes * p.M * std::int64_t(l.pitch);
+    const auto held = [&](std::int64_t slab_steps) {  // bytes
+        const std::int64_t pitch = (2 * (slab_steps * kStep + (rest + 31) / 32 * 32) + 127) / 128 * 128 + 16;
+        l.pitch = int(pitch);
+        return AOperand<T>::kPlanes * p.M * pitch;
     };
     l.slabs = 1;
-    while (l.slabs < steps && held((std::int64_t(steps) + l.slabs - 1) / l.slabs) > kLds) ++l.slabs;
-    std::size_t shared = std::size_t(held((std::int64_t(steps) + l.slabs - 1) / l.slabs));
+    // A that does not fit at once goes straight to registers while there is at
+    // most one column tile for each compute unit: 16 rows of float32 by 4096
+    // columns, K = 4096, 13.5 us against 17.8, by 1024, K = 16384, 38.8 against
+    // 54.9, but by 8192, K = 8192, 41.8 against 32.8.
+    const bool straight = held(steps) > kLds && tiles_n <= p.cus;
+    while (!straight && l.slabs < steps && held((std::int64_t(steps) + l.slabs - 1) / l.slabs) > kLds) ++l.slabs;
+    std::size_t shared = straight ? 0 : std::size_t(held((std::int64_t(steps) + l.slabs - 1) / l.slabs));
     l.wk = 1;
     while (2 * l.wk * l.wn <= kRowsWaves && 2 * l.wk <= steps / l.slabs) l.wk *= 2;
     const int waves = l.wn * l.wk, width = 16 * l.wn;
     const std::size_t sums = std::size_t(waves) * 1024;
     if (shared < sums) shared = sums;
     tiles_n = (tiles_n + l.wn - 1) / l.wn;
-    const void *kernel = steps > 0 ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, GS, ZP, U, false, Run>)
-                                   : reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, 1, ZP, U, true, false>);
+    const void *kernel = steps == 0 ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, 1, ZP, U, true, false, true>)
+                         : straight ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, GS, ZP, U, false, Run, false>)
+                                    : reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, GS, ZP, U, false, Run, true>);
     if (shared > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
         if (e != hipSuccess) return e;

@@ -154,6 +154,17 @@ def test_infinities_nan_and_zero_groups(M, zeros, dtype):
     assert np.isnan(C[1]).all() and np.isfinite(C[2:]).all()
 
 
+# More of A than a compute unit's LDS holds: in slabs, or (few columns) straight to registers.
+@pytest.mark.parametrize("M,N,K,group,zeros,dtype", [
+    (13, 200, 4093, 32, True, "f32"), (16, 48, 4096, 128, False, "f32"), (3, 17, 20001, 64, True, "f32"),
+    (8, 40, 12000, 96, True, "bf16"), (8, 33, 16384, 128, False, "f16"), (1, 5, 90000, 128, True, "bf16"),
+    (13, 4200, 4093, 64, False, "f32"), (8, 4100, 11000, 128, True, "bf16")])
+def test_rows_longer_than_lds(M, N, K, group, zeros, dtype):
+    A, W, dense = operands(11, M, N, K, group, dtype, "f16", zeros)
+    a = A.double().numpy()
+    assert_within(sg.gemm_w4(A.cuda(), W).cpu().numpy(), a @ dense.T, np.abs(a) @ np.abs(dense).T)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M", [4, 40])
 def test_infinite_and_nan_scales_of_a_short_last_group(M, dtype):
