@@ -183,6 +183,12 @@ template <class T> constexpr int kv8_waves_per_simd(int DC, int MT) { return DC 
 // each has half a turn to arrive. No load is conditional (that would make the
 // compiler wait for all of them): pages that may not be read are replaced by
 // page 0 and their scores by NaN.
+//
+// 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 query heads each
+// (0.41 GB): 84.8 us, 4.8 TB/s, bound by memory. 2 prompts of 1024 rows behind
+// 4096 tokens in f16: 260 us, 460 TFLOP/s, bound by the SIMDs: matrix
+// instructions take 43% of the cycles a compute unit is busy, the softmax and
+// the conversion of codes 55%.
 template <class T, int DC, bool Full, int MT, bool Rows>
 __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) void kv8_attend_kernel(Kv8AttendProblem p)
 {
@@ -486,7 +492,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
 }
 
 // Adds the sums that the splits of a row tile left in the workspace, in their
-// order: one wave for each row.
+// order: one wave for each row (32 sequences of 8192 tokens in 3 splits: 5 us,
+// most of it the launch).
 template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendProblem p)
 {
     constexpr int kRows = 16 * MT;
