@@ -209,3 +209,76 @@ def test_large_matrix_offsets():
         assert (C[:, :-4] == 0).all()
         a = A.double().numpy()
         assert_within(C[:, -4:].cpu().numpy(), a @ dense.T, np.abs(a) @ np.abs(dense).T, f"{M} rows")
+
+
+def test_the_helpers_refuse():
+    # Wrong kinds, types, sizes, strides and places of every tensor; nothing is launched.
+    case = Case(41, [40, 20], [2, 1], 2, 16, 64)
+    cache, (table, lens, starts) = case.device(), case.args()
+    K, Q = case.normal(2, "f32").cuda(), case.normal(4, "bf16").cuda()
+    W = sg.quantize_w4(torch.randn(32, 64, device="cuda"), 32, True)
+    A, C = torch.randn(3, 64, device="cuda"), torch.zeros(3, 32, device="cuda")
+    wide = torch.randn(3, 4, 128, device="cuda")
+    bad = {
+        TypeError: [
+            lambda: sg.kv8_write(cache, K.double(), K, table, lens, starts), lambda: sg.kv8_write(cache, K, K.half(), table, lens, starts),
+            lambda: sg.kv8_write(cache, K, K, table.long(), lens, starts), lambda: sg.kv8_write(cache, K, K, table, lens.float(), starts),
+            lambda: sg.kv8_write(cache, K, K, table[0], lens, starts), lambda: sg.kv8_write(cache, K[0], K, table, lens, starts),
+            lambda: sg.kv8_read(cache, table, lens, starts, rows=3, dtype=torch.float64),
+            lambda: sg.kv8_attend(Q, cache, table, lens, starts, out=torch.zeros(Q.shape, device="cuda").half()),
+            lambda: sg.kv8_attend(Q.int(), cache, table, lens, starts), lambda: sg.kv8_attend(Q, W, table, lens, starts),
+            lambda: sg.gemm_w4(A.double(), W), lambda: sg.gemm_w4(A, W, C.half()), lambda: sg.gemm_w4(A, W.codes),
+            lambda: sg.dequantize_w4(W, torch.int32), lambda: sg.dequantize_w4(W, torch.float16, torch.zeros(32, 64, device="cuda")),
+            lambda: sg.W4(W.codes.int(), W.scales, None, 64, 32), lambda: sg.W4(W.codes, W.scales, W.scales, 64, 32),
+            lambda: sg.KV8(cache.K.view(torch.uint8), cache.V, cache.Ks, cache.Vs), lambda: sg.KV8(cache.K, cache.V, cache.Ks.half(), cache.Vs),
+        ],
+        ValueError: [
+            lambda: sg.kv8_write(cache, K.cpu(), K, table, lens, starts), lambda: sg.kv8_write(cache, K, K, table.cpu(), lens, starts),
+            lambda: sg.kv8_write(cache, K, K[:2], table, lens, starts), lambda: sg.kv8_write(cache, K[:, :, :32], K, table, lens, starts),
+            lambda: sg.kv8_write(cache, K, K, table, lens[:1], starts), lambda: sg.kv8_write(cache, K, K, table, lens, starts[:2]),
+            lambda: sg.kv8_write(cache, K, K, table.t().contiguous().t(), lens, starts), lambda: sg.kv8_write(cache, Q.float(), K, table, lens, starts),
+            lambda: sg.kv8_write(cache, K.transpose(1, 2).contiguous().transpose(1, 2), K, table, lens, starts),
+            lambda: sg.kv8_read(cache, table, lens, starts), lambda: sg.kv8_read(cache, table, lens, starts, K=K),
+            lambda: sg.kv8_read(cache, table, lens, starts, rows=4, K=K, V=K.clone()),
+            lambda: sg.kv8_attend(wide, cache, table, lens, starts), lambda: sg.kv8_attend(Q, cache, table, lens, starts, out=K),
+            lambda: sg.kv8_attend(Q, cache, table, lens, starts, workspace=torch.zeros(8)),
+            lambda: sg.gemm_w4(A.cpu(), W), lambda: sg.gemm_w4(A[:, :63], W), lambda: sg.gemm_w4(A, W, C[:2]), lambda: sg.gemm_w4(A, W, beta=1.0),
+            lambda: sg.gemm_w4(A.t().contiguous().t(), W), lambda: sg.gemm_w4(A[:1].expand(3, 64), W),
+            lambda: sg.dequantize_w4(W, out=torch.zeros(32, 63, device="cuda")), lambda: sg.quantize_w4(A, 48),
+            lambda: sg.W4(W.codes, W.scales, None, 66, 32), lambda: sg.W4(W.codes, W.scales[:, :1], None, 64, 32),
+            lambda: sg.W4(W.codes.cpu(), W.scales, None, 64, 32), lambda: sg.KV8(cache.K.cpu(), cache.V.cpu(), cache.Ks.cpu(), cache.Vs.cpu()),
+            lambda: sg.KV8(cache.K, cache.V, cache.Ks[:1], cache.Vs), lambda: sg.KV8(cache.K[:, :, :12], cache.V[:, :, :12], cache.Ks, cache.Vs),
+        ],
+        sg.SgemmError: [
+            lambda: sg.kv8_attend(Q[:, :3].contiguous(), cache, table, lens, starts), lambda: sg.kv8_attend(Q, cache, table, lens, starts, causal=False, window=4),
+            lambda: sg.kv8_attend(K[:1].expand(3, 2, 64), cache, table, lens, starts), lambda: sg.kv8_read(cache, table, lens, starts, K=K, V=K),
+            lambda: sg.gemm_w4(A, W, A[:, :32]), lambda: sg.kv8_attend(K, cache, table, lens, starts, out=K),
+        ],
+    }
+    before = [t.clone() for t in (cache.K.view(torch.uint8), cache.Ks, A, K)]
+    for error, calls in bad.items():
+        for i, call in enumerate(calls):
+            with pytest.raises(error):
+                call()
+                pytest.fail(f"{error.__name__} {i} was not refused")
+    assert all(torch.equal(x, y) for x, y in zip(before, (cache.K.view(torch.uint8), cache.Ks, A, K)))
+
+
+def test_calls_with_nothing_to_do():
+    case = Case(42, [40, 20], [0, 0], 2, 16, 64)
+    cache, args = case.device(), case.args()
+    none = torch.empty(0, 2, 64, device="cuda")
+    sg.kv8_write(cache, none, none, *args)
+    assert [t.shape for t in sg.kv8_read(cache, *args, rows=0)] == [none.shape] * 2 and sg.kv8_attend(none, cache, *args).shape == none.shape
+    empty = [args[0][:0], args[1][:0], args[2][:1]]
+    out = torch.full((3, 2, 64), 2.5, device="cuda")
+    sg.kv8_write(cache, out, out, *empty)
+    assert (sg.kv8_attend(torch.zeros_like(out), cache, *empty, out=out) == 2.5).all()
+    same_cache(cache, case.ref, "nothing written")
+    for N, K in ((0, 64), (5, 0)):
+        W = sg.quantize_w4(torch.empty(N, K, device="cuda"), 32, True)
+        assert sg.dequantize_w4(W).shape == (N, K)
+        assert (sg.gemm_w4(torch.empty(2, K, device="cuda"), W) == torch.zeros(2, N, device="cuda")).all()
+        assert (sg.gemm_w4(torch.empty(2, K, device="cuda"), W, torch.full((2, N), 3.0, device="cuda"), beta=0.5) == 1.5).all()
+    W = sg.quantize_w4(torch.randn(32, 64, device="cuda"), 32)
+    assert sg.gemm_w4(torch.empty(0, 64, device="cuda"), W).shape == (0, 32)
