@@ -79,24 +79,32 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
         const int g = int(id % groups);
         const int k0 = g * p.group, k1 = p.K - k0 < p.group ? p.K : k0 + p.group;
         const typename T::elem *row = static_cast<const typename T::elem *>(p.B) + n * p.ldb;
-        float lo = 0.0f, hi = 0.0f, x[8];
-        bool fine = true;
+        // The largest and the least of the values and 0 by their bits: as
+        // signed numbers positive floats are in order and above the negative,
+        // as unsigned ones negative floats lie above the positive, the largest
+        // magnitude on top. What is not finite ends above either range.
+        int top = 0;
+        std::uint32_t bottom = 0x80000000u;
+        float x[8];
         for (int k = k0 + 8 * part; k < k1; k += 8 * LG) {
             load8<T>(row, k, k1, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                fine = fine && (f32_bits(x[i]) & 0x7f800000u) != 0x7f800000u;
-                lo = __builtin_fminf(lo, x[i]);
-                hi = __builtin_fmaxf(hi, x[i]);
+                const std::uint32_t bits = f32_bits(x[i]);
+                top = int(bits) > top ? int(bits) : top;
+                bottom = bits > bottom ? bits : bottom;
             }
             if (Once) break;
         }
 #pragma unroll
         for (int d = LG / 2; d > 0; d /= 2) {
-            lo = __builtin_fminf(lo, __shfl_xor(lo, d));
-            hi = __builtin_fmaxf(hi, __shfl_xor(hi, d));
-            fine = __shfl_xor(int(fine), d) != 0 && fine;
+            const int t = __shfl_xor(top, d);
+            const std::uint32_t b = std::uint32_t(__shfl_xor(int(bottom), d));
+            top = t > top ? t : top;
+            bottom = b > bottom ? b : bottom;
         }
+        const float lo = bits_f32(bottom), hi = bits_f32(std::uint32_t(top));
+        const bool fine = top < 0x7f800000 && bottom < 0xff800000u;
         float s = ZP ? (hi - lo) / 15.0f : __builtin_fmaxf(hi, -lo) / 7.0f;
         if (!fine) s = __builtin_nanf("");
         // Every lane of the group rounds the scale; the first stores it.
@@ -119,12 +127,15 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
         for (int k = k0 + 8 * part; k < k1; k += 8 * LG) {
             if (!Once) load8<T>(row, k, k1, x);
             float q[8];
+            if (up != 1.0f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = flat ? 0.0f : x[i] * up;
+                for (int i = 0; i < 8; ++i) x[i] *= up;
+            }
             rounded_quotients<8>(x, scale, inverse, q);
             std::uint32_t w = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w |= std::uint32_t(__builtin_amdgcn_fmed3f(flat ? 8.0f : q[i] + z, 0.0f, 15.0f)) << (4 * i);
+            for (int i = 0; i < 8; ++i) w |= std::uint32_t(__builtin_amdgcn_fmed3f(q[i] + z, 0.0f, 15.0f)) << (4 * i);
+            w = flat ? 0x88888888u : w;
             if (k + 8 > k1) w &= (1u << (4 * (k1 - k))) - 1u;  // past the row's end: 0
             std::uint8_t *dst = p.W + n * p.ldw + k / 2;
             if (k + 8 <= k1) {
