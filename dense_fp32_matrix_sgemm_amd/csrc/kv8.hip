@@ -132,25 +132,29 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(
         const std::int64_t start = w.s.len - w.s.n;  // position of the sequence's first row (may be below 0)
         const std::int64_t t0 = w.page * block;
         const std::int64_t lo = start > t0 ? start : t0, hi = w.s.len < t0 + block ? w.s.len : t0 + block;
-        const std::int64_t page = kv8_page(p.c, p.b, w.s.seq, w.page);
-        if (page < 0) return;  // the same for the whole work-group
-        const int kept = int(lo - t0), fresh = int(hi - lo);
+        const int kept = int(lo - t0), fresh = int(hi - lo);  // fresh >= 1
         const std::int64_t ld = w.kv ? p.ldv : p.ldk;
         const elem *src = static_cast<const elem *>(w.kv ? p.V : p.K) + (w.s.row0 + (lo - start)) * ld +
                           w.head * (w.kv ? p.hsv : p.hsk) + lanes.at;
+        // The first pieces stay in registers; further ones are read again
+        // below. They are on their way while the table is read, without
+        // conditions (which would make them wait for one another): past the
+        // last row it is read again, which changes no maximum.
+        Eight<T> held[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int r = lanes.row + i * lanes.step;
+            held[i] = load_any<Eight<T>>(src + (r < fresh ? r : fresh - 1) * ld);
+        }
+        const std::int64_t page = kv8_page(p.c, p.b, w.s.seq, w.page);
+        if (page < 0) return;  // the same for the whole work-group
         std::uint8_t *codes = static_cast<std::uint8_t *>(w.kv ? p.c.V : p.c.K) + (page * p.c.heads + w.head) * block * dim + lanes.at;
         float *scale = (w.kv ? p.c.Vs : p.c.Ks) + page * p.c.heads + w.head;
         const float before = kept > 0 ? *scale : 0.0f;
 
-        // The first pieces stay in registers; further ones are read again below.
-        Eight<T> held[kHeld];
         std::uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            if (lanes.row + i * lanes.step < fresh) held[i] = load_any<Eight<T>>(src + (lanes.row + i * lanes.step) * ld);
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            if (lanes.row + i * lanes.step < fresh) m = largest<T>(held[i].x, m);
+        for (int i = 0; i < kHeld; ++i) m = largest<T>(held[i].x, m);
         for (int r = lanes.row + kHeld * lanes.step; r < fresh; r += lanes.step) m = largest<T>(load_any<Eight<T>>(src + r * ld).x, m);
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) {
