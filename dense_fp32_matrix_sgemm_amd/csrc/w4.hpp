@@ -566,7 +566,7 @@ template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_rows(c
 // The matrix cores bound it: what shares their time is the conversion (7
 // cycles a code and column, so tall tiles) and the reads of A from LDS (4
 // cycles a row and 64 k for four waves against MT NT matrix instructions, so
-// wide ones). 2048 x 4096 x 4096 in bf16: 87 us in a run of calls (790
+// wide ones). 2048 x 4096 x 4096 in bf16: 86 us in a run of calls (800
 // TFLOP/s), 99 in a replayed graph; matrix instructions take 37% of the cycles
 // a compute unit is busy, the other vector instructions 53%. 128 x 64 a wave,
 // one wave a SIMD: 121 us; 16x16x32 instructions: 571.

@@ -1,7 +1,8 @@
 // Quantising a matrix to the W4 form (sgemm_w4_quantize) and reading it back
 // (sgemm_w4_dequantize). Each matrix is moved once. 4096 x 4096 in bf16 (42
-// MB): quantising takes 18.4 us, 2.3 TB/s, bound by the arithmetic of rounding
-// as the definition does; reading back 14.4 us, 2.9 TB/s, bound by memory.
+// MB): quantising takes 16.3 us, 2.6 TB/s (its arithmetic, to round as the
+// definition does, takes about as long as its bytes); reading back 14.4 us,
+// 2.9 TB/s, bound by memory.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
