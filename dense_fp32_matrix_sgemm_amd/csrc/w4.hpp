@@ -667,7 +667,17 @@ __global__ __launch_bounds__(64 * WN * WK, WN > 1 && AOperand<T>::kPlanes == 1 ?
             }
         }
     };
+    // A wave with a buffer of its own writes what its other lanes read: the
+    // hardware runs one wave's LDS accesses in order, the fences keep the
+    // compiler to that order (no instruction). WN > 1 has the barrier.
+    auto own_order = [] {
+        if constexpr (WN == 1) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
     auto hold = [&](char *buffer) {
+        own_order();
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             Operand a;
@@ -676,6 +686,7 @@ __global__ __launch_bounds__(64 * WN * WK, WN > 1 && AOperand<T>::kPlanes == 1 ?
             for (int f = 0; f < kPlanes; ++f)
                 *reinterpret_cast<u32x4 *>(buffer + (f * BM + prow + 4 * WN * i) * kTilePitch + 16 * piece) = a.f[f].v;
         }
+        own_order();
     };
 
     const int slabs = (p.K + kW4Chunk - 1) / kW4Chunk, whole = p.K / kW4Chunk;
