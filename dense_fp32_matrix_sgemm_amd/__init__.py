@@ -55,9 +55,9 @@ import os
 
 from . import lowbit
 from .lowbit import (KV8, SGEMM_F32, W4, KV8Batch, KV8Cache, dequantize_w4, gemm_w4, kv8_attend, kv8_read, kv8_write,
-                     quantize_w4, sgemm_kv8_attend, sgemm_kv8_attend_check_args, sgemm_kv8_attend_workspace_size,
-                     sgemm_kv8_check_args, sgemm_kv8_read, sgemm_kv8_write, sgemm_w4, sgemm_w4_check_args,
-                     sgemm_w4_dequantize, sgemm_w4_pack_check_args, sgemm_w4_quantize)
+                     quantize_w4, sgemm_kv8_attend, sgemm_kv8_attend_check_args, sgemm_kv8_attend_shape,
+                     sgemm_kv8_attend_workspace_size, sgemm_kv8_check_args, sgemm_kv8_read, sgemm_kv8_write, sgemm_w4,
+                     sgemm_w4_check_args, sgemm_w4_dequantize, sgemm_w4_pack_check_args, sgemm_w4_quantize, sgemm_w4_shape)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libsgemm.so")

@@ -1,5 +1,5 @@
 // Host-side argument checks of the products whose stored operand is held in
-// few bits, and the layout of attention over the device.
+// few bits, and how products and attention are laid out over the device.
 //
 // Pure C++: no HIP header and no device call, like args.cpp.
 #include <cstddef>
@@ -191,6 +191,59 @@ bool kv8_read_overlaps(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int d
     return overlap(k, v) || overlaps_batch(k, &b) || overlaps_batch(v, &b);
 }
 
+W4Plan plan_w4(int dtype, int M, int N, int K, int cus)
+{
+    cus = cus <= 0 ? 256 : cus;
+    const bool f32 = dtype == SGEMM_F32;
+    W4Plan plan = {};
+    // Up to 8 rows (16 in float32, whose parts fill the tile kernel's LDS) the
+    // rows kernel is faster: 8192 x 8192 bf16, 8 rows 17.0 us against 17.7, 16
+    // rows 22.1 against 18.4; float32, 16 rows 32.8 against 41.5.
+    if (M > (f32 ? 16 : 8)) {
+        // The largest tile that still gives every compute unit one; with fewer
+        // tiles the waves divide K. float32 rows take three times the LDS.
+        const auto tiles = [&](int bm, int bn) { return (i64(M) + bm - 1) / bm * ((i64(N) + bn - 1) / bn); };
+        if (tiles(64, 256) >= cus) {
+            plan.mt = 2, plan.nt = 2, plan.wn = 4, plan.wk = 1;
+        } else if (f32) {
+            plan.mt = 1, plan.nt = 1, plan.wn = 1, plan.wk = 4;
+        } else if (tiles(64, 64) >= 2 * i64(cus)) {
+            plan.mt = 2, plan.nt = 2, plan.wn = 1, plan.wk = 4;
+        } else {
+            plan.mt = M > 32 ? 2 : 1, plan.nt = 1, plan.wn = 1, plan.wk = 8;
+        }
+        return plan;
+    }
+    plan.few = 1;
+    constexpr i64 kLds = 160 * 1024;
+    // Waves along K while there are too few columns to fill the device.
+    const i64 tiles_n = (i64(N) + 15) / 16;
+    plan.wn = 1;
+    while (plan.wn < 4 && tiles_n >= 2 * plan.wn * i64(cus)) plan.wn *= 2;
+    // K in as few slabs as the LDS holds, of even length, each with a whole
+    // step for every wave. (A slab of one step and the rest always fits: 16
+    // float32 rows take 25 KB of it.)
+    const int step = w4_step(f32), steps = K / step, rest = K % step;
+    const auto pitch = [&](i64 slab_steps) { return (2 * (slab_steps * step + (rest + 31) / 32 * 32) + 127) / 128 * 128 + 16; };
+    const auto held = [&](i64 slab_steps) { return (f32 ? 3 : 1) * M * pitch(slab_steps); };  // bytes
+    // A that does not fit at once goes straight to registers while there is at
+    // most one column tile for each compute unit: 16 rows of float32 by 4096
+    // columns, K = 4096, 13.5 us against 17.8, by 1024, K = 16384, 38.8 against
+    // 54.9, but by 8192, K = 8192, 41.8 against 32.8.
+    if (held(steps) > kLds && tiles_n <= cus) {
+        plan.slabs = 0;
+    } else {
+        plan.slabs = 1;
+        const auto longest = [&] { return (i64(steps) + plan.slabs - 1) / plan.slabs; };
+        while (plan.slabs < steps && held(longest()) > kLds) ++plan.slabs;
+        plan.pitch = int(pitch(longest()));
+        plan.held = int(held(longest()));
+    }
+    plan.wk = 1;
+    while (2 * plan.wk * plan.wn <= kRowsWaves && 2 * plan.wk <= steps / (plan.slabs ? plan.slabs : 1)) plan.wk *= 2;
+    return plan;
+}
+
 Kv8Plan plan_kv8_attend(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus)
 {
     cus = cus <= 0 ? 256 : cus < 4096 ? cus : 4096;
@@ -240,4 +293,34 @@ extern "C" size_t sgemm_kv8_attend_workspace_size(const sgemm_kv8_cache *c, cons
     // For each row of each split: the sums of its components, maximum and sum of the softmax.
     return std::size_t(b->seqs) * std::size_t(c->heads) * std::size_t(plan.tiles) * std::size_t(plan.splits) * std::size_t(16 * plan.mt) *
            std::size_t(c->dim + 4) * 4;
+}
+
+extern "C" int sgemm_w4_shape(int dtype, int M, int N, int K, int cus, int *shape)
+{
+    if (!known_type(dtype)) return SGEMM_ERR_DTYPE;
+    if (M < 0 || N < 0 || K < 0 || K > kMostK) return SGEMM_ERR_DIM;
+    if (shape == nullptr) return SGEMM_ERR_NULL;
+    const sgemm_impl::W4Plan plan = sgemm_impl::plan_w4(dtype, M, N, K, cus);
+    shape[0] = plan.few ? 16 : 32 * plan.mt;
+    shape[1] = plan.few ? 16 * plan.wn : 32 * plan.nt * plan.wn;
+    shape[2] = plan.wn;
+    shape[3] = plan.wk;
+    shape[4] = plan.few ? plan.slabs : 1;
+    return SGEMM_OK;
+}
+
+extern "C" int sgemm_kv8_attend_shape(const sgemm_kv8_cache *c, const sgemm_kv8_batch *b, int heads_q, int window, int cus,
+                                      int *shape)
+{
+    const int rc = check_cache_batch(c, b);
+    if (rc != SGEMM_OK) return rc;
+    if (heads_q < 1 || heads_q % c->heads != 0) return SGEMM_ERR_HEADS;
+    if (window < 0) return SGEMM_ERR_MASK;
+    if (shape == nullptr) return SGEMM_ERR_NULL;
+    const sgemm_impl::Kv8Plan plan = sgemm_impl::plan_kv8_attend(*c, *b, heads_q, window, cus);
+    shape[0] = 16 * plan.mt;
+    shape[1] = plan.rows ? 4 : 1;
+    shape[2] = plan.tiles;
+    shape[3] = plan.splits;
+    return SGEMM_OK;
 }

@@ -5,6 +5,21 @@
 
 namespace sgemm_impl {
 
+// How sgemm_w4 is laid out over the device (args_lowbit.cpp).
+struct W4Plan {
+    int few;     // 1: the kernel for few rows (16 rows by 16 wn columns a work-group); 0: the tile kernel
+    int mt, nt;  // tile kernel: a wave's tile is 32 mt rows by 32 nt columns
+    int wn, wk;  // waves of a work-group along N and along K
+    int slabs;   // few rows: runs of K whose A is held in LDS one after the other; 0: A goes straight to registers
+    int pitch;   // few rows: bytes from one held row to the next
+    int held;    // few rows: bytes of LDS for them
+};
+W4Plan plan_w4(int dtype, int M, int N, int K, int cus);
+
+// k that a wave of the kernel for few rows takes at a time, and its waves at most.
+constexpr int w4_step(bool f32) { return f32 ? 128 : 256; }
+constexpr int kRowsWaves = 16;
+
 // How attention is laid out over the device; from sizes the host knows
 // (args_lowbit.cpp), so that the workspace's size needs no device.
 struct Kv8Plan {

@@ -26,8 +26,7 @@
 namespace sgemm_impl {
 namespace {
 
-constexpr int kW4Chunk = 128;    // k that a wave takes at a time: 16 bytes of codes a lane
-constexpr int kRowsWaves = 16;   // waves of a work-group of the rows kernel at most
+constexpr int kW4Chunk = 128;  // k that a wave takes at a time: 16 bytes of codes a lane
 
 // (x & m) | c in one v_and_or_b32: with two constants that takes one of them
 // in a vector register, which the compiler does not do by itself.
@@ -323,7 +322,7 @@ template <class T, class ST, int GS, int U, bool ZP, bool Run, bool Held> struct
     Eight<T> a[Held ? 1 : 4 * U];  // Held: not used
 };
 
-// How a product is laid out over work-groups (launch_rows).
+// How a product is laid out over work-groups (plan_w4).
 struct W4Layout {
     int wn, wk;  // waves along N and along K
     int slabs;   // runs of K whose A is held in LDS, one after the other
@@ -340,7 +339,7 @@ struct W4Layout {
 // Held: a slab of A's rows lies in LDS as matrix operands, read by every wave
 // (and the runs are the slab's). Otherwise A comes straight to registers,
 // eight elements of a row for each lane and matrix instruction: no barriers,
-// but more loads in all. launch_rows chooses.
+// but more loads in all. plan_w4 chooses.
 //
 // Memory bounds it: 1 row of bf16 by 16384 x 4096 with zero points (35 MB)
 // takes 12.4 us on the device, 2.8 TB/s; 8 rows by 8192 x 8192 (34 MB) 15.8.
@@ -491,43 +490,20 @@ __global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W
     }
 }
 
-template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_rows(const W4Problem &p, hipStream_t stream)
+template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_rows(const W4Problem &p, const W4Plan &plan, hipStream_t stream)
 {
     constexpr int U = sizeof(typename T::elem) == 2 ? 2 : 1, kStep = kW4Chunk * U;
-    constexpr std::int64_t kLds = 160 * 1024;
-    W4Layout l;
-    // Waves along K while there are too few columns to fill the device.
-    std::int64_t tiles_n = (std::int64_t(p.N) + 15) / 16;
-    l.wn = 1;
-    while (l.wn < 4 && tiles_n >= 2 * l.wn * std::int64_t(p.cus)) l.wn *= 2;
-    // K in as few slabs as the LDS holds, of even length, each with a whole
-    // step for every wave. (A slab of one step and the rest always fits: 16
-    // float32 rows take 25 KB of it.)
-    const int steps = p.K / kStep, rest = p.K % kStep;
-    const auto held = [&](std::int64_t slab_steps) {  // bytes
-        const std::int64_t pitch = (2 * (slab_steps * kStep + (rest + 31) / 32 * 32) + 127) / 128 * 128 + 16;
-        l.pitch = int(pitch);
-        return AOperand<T>::kPlanes * p.M * pitch;
-    };
-    l.slabs = 1;
-    // A that does not fit at once goes straight to registers while there is at
-    // most one column tile for each compute unit: 16 rows of float32 by 4096
-    // columns, K = 4096, 13.5 us against 17.8, by 1024, K = 16384, 38.8 against
-    // 54.9, but by 8192, K = 8192, 41.8 against 32.8.
-    const bool straight = held(steps) > kLds && tiles_n <= p.cus;
-    while (!straight && l.slabs < steps && held((std::int64_t(steps) + l.slabs - 1) / l.slabs) > kLds) ++l.slabs;
-    std::size_t shared = straight ? 0 : std::size_t(held((std::int64_t(steps) + l.slabs - 1) / l.slabs));
-    l.wk = 1;
-    while (2 * l.wk * l.wn <= kRowsWaves && 2 * l.wk <= steps / l.slabs) l.wk *= 2;
-    const int waves = l.wn * l.wk, width = 16 * l.wn;
-    const std::size_t sums = std::size_t(waves) * 1024;
-    if (shared < sums) shared = sums;
-    tiles_n = (tiles_n + l.wn - 1) / l.wn;
+    static_assert(kStep == w4_step(AOperand<T>::kPlanes > 1), "the plan's step");
+    const bool straight = plan.slabs == 0;
+    W4Layout l{plan.wn, plan.wk, straight ? 1 : plan.slabs, plan.pitch};
+    const int steps = p.K / kStep, waves = l.wn * l.wk, width = 16 * l.wn;
+    const std::size_t sums = std::size_t(waves) * 1024, shared = std::size_t(plan.held) < sums ? sums : std::size_t(plan.held);
+    const std::int64_t tiles_n = (std::int64_t(p.N) + width - 1) / width;
     const void *kernel = steps == 0 ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, 1, ZP, U, true, false, true>)
                          : straight ? reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, GS, ZP, U, false, Run, false>)
                                     : reinterpret_cast<const void *>(&w4_rows_kernel<T, ST, GS, ZP, U, false, Run, true>);
     if (shared > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
+        const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != hipSuccess) return e;
     }
     // Bands of columns keep the launch under 2^32 work-items.
@@ -820,16 +796,12 @@ hipError_t launch_tile_shape(const W4Problem &p, hipStream_t stream)
     return hipSuccess;
 }
 
-template <class T, int GS, bool ZP, bool Run> hipError_t launch_tile(const W4Problem &p, hipStream_t stream)
+template <class T, int GS, bool ZP, bool Run> hipError_t launch_tile(const W4Problem &p, const W4Plan &plan, hipStream_t stream)
 {
-    // The largest tile that still gives every compute unit one; with fewer
-    // tiles the waves divide K. float32 rows take three times the LDS.
-    constexpr bool wide = AOperand<T>::kPlanes == 1;
-    const auto tiles = [&](int bm, int bn) { return (std::int64_t(p.M) + bm - 1) / bm * ((std::int64_t(p.N) + bn - 1) / bn); };
-    if (tiles(64, 256) >= p.cus) return launch_tile_shape<T, 2, 2, GS, ZP, Run, 4, 1>(p, stream);
-    if constexpr (wide) {
-        if (tiles(64, 64) >= 2 * p.cus) return launch_tile_shape<T, 2, 2, GS, ZP, Run, 1, 4>(p, stream);
-        if (p.M > 32) return launch_tile_shape<T, 2, 1, GS, ZP, Run, 1, 8>(p, stream);
+    if (plan.wn == 4) return launch_tile_shape<T, 2, 2, GS, ZP, Run, 4, 1>(p, stream);
+    if constexpr (AOperand<T>::kPlanes == 1) {
+        if (plan.nt == 2) return launch_tile_shape<T, 2, 2, GS, ZP, Run, 1, 4>(p, stream);
+        if (plan.mt == 2) return launch_tile_shape<T, 2, 1, GS, ZP, Run, 1, 8>(p, stream);
         return launch_tile_shape<T, 1, 1, GS, ZP, Run, 1, 8>(p, stream);
     } else {
         return launch_tile_shape<T, 1, 1, GS, ZP, Run, 1, 4>(p, stream);
@@ -838,11 +810,9 @@ template <class T, int GS, bool ZP, bool Run> hipError_t launch_tile(const W4Pro
 
 template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_shape(const W4Problem &p, hipStream_t stream)
 {
-    // Up to 8 rows (16 in float32, whose parts fill the tile kernel's LDS) the
-    // rows kernel is faster: 8192 x 8192 bf16, 8 rows 17.0 us against 17.7, 16
-    // rows 22.1 against 18.4; float32, 16 rows 32.8 against 41.5.
-    if (p.M <= (AOperand<T>::kPlanes == 1 ? 8 : 16)) return launch_rows<T, ST, GS, ZP, Run>(p, stream);
-    return launch_tile<T, GS, ZP, Run>(p, stream);
+    const int dtype = std::is_same<T, F32>::value ? SGEMM_F32 : std::is_same<T, BF16>::value ? SGEMM_LP_BF16 : SGEMM_LP_F16;
+    const W4Plan plan = plan_w4(dtype, p.M, p.N, p.K, p.cus);
+    return plan.few ? launch_rows<T, ST, GS, ZP, Run>(p, plan, stream) : launch_tile<T, GS, ZP, Run>(p, plan, stream);
 }
 
 template <class T, class ST, bool ZP> hipError_t launch_group(const W4Problem &p, hipStream_t stream)

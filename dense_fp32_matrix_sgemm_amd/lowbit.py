@@ -17,7 +17,7 @@ SGEMM_F32 = 0
 
 EXPORTS = ("sgemm_w4", "sgemm_w4_check_args", "sgemm_w4_quantize", "sgemm_w4_dequantize", "sgemm_w4_pack_check_args",
            "sgemm_kv8_write", "sgemm_kv8_read", "sgemm_kv8_check_args", "sgemm_kv8_attend",
-           "sgemm_kv8_attend_check_args", "sgemm_kv8_attend_workspace_size")
+           "sgemm_kv8_attend_check_args", "sgemm_kv8_attend_workspace_size", "sgemm_w4_shape", "sgemm_kv8_attend_shape")
 
 
 class KV8Cache(ctypes.Structure):
@@ -55,6 +55,9 @@ def declare(lib) -> None:
     lib.sgemm_kv8_attend_check_args.argtypes, lib.sgemm_kv8_attend_check_args.restype = attend, i
     lib.sgemm_kv8_attend_workspace_size.argtypes = [cache, batch, i, i, i]
     lib.sgemm_kv8_attend_workspace_size.restype = sz
+    lib.sgemm_w4_shape.argtypes, lib.sgemm_w4_shape.restype = [i, i, i, i, i, ctypes.POINTER(i)], i
+    lib.sgemm_kv8_attend_shape.argtypes = [cache, batch, i, i, i, ctypes.POINTER(i)]
+    lib.sgemm_kv8_attend_shape.restype = i
 
 
 _LIB = None
@@ -111,6 +114,26 @@ def sgemm_kv8_attend_check_args(*args) -> int:
 
 def sgemm_kv8_attend_workspace_size(*args) -> int:
     return int(_lib().sgemm_kv8_attend_workspace_size(*args))
+
+
+def _shape(entry, size, *args) -> tuple:
+    shape = (ctypes.c_int * size)()
+    rc = entry(*args, shape)
+    if rc:
+        from . import SgemmError
+
+        raise SgemmError(rc)
+    return tuple(shape)
+
+
+def sgemm_w4_shape(dtype, M, N, K, cus=0) -> tuple:
+    """Rows and columns of a work-group, waves along N and K, slabs of A."""
+    return _shape(_lib().sgemm_w4_shape, 5, dtype, M, N, K, cus)
+
+
+def sgemm_kv8_attend_shape(cache, batch, heads_q, window=0, cus=0) -> tuple:
+    """Rows of a wave's tile, row tiles of a work-group, work-groups along the rows, splits of the tokens."""
+    return _shape(_lib().sgemm_kv8_attend_shape, 4, cache, batch, heads_q, window, cus)
 
 
 # ------------------------------------------------------------ tensor helpers

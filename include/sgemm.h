@@ -419,6 +419,17 @@ int sgemm_w4_check_args(int dtype, int stype, int M, int N, int K, int group,
                         const float *C, int ldc);
 
 /*
+ * How sgemm_w4 lays a product out over a device with `cus` compute units (cus
+ * <= 0: 256), in shape[0..4]: the rows and columns of C that a work-group
+ * takes (16 rows: the kernel for few rows), its waves along N and along K, and
+ * for few rows the number of runs of K whose A it holds in LDS one after the
+ * other (0: A goes straight to registers; 1 for the larger tiles). Pure host
+ * logic. Returns SGEMM_OK, SGEMM_ERR_DTYPE, SGEMM_ERR_DIM or SGEMM_ERR_NULL
+ * (shape NULL).
+ */
+int sgemm_w4_shape(int dtype, int M, int N, int K, int cus, int *shape);
+
+/*
  * Quantises the N x K matrix B (dtype, row-major, ldb >= max(1, K)) to the W4
  * form. For each group of a row, with rounding to nearest, ties to even:
  *   without zeros (Z == NULL)  s = max |b| / 7, q = 8 + round(b / s) in 0..15;
@@ -589,6 +600,20 @@ int sgemm_kv8_attend_check_args(const sgemm_kv8_cache *cache, const sgemm_kv8_ba
  * split them (or the sizes are invalid). Pure host logic; reads no array. */
 size_t sgemm_kv8_attend_workspace_size(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int heads_q,
                                        int window, int cus);
+
+/*
+ * How sgemm_kv8_attend lays this call out on a device with `cus` compute units
+ * (cus <= 0: 256), in shape[0..3]: the rows (new rows times query heads of a
+ * cache head) of a wave's tile, the row tiles of a work-group (4: its waves
+ * take tiles of their own; 1: they share one tile's tokens), the work-groups
+ * along the rows of a sequence and head, and those that share one row tile's
+ * tokens (given the workspace). Pure host logic; reads no array. Returns
+ * SGEMM_OK, the cache's and batch's SGEMM_ERR_NULL, SGEMM_ERR_DIM or
+ * SGEMM_ERR_CACHE, SGEMM_ERR_HEADS, SGEMM_ERR_MASK (window negative) or
+ * SGEMM_ERR_NULL (shape NULL).
+ */
+int sgemm_kv8_attend_shape(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int heads_q, int window, int cus,
+                           int *shape);
 
 /* Static English text for a status code ("unknown status" otherwise). */
 const char *sgemm_status_string(int status);
