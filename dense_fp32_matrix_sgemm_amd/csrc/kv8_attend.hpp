@@ -123,6 +123,8 @@ template <class V> __device__ inline V uniform_load(const V *p, std::int64_t i)
 // The bytes of a word that are e4m3 NaN, as 0x80 in each such byte.
 __device__ inline std::uint32_t nan_codes(std::uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
+__device__ inline bool finite(float x) { return (f32_bits(x) & 0x7f800000u) != 0x7f800000u; }
+
 // Eight weights p * scale, p >= 0, as three bf16 parts that add up to them
 // exactly (split3 without its care for infinities: a weight that is not
 // finite makes its whole row NaN in any case).
@@ -155,6 +157,12 @@ struct Kv8Seen {
     std::int64_t first, len, nameable;  // position of new row 0, tokens, tokens that the table can name
     int R, causal, window;
     __device__ std::int64_t behind(std::int64_t row) const { return causal ? first + row / R + 1 : len; }
+    __device__ bool nothing(std::int64_t row) const
+    {
+        int from, count;
+        (*this)(row, from, count);
+        return count == 0;
+    }
     __device__ void operator()(std::int64_t row, int &from, int &count) const
     {
         const std::int64_t end = behind(row), begin = window > 0 ? end - window : 0;
@@ -167,8 +175,13 @@ struct Kv8Seen {
 };
 
 // Waves a SIMD has registers for: two, but for the longest heads and for two
-// groups of float32 rows (three parts of Q each).
-template <class T> constexpr int kv8_waves_per_simd(int DC, int MT) { return DC > 4 || (DC == 4 && MT == 2 && sizeof(typename T::elem) == 4) ? 1 : 2; }
+// groups of float32 rows (three parts of Q each); three for one group of
+// 16-bit rows (the plan counts on three work-groups a compute unit).
+template <class T> constexpr int kv8_waves_per_simd(int DC, int MT)
+{
+    constexpr bool f32 = sizeof(typename T::elem) == 4;
+    return DC > 4 || (DC == 4 && MT == 2 && f32) ? 1 : DC == 4 && MT == 1 && !f32 ? 3 : 2;
+}
 
 // DC: a head of up to 32 DC components; Full: of exactly that many. MT: groups
 // of 16 rows a wave holds. Rows: the four waves of a work-group take row tiles
@@ -318,8 +331,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                     load_keys(next);
                     bool poisoned = false;
                     if (Cut) {
-                        // NaN codes must not reach rows that do not see them (0 * NaN):
-                        // they leave the product and are put back below.
+                        // NaN codes and scales must not reach rows that do not see them
+                        // (0 * NaN): they leave the product and are put back below.
                         std::uint32_t any = 0;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -329,7 +342,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                                 any |= nan;
                                 v[e][i] &= ~((nan >> 7) * 0xffu);
                             }
-                        poisoned = __ballot(any != 0) != 0;
+                        poisoned = __ballot(any != 0) != 0 || !finite(now[0].vs) || !finite(now[1].vs);
                     }
                     Frag ph[MT], pm[MT], pl[MT];
 #pragma unroll
@@ -385,13 +398,12 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                     }
                     if (Cut && poisoned) {
                         for (int u = 0; u < 32; ++u) {
-                            const float vs = u < 16 ? now[0].vs : now[1].vs;
-                            if (vs != vs) continue;  // not read
+                            const bool all = !finite(u < 16 ? now[0].vs : now[1].vs);
                             const std::uint8_t *row = (u < 16 ? now[0].v : now[1].v) + (u % 16) * dim;
 #pragma unroll
                             for (int x = 0; x < 4 * kDTiles; ++x) {
                                 const int d = kq * 8 * DC + x;  // component of register x / kDTiles of d-tile x % kDTiles
-                                if (d >= dim || (row[d] & 0x7f) != 0x7f) continue;
+                                if (d >= dim || !(all || (row[d] & 0x7f) == 0x7f)) continue;
 #pragma unroll
                                 for (int t = 0; t < MT; ++t)
                                     if (unsigned(t0 + u - lo_t[t]) < unsigned(n_t[t])) o[t][x % kDTiles][x / kDTiles] = __builtin_nanf("");
@@ -419,7 +431,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                 for (int t = 0; t < MT; ++t) {
                     const std::int64_t row = row0 + 16 * t + c;
                     if (row >= all_rows) continue;
-                    float inverse = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+                    float inverse = n_t[t] == 0 ? 0.0f : 1.0f / l[t];  // a sum of 0 (scores all -inf) gives NaN
                     if (seen.beyond(row)) inverse = __builtin_nanf("");
                     float *dst = p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + kq * 8 * DC;
 #pragma unroll
@@ -477,7 +489,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                 f32x4 x = *reinterpret_cast<const f32x4 *>(&sm_o[i * kLd + d]);
                 if (whole) {
                     const std::int64_t row = row0 + i;
-                    x = sum == 0.0f ? f32x4{0, 0, 0, 0} : x / sum;
+                    x = seen.nothing(row) ? f32x4{0, 0, 0, 0} : x / sum;
                     if (seen.beyond(row)) x = x * __builtin_nanf("");
                     __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + d, &x, sizeof(x));
                 } else {
@@ -530,8 +542,8 @@ template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Atte
     }
     for (; x < splits; ++x) y += *reinterpret_cast<const f32x4 *>(at + x * pitch) * __shfl(a, x);
     if (4 * lane >= dim) return;
-    y = sum == 0.0f ? f32x4{0, 0, 0, 0} : y / sum;
     const Kv8Seen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) * p.c.block, R, p.causal, p.window};
+    y = seen.nothing(row) ? f32x4{0, 0, 0, 0} : y / sum;
     if (seen.beyond(row)) y = y * __builtin_nanf("");
     __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + 4 * lane, &y, sizeof(y));
 }

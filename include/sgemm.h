@@ -566,8 +566,9 @@ int sgemm_kv8_check_args(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *ba
  *   causal == 1, window == 0 tokens 0 .. p;
  *   causal == 1, window > 0  tokens p - window + 1 .. p.
  * A row that sees no token gets zeros; one that sees a token on a page that
- * is not the cache's gets NaN. Tokens a row does not see do not reach it, not
- * even as NaN.
+ * is not the cache's gets NaN, and so does one whose scores are all minus
+ * infinity, or one of them plus infinity or NaN. Tokens a row does not see do
+ * not reach it, not even as NaN.
  *
  * Q is rows x heads_q x dim (dtype), O the same in float32 (strides as for
  * sgemm_kv8_write). Sequences too few to fill the device are split along
