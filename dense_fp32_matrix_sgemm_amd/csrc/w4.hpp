@@ -812,11 +812,35 @@ template <class T, int GS, bool ZP, bool Run> hipError_t launch_tile(const W4Pro
     }
 }
 
+// k whose groups one wave adds up in one float32 sum at most: up to 2048 terms.
+// A longer sum would take on the roundings of all its terms, and stop growing
+// from 2^24 of them on.
+constexpr std::int64_t kW4SumK = 1 << 16;
+
 template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_shape(const W4Problem &p, hipStream_t stream)
 {
     const int dtype = std::is_same<T, F32>::value ? SGEMM_F32 : std::is_same<T, BF16>::value ? SGEMM_LP_BF16 : SGEMM_LP_F16;
     const W4Plan plan = plan_w4(dtype, p.M, p.N, p.K, p.cus);
-    return plan.few ? launch_rows<T, ST, GS, ZP, Run>(p, plan, stream) : launch_tile<T, GS, ZP, Run>(p, plan, stream);
+    const std::int64_t most = kW4SumK * plan.wk;
+    if (p.K <= most) return plan.few ? launch_rows<T, ST, GS, ZP, Run>(p, plan, stream) : launch_tile<T, GS, ZP, Run>(p, plan, stream);
+    // Longer K in pieces, each added to C: they end where a group ends, or lie inside one.
+    for (std::int64_t k0 = 0; k0 < p.K;) {
+        const std::int64_t left = p.group - k0 % p.group, inside = left < most ? left : most;
+        std::int64_t n = k0 % p.group != 0 || p.group > most ? inside : most / p.group * p.group;
+        if (n > p.K - k0) n = p.K - k0;
+        W4Problem q = p;
+        q.K = int(n);
+        q.A = static_cast<const char *>(p.A) + k0 * std::int64_t(sizeof(typename T::elem));
+        q.W = p.W + k0 / 2;  // k0 is a multiple of 32
+        q.S = static_cast<const char *>(p.S) + k0 / p.group * (p.stype == SGEMM_F32 ? 4 : 2);
+        if (p.Z) q.Z = p.Z + k0 / p.group;
+        if (k0 > 0) q.beta = 1.0f;
+        const W4Plan part = plan_w4(dtype, p.M, p.N, q.K, p.cus);
+        const hipError_t e = part.few ? launch_rows<T, ST, GS, ZP, Run>(q, part, stream) : launch_tile<T, GS, ZP, Run>(q, part, stream);
+        if (e != hipSuccess) return e;
+        k0 += n;
+    }
+    return hipSuccess;
 }
 
 template <class T, class ST, bool ZP> hipError_t launch_group(const W4Problem &p, hipStream_t stream)

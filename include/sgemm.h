@@ -390,9 +390,13 @@ int sgemm_lp_check_args(int dtype, int transA, int transB, int M, int N, int K,
  * max(1, N)), then (only if M > 0 and N > 0) NULL C and, when A and W are
  * read (K > 0 and alpha != 0), NULL A, W or S and overlap of C with A, W, S
  * or Z. beta == 0 never reads C. One kernel is enqueued (several for more
- * columns or rows than one launch takes, from 131072 on); nothing is
- * allocated. The result is the same on every run, and within 1e-5 * (|alpha|
- * sum_k |A[m][k]| |W[n][k]| + |beta c|) + 1e-6 of the exact value. A group's
+ * columns or rows than one launch takes, from 131072 on, or K over 65536);
+ * nothing is allocated. The result is the same on every run, and within
+ *     (1e-5 + 2^-29 min(K, 65536) + 2^-40 K) *
+ *         (|alpha| sum_k |A[m][k]| |W[n][k]| + |beta c|) + 1e-6
+ * of the exact value: a float32 sum of up to min(K, 65536) / 32 groups, each
+ * rounded by at most 2^-24, from 65536 k on several such sums added up in C,
+ * and the sums inside a group, of the waves, and with beta c. A group's
  * products with the whole numbers q - z are summed before its scale
  * multiplies them, so that sum |A[m][k] (q - z)| over a group has to stay
  * within float32's range, and float32 elements of A below 2^-110 may lose

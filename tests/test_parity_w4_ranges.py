@@ -39,3 +39,49 @@ def test_the_largest_scales(M, N, K, dtype):
             W = sg.W4(codes.cuda(), S, zeros, K, 32)
             C = sg.gemm_w4(a.to(TYPES[dtype]).cuda(), W, alpha=alpha).cpu().double()
             assert torch.equal(C, want), (stype, zeros is not None)
+
+
+def dense_of(codes, zeros, scales, K, group):
+    """The matrix in 64 bits, on the GPU."""
+    g = torch.arange(K, device="cuda") // group
+    q = torch.stack((codes & 15, codes >> 4), dim=2).flatten(1)[:, :K].double()
+    return (q - (8.0 if zeros is None else zeros.double()[:, g])) * scales.double()[:, g]
+
+
+# K in pieces: ends inside groups, groups longer than a piece, every kernel, float32's three parts, an odd end.
+@pytest.mark.parametrize("M,N,K,group,zeros,dtype", [
+    (1030, 4100, 65536 + 305, 96, True, "bf16"), (1030, 4100, 140001, 131072, True, "f16"), (1030, 4100, 131072 + 33, 32, False, "f32"),
+    (1030, 4100, 3 * 65536, 64, False, "bf16"), (257, 8200, 4 * 65536 + 97, 128, True, "f16"), (50, 40, 8 * 65536 + 500, 160, False, "bf16"),
+    (20, 40, 8 * 65536 + 31, 2**20, True, "f16"), (20, 40, 4 * 65536 + 1001, 32, True, "f32"), (2, 16, 16 * 65536 + 777, 64, True, "bf16"),
+    (16, 20, 16 * 65536 + 1001, 128, False, "f32")])
+def test_k_in_pieces(M, N, K, group, zeros, dtype):
+    print(f"[w4 ranges] {M}x{N}x{K} group={group} zeros={zeros} {dtype}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    A = torch.randint(-4, 5, (M, K), generator=g, device="cuda", dtype=torch.int8).to(TYPES[dtype])
+    codes = torch.randint(0, 256, (N, -(-K // 2)), generator=g, device="cuda", dtype=torch.uint8)
+    S = torch.tensor([0.5, 1.0, 2.0], device="cuda")[torch.randint(0, 3, (N, -(-K // group)), generator=g, device="cuda")]
+    Z = torch.randint(6, 10, S.shape, generator=g, device="cuda", dtype=torch.uint8) if zeros else None
+    C0 = torch.randint(-9, 10, (M, N), generator=g, device="cuda").float()
+    want = -0.5 * torch.matmul(A.double(), dense_of(codes, Z, S, K, group).t()) + 2.0 * C0.double()
+    assert want.abs().max() < 2**21  # quarters below 2^22: float32 holds every partial sum
+    W = sg.W4(codes, S, Z, K, group)
+    C = C0.clone()
+    sg.gemm_w4(A, W, C, -0.5, 2.0)
+    assert torch.equal(C.double(), want)
+    C.fill_(float("nan"))
+    assert torch.equal(sg.gemm_w4(A, W, C, -0.5, 0.0).double(), want - 2.0 * C0.double())
+
+
+# Terms of one sign, the same everywhere: the roundings of a long sum all go one way.
+@pytest.mark.parametrize("M,N,K,dtype", [(1030, 4100, 65536, "bf16"), (1030, 4100, 2**20, "bf16"), (1030, 4100, 2**18, "f32"), (20, 96, 2**24, "f16"),
+                                         (2, 16, 2**25, "bf16"), (16, 20, 2**24, "f32")])
+def test_long_sums_of_one_sign(M, N, K, dtype):
+    print(f"[w4 ranges] one sign {M}x{N}x{K} {dtype}", flush=True)
+    A = torch.full((M, K), 0.7, dtype=TYPES[dtype], device="cuda")
+    S = torch.full((N, K // 32), 0.013, dtype=torch.bfloat16, device="cuda")
+    W = sg.W4(torch.full((N, K // 2), 0xFF, dtype=torch.uint8, device="cuda"), S, None, K, 32)
+    exact = K * A[0, 0].double().item() * 7 * S[0, 0].double().item()
+    C = sg.gemm_w4(A, W).double()
+    worst = ((C - exact).abs().max() / exact).item()
+    print(f"[w4 ranges] worst {worst:.2e}", flush=True)
+    assert worst <= 1e-5 + 2.0**-29 * min(K, 65536) + 2.0**-40 * K
