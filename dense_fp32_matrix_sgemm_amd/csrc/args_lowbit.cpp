@@ -191,6 +191,19 @@ bool kv8_read_overlaps(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int d
     return overlap(k, v) || overlaps_batch(k, &b) || overlaps_batch(v, &b);
 }
 
+bool kv8_write_overlaps(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b)
+{
+    const i64 ph = i64(c.pages) * c.heads, codes = i64(c.block) * c.dim;
+    const Span own[] = {span_of(c.K, ph, codes, codes, 1), span_of(c.V, ph, codes, codes, 1), span_of(c.Ks, 1, ph, ph, 4),
+                        span_of(c.Vs, 1, ph, ph, 4)};
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps_batch(own[i], &b)) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlap(own[i], own[j])) return true;
+    }
+    return false;
+}
+
 W4Plan plan_w4(int dtype, int M, int N, int K, int cus)
 {
     cus = cus <= 0 ? 256 : cus;

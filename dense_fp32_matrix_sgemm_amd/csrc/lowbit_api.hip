@@ -68,6 +68,7 @@ extern "C" int sgemm_kv8_write(const sgemm_kv8_cache *cache, const sgemm_kv8_bat
     const int rc = sgemm_kv8_check_args(cache, batch, dtype, K, ldk, hsk, V, ldv, hsv);
     if (rc != SGEMM_OK) return rc;
     if (batch->seqs == 0 || batch->rows == 0) return SGEMM_OK;
+    if (sgemm_impl::kv8_write_overlaps(*cache, *batch)) return SGEMM_ERR_ALIAS;
     if (sgemm_impl::current_gfx950_cus() == 0) return SGEMM_ERR_DEVICE;
     const sgemm_impl::Kv8Problem p{*cache, *batch, const_cast<void *>(K), const_cast<void *>(V), ldk, hsk, ldv, hsv, dtype};
     return status_of(sgemm_impl::launch_kv8_write(p, static_cast<hipStream_t>(stream)));

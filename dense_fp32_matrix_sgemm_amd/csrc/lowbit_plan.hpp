@@ -35,4 +35,8 @@ Kv8Plan plan_kv8_attend(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int 
 bool kv8_read_overlaps(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int dtype, const void *K, int ldk, int hsk,
                        const void *V, int ldv, int hsv);
 
+// Whether the cache's arrays overlap one another or the batch's: two writers,
+// or a table that changes while it is read.
+bool kv8_write_overlaps(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b);
+
 }  // namespace sgemm_impl

@@ -358,7 +358,8 @@ class KV8:
     ``Vs`` (float32, pages x heads), one scale for each page and head. The
     tensors are used in place and belong to the KV8 for good (what they hold
     may change). ``block`` is a power of two from 16 to 1024 and ``dim`` a
-    multiple of 16 up to 256."""
+    multiple of 16 up to 256. K and V may be one tensor (so may Ks and Vs) to
+    read and attend, but not for :func:`kv8_write`."""
 
     __slots__ = ("_tensors", "_struct", "_device", "_heads", "_dim")
 

@@ -534,8 +534,10 @@ typedef struct sgemm_kv8_batch {
  * max_new), cache (block, dim, alignment), strides (elements must not share
  * places: heads inside a row, hs >= dim and ld >= (heads - 1) * hs + dim, or
  * rows inside a head, ld >= dim and hs >= (rows - 1) * ld + dim), then (seqs
- * > 0 and rows > 0) NULL pointers and overlap of the operand with the cache.
- * One kernel is enqueued.
+ * > 0 and rows > 0) NULL pointers and overlap of the operand with the cache;
+ * sgemm_kv8_write() alone also refuses a cache whose arrays overlap one another
+ * or the batch's (keys that are the values as well may be read and attended
+ * over, but would have two writers). One kernel is enqueued.
  */
 int sgemm_kv8_write(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype,
                     const void *K, int ldk, int hsk,
@@ -545,14 +547,15 @@ int sgemm_kv8_write(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, 
 /* The last rows of each sequence read back: code * scale in float32, rounded
  * to dtype, into K and V (rows x heads x dim, strides as above). A row whose
  * page is not one of the cache's reads NaN; a row before token 0 is left as
- * it was. The same checks. */
+ * it was. The same checks; outputs that overlap each other or the batch's
+ * arrays are refused as well. */
 int sgemm_kv8_read(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype,
                    void *K, int ldk, int hsk,
                    void *V, int ldv, int hsv,
                    void *stream);
 
-/* The host-side argument checks of sgemm_kv8_write() and sgemm_kv8_read()
- * alone. */
+/* The host-side argument checks that sgemm_kv8_write() and sgemm_kv8_read()
+ * share. */
 int sgemm_kv8_check_args(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int dtype,
                          const void *K, int ldk, int hsk,
                          const void *V, int ldv, int hsv);
