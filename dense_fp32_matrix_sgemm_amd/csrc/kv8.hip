@@ -111,6 +111,13 @@ __device__ inline float scale_for(std::uint32_t amax)
     return bits_f32(std::uint32_t(field < 1 ? 1 : field) << 23);
 }
 
+// Whether s > 0 is a power of two with a normal inverse.
+__device__ inline bool exact_inverse(float s)
+{
+    const std::uint32_t u = f32_bits(s), e = u >> 23;
+    return (u & 0x7fffffu) == 0 && e >= 1 && e <= 253;
+}
+
 __device__ inline std::uint32_t to_codes(float a, float b, float c, float d)
 {
     const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -166,6 +173,9 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(
         for (int i = 0; i < kThreads / 64; ++i) m = wave_max[i] > m ? wave_max[i] : m;
         const float s = __builtin_fmaxf(scale_for(m), before);
         const float inverse = s > 0.0f ? 1.0f / s : 0.0f;
+        // A scale that this kernel left is a power of two, whose inverse is
+        // exact; one that a caller set need not be (or have an inverse).
+        const bool power = __builtin_amdgcn_readfirstlane(s == 0.0f || exact_inverse(s)) != 0;
 
         if (s != before) {
             // The page's earlier tokens, rounded to the risen scale.
@@ -185,10 +195,17 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv8_write_kernel(
         auto store = [&](const Eight<T> &v, int r) {
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = to_f32<T>(v.x[i]);
-                x[i] = (f32_bits(a) & 0x7f800000u) == 0x7f800000u ? __builtin_nanf("") : a * inverse;
+            for (int i = 0; i < 8; ++i) x[i] = to_f32<T>(v.x[i]);
+            if (power) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= inverse;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] /= s;
             }
+            // Finite quotients are at most 448.
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = (f32_bits(x[i]) & 0x7f800000u) == 0x7f800000u ? __builtin_nanf("") : x[i];
             *reinterpret_cast<u32x2 *>(codes + (kept + r) * dim) = u32x2{to_codes(x[0], x[1], x[2], x[3]), to_codes(x[4], x[5], x[6], x[7])};
         };
 #pragma unroll

@@ -526,7 +526,9 @@ typedef struct sgemm_kv8_batch {
  *           not finite); when the scale rises, the earlier tokens' codes are
  *           rounded to the new one.
  * With powers of two that last rounding changes only values that fall among
- * e4m3's subnormals. A page that receives rows must belong to one sequence
+ * e4m3's subnormals. (A page's scale that the caller set to something else is
+ * used as it is; x / scale, and old scale / new scale times an earlier code,
+ * are then rounded to float32 before they are to e4m3.) A page that receives rows must belong to one sequence
  * and appear once in its row of the table: two writers leave codes and scale
  * of that page undefined (nothing else).
  *
