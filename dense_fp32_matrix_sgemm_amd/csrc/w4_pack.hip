@@ -111,11 +111,11 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
         // Every lane of the group rounds the scale; the first stores it.
         if (p.stype == SGEMM_LP_BF16) s = to_f32<BF16>(from_f32<BF16>(s));
         if (p.stype == SGEMM_LP_F16) s = to_f32<F16>(from_f32<F16>(s));
-        const bool flat = !(s > 0.0f) || __builtin_isinf(s);
+        const bool endless = __builtin_isinf(s), flat = !(s > 0.0f) || endless;
         // Quotients are formed on values moved away from the subnormals.
         const float up = s < 0x1p-90f ? 0x1p90f : 1.0f, scale = s * up;
         const float inverse = flat ? 0.0f : 1.0f / scale;
-        float z = 8.0f;
+        float z = ZP && endless ? 0.0f : 8.0f;  // every quotient by an infinite scale is 0
         if (ZP && !flat) {
             const float low = -lo * up;
             rounded_quotients<1>(&low, scale, inverse, &z);
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(W4PackProblem p, 
             std::uint32_t w = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) w |= std::uint32_t(__builtin_amdgcn_fmed3f(q[i] + z, 0.0f, 15.0f)) << (4 * i);
-            w = flat ? 0x88888888u : w;
+            w = flat ? (ZP && endless ? 0u : 0x88888888u) : w;
             if (k + 8 > k1) w &= (1u << (4 * (k1 - k))) - 1u;  // past the row's end: 0
             std::uint8_t *dst = p.W + n * p.ldw + k / 2;
             if (k + 8 <= k1) {

@@ -442,7 +442,8 @@ int sgemm_w4_shape(int dtype, int M, int N, int K, int cus, int *shape);
  *                              q = z + round(b / s) in 0..15.
  * hi - lo and the quotient that gives s are rounded to float32 and s then to
  * stype; the other quotients are by that stored s and rounded once. s == 0
- * gives codes (and z) of 8. A group that holds a value that is not finite
+ * gives codes (and z) of 8. An s that overflows is infinite: its quotients are
+ * 0, and what is read back or multiplied is NaN. A group that holds a value that is not finite
  * gets the scale NaN and codes of 8, so that products with it show it.
  *
  * Checks: types, sizes, group, leading dimensions, then (N > 0 and K > 0)
