@@ -157,12 +157,6 @@ struct Kv8Seen {
     std::int64_t first, len, nameable;  // position of new row 0, tokens, tokens that the table can name
     int R, causal, window;
     __device__ std::int64_t behind(std::int64_t row) const { return causal ? first + row / R + 1 : len; }
-    __device__ bool nothing(std::int64_t row) const
-    {
-        int from, count;
-        (*this)(row, from, count);
-        return count == 0;
-    }
     __device__ void operator()(std::int64_t row, int &from, int &count) const
     {
         const std::int64_t end = behind(row), begin = window > 0 ? end - window : 0;
@@ -175,13 +169,8 @@ struct Kv8Seen {
 };
 
 // Waves a SIMD has registers for: two, but for the longest heads and for two
-// groups of float32 rows (three parts of Q each); three for one group of
-// 16-bit rows (the plan counts on three work-groups a compute unit).
-template <class T> constexpr int kv8_waves_per_simd(int DC, int MT)
-{
-    constexpr bool f32 = sizeof(typename T::elem) == 4;
-    return DC > 4 || (DC == 4 && MT == 2 && f32) ? 1 : DC == 4 && MT == 1 && !f32 ? 3 : 2;
-}
+// groups of float32 rows (three parts of Q each).
+template <class T> constexpr int kv8_waves_per_simd(int DC, int MT) { return DC > 4 || (DC == 4 && MT == 2 && sizeof(typename T::elem) == 4) ? 1 : 2; }
 
 // DC: a head of up to 32 DC components; Full: of exactly that many. MT: groups
 // of 16 rows a wave holds. Rows: the four waves of a work-group take row tiles
@@ -311,7 +300,13 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                 constexpr int kStride = Rows ? 1 : kAttendWaves;
                 int turn = from + (Rows ? 0 : (wave - from) & (kAttendWaves - 1));
                 if (turn >= to) return;
-                Half now[2] = {half_at(32 * turn), half_at(32 * turn + 16)};
+                // A scale of V that is not finite makes every row that sees the page NaN, whatever its weights: by
+                // the scores, of which a row takes those that it sees.
+                auto checked = [](Half h) {
+                    if (!finite(h.vs)) h.ks = __builtin_nanf("");
+                    return h;
+                };
+                Half now[2] = {checked(half_at(32 * turn)), checked(half_at(32 * turn + 16))};
                 load_keys(now);
                 load_values(now);
                 for (; turn < to; turn += kStride) {
@@ -331,8 +326,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                     load_keys(next);
                     bool poisoned = false;
                     if (Cut) {
-                        // NaN codes and scales must not reach rows that do not see them
-                        // (0 * NaN): they leave the product and are put back below.
+                        // NaN codes must not reach rows that do not see them (0 * NaN):
+                        // they leave the product and are put back below.
                         std::uint32_t any = 0;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -342,7 +337,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                                 any |= nan;
                                 v[e][i] &= ~((nan >> 7) * 0xffu);
                             }
-                        poisoned = __ballot(any != 0) != 0 || !finite(now[0].vs) || !finite(now[1].vs);
+                        poisoned = __ballot(any != 0) != 0;
                     }
                     Frag ph[MT], pm[MT], pl[MT];
 #pragma unroll
@@ -398,12 +393,13 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                     }
                     if (Cut && poisoned) {
                         for (int u = 0; u < 32; ++u) {
-                            const bool all = !finite(u < 16 ? now[0].vs : now[1].vs);
+                            const float vs = u < 16 ? now[0].vs : now[1].vs;
+                            if (vs != vs) continue;  // NaN already
                             const std::uint8_t *row = (u < 16 ? now[0].v : now[1].v) + (u % 16) * dim;
 #pragma unroll
                             for (int x = 0; x < 4 * kDTiles; ++x) {
                                 const int d = kq * 8 * DC + x;  // component of register x / kDTiles of d-tile x % kDTiles
-                                if (d >= dim || !(all || (row[d] & 0x7f) == 0x7f)) continue;
+                                if (d >= dim || (row[d] & 0x7f) != 0x7f) continue;
 #pragma unroll
                                 for (int t = 0; t < MT; ++t)
                                     if (unsigned(t0 + u - lo_t[t]) < unsigned(n_t[t])) o[t][x % kDTiles][x / kDTiles] = __builtin_nanf("");
@@ -411,8 +407,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                         }
                     }
                     load_values(next);
-                    now[0] = next[0];
-                    now[1] = next[1];
+                    now[0] = checked(next[0]);
+                    now[1] = checked(next[1]);
                 }
             };
             if (inner < outer) {
@@ -424,14 +420,18 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                 turns(begin, end, std::true_type{});
             }
 #pragma unroll
-            for (int t = 0; t < MT; ++t) l[t] = column_sum(l[t]);
+            for (int t = 0; t < MT; ++t) {
+                // A row that sees no token is 0 / 1; one whose scores are all -inf is 0 / 0.
+                const float sum = column_sum(l[t]);
+                l[t] = n_t[t] == 0 ? 1.0f : sum;
+            }
 
             if constexpr (Rows) {
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     const std::int64_t row = row0 + 16 * t + c;
                     if (row >= all_rows) continue;
-                    float inverse = n_t[t] == 0 ? 0.0f : 1.0f / l[t];  // a sum of 0 (scores all -inf) gives NaN
+                    float inverse = 1.0f / l[t];
                     if (seen.beyond(row)) inverse = __builtin_nanf("");
                     float *dst = p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + kq * 8 * DC;
 #pragma unroll
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
                 f32x4 x = *reinterpret_cast<const f32x4 *>(&sm_o[i * kLd + d]);
                 if (whole) {
                     const std::int64_t row = row0 + i;
-                    x = seen.nothing(row) ? f32x4{0, 0, 0, 0} : x / sum;
+                    x = x / sum;
                     if (seen.beyond(row)) x = x * __builtin_nanf("");
                     __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + d, &x, sizeof(x));
                 } else {
@@ -525,7 +525,7 @@ template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Atte
     float top = m;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    // A split that saw nothing weighs nothing, and its components were left as sums of nothing: zeros.
+    // A split that saw nothing of its row weighs nothing, and its components were left as sums of nothing: zeros.
     const float a = l == 0.0f ? 0.0f : rescale(m, top);
     float sum = l * a;
 #pragma unroll
@@ -542,8 +542,8 @@ template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Atte
     }
     for (; x < splits; ++x) y += *reinterpret_cast<const f32x4 *>(at + x * pitch) * __shfl(a, x);
     if (4 * lane >= dim) return;
+    y = y / sum;
     const Kv8Seen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) * p.c.block, R, p.causal, p.window};
-    y = seen.nothing(row) ? f32x4{0, 0, 0, 0} : y / sum;
     if (seen.beyond(row)) y = y * __builtin_nanf("");
     __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + 4 * lane, &y, sizeof(y));
 }
