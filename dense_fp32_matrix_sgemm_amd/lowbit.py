@@ -457,7 +457,9 @@ def kv8_read(cache, table, lens, starts, rows=None, dtype=None, K=None, V=None, 
     """The last ``starts[b + 1] - starts[b]`` tokens of each sequence read
     back: (K, V), each rows x heads x dim of ``dtype`` (float32 by default).
     Either ``rows`` (``starts[-1]``, known to the host) or both outputs have
-    to be given."""
+    to be given. Rows outside the sequences, and rows before token 0, stay as
+    they are in given outputs; in new ones they hold whatever was in the
+    memory."""
     import torch
 
     if not isinstance(cache, KV8):
@@ -485,8 +487,9 @@ def kv8_attend(Q, cache, table, lens, starts, scale=None, causal=True, window=0,
     sees the tokens up to it (``causal``), the last ``window`` of those
     (``window`` > 0), or all of the sequence (not ``causal``). Query heads are
     a multiple of the cache's heads; ``scale`` is 1 / sqrt(dim) by default.
-    A row that sees nothing is zero; rows outside the sequences stay as they
-    are in ``out``. table, lens, starts and ``max_new`` are as for
+    A row that sees nothing is zero. Rows outside the sequences (a batch
+    padded behind ``starts[-1]``) stay as they are in ``out``; in a new output
+    they hold whatever was in the memory. table, lens, starts and ``max_new`` are as for
     :func:`kv8_write`. ``workspace`` (a contiguous tensor of
     sgemm_kv8_attend_workspace_size() bytes, used by one stream at a time) is
     allocated when None.

@@ -362,7 +362,8 @@ int sgemm_lp_check_args(int dtype, int transA, int transB, int M, int N, int K,
  * float32 and results are float32; codes enter the matrix cores as the whole
  * numbers (W4) or floats (KV8) they stand for, which the 16-bit types hold
  * exactly, and scales multiply the float32 sums. float32 operands enter as
- * three bf16 parts that add up to them exactly.
+ * three bf16 parts that add up to them exactly (below 2^-110 their last bits
+ * may be lost).
  *
  * The W4 form of an N x K matrix W, in groups of `group` k of a row (a
  * positive multiple of 32; the last group of a row may be shorter; K at most
@@ -502,7 +503,9 @@ typedef struct sgemm_kv8_cache {
  * rows; rows at positions before token 0 have no token; a page outside 0 ..
  * pages - 1, or a token behind the table's last column, is never read or
  * written. Rows of the operand before starts[0] or from starts[seqs] on are
- * left as they were.
+ * left as they were. Where starts fall and rise again, a row that two
+ * sequences cover takes part in both; as an output it holds either's result,
+ * element by element.
  */
 typedef struct sgemm_kv8_batch {
     const int *table;   /* seqs x table_ld page numbers                         */
@@ -579,6 +582,11 @@ int sgemm_kv8_check_args(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *ba
  * is not the cache's gets NaN, and so does one whose scores are all minus
  * infinity, or one of them plus infinity or NaN. Tokens a row does not see do
  * not reach it, not even as NaN.
+ *
+ * Scores are <Q, code> in float32 times scale * log2(e) * K's scale, and values
+ * are multiplied by p * V's scale in three bf16 parts: <Q, code> and scale *
+ * log2(e) * K's scale have to stay within float32's normal numbers, and weights
+ * below 2^-110 may lose their last bits.
  *
  * Q is rows x heads_q x dim (dtype), O the same in float32 (strides as for
  * sgemm_kv8_write). Sequences too few to fill the device are split along
