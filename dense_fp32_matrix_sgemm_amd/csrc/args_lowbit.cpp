@@ -210,8 +210,11 @@ W4Plan plan_w4(int dtype, int M, int N, int K, int cus)
     const bool f32 = dtype == SGEMM_F32;
     W4Plan plan = {};
     // Up to 8 rows (16 in float32, whose parts fill the tile kernel's LDS) the
-    // rows kernel is faster: 8192 x 8192 bf16, 8 rows 17.0 us against 17.7, 16
-    // rows 22.1 against 18.4; float32, 16 rows 32.8 against 41.5.
+    // rows kernel is faster: bf16, 8 rows by 8192 x 8192 16.2 us against 17.2,
+    // 4096 x 4096 8.0 against 9.0, 16384 x 4096 14.1 against 18.4; float32, 16
+    // rows 32.1 against 40.5, 13.2 against 21.0, 24.0 against 40.6. From 9 to
+    // 16 bf16 rows it depends on the width: 16 rows by 8192 x 8192 21.2 against
+    // 18.3, 4096 x 4096 9.9 against 9.2, but 16384 x 4096 16.8 against 18.8.
     if (M > (f32 ? 16 : 8)) {
         // The largest tile that still gives every compute unit one; with fewer
         // tiles the waves divide K. float32 rows take three times the LDS.

@@ -9,11 +9,13 @@
 // Work is laid out by what shares a scale: one work-group for each sequence,
 // page that the sequence's rows reach, head, and K or V. It alone reads and
 // writes that scale and those codes, so nothing is atomic and the result does
-// not depend on timing. Both kernels are bound by memory: rows come in once
-// (what does not stay in registers until the maximum is known is read again,
-// from the caches). 4 prompts of up to 4096 rows in bf16 (about 100 MB):
-// writing 20.2 us, 5 TB/s, reading back 15.4; 64 sequences of one new token
-// each: 6.3, round trips, and their last tokens read back in float32 17.5.
+// not depend on timing. Rows come in once (what does not stay in registers
+// until the maximum is known is read again, from the caches). 4 prompts of up
+// to 4096 rows in bf16 (11674 rows, 72 MB): reading back 15.3 us, 4.7 TB/s,
+// bound by memory; writing 18.9 us, 3.8 TB/s: a work-group's loads and stores
+// lie on either side of a barrier and its vector instructions take over half
+// of the time. 64 sequences of one new token each: 6.5, round trips, and their
+// last tokens read back in float32 17.5 to 18.8.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -187,10 +187,13 @@ template <class T> constexpr int kv8_waves_per_simd(int DC, int MT) { return DC 
 // page 0 and their scores by NaN.
 //
 // 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 query heads each
-// (0.41 GB): 84.8 us, 4.8 TB/s, bound by memory. 2 prompts of 1024 rows behind
+// (0.41 GB): 82.6 us, 4.9 TB/s, bound by memory. 2 prompts of 1024 rows behind
 // 4096 tokens in f16: 260 us, 460 TFLOP/s, bound by the SIMDs: matrix
 // instructions take 43% of the cycles a compute unit is busy, the softmax and
-// the conversion of codes 55%.
+// the conversion of codes 55%. No vector register is spilled; the table,
+// scales and addresses take more scalar registers than there are (29 to 284 go
+// to vector registers; for padded heads of 144 to 240 components 48 bytes a
+// lane go to scratch).
 template <class T, int DC, bool Full, int MT, bool Rows>
 __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) void kv8_attend_kernel(Kv8AttendProblem p)
 {

@@ -342,11 +342,13 @@ struct W4Layout {
 // eight elements of a row for each lane and matrix instruction: no barriers,
 // but more loads in all. plan_w4 chooses.
 //
-// Memory bounds it: 1 row of bf16 by 16384 x 4096 with zero points (35 MB)
-// takes 12.4 us on the device, 2.8 TB/s; 8 rows by 8192 x 8192 (34 MB) 15.8.
-// Of the 12.4 us the loads alone take 8.7 and A's way to LDS 1, neither of
-// which more loads in flight shortened (A or codes, one to three steps
-// further ahead: 13.9 to 16.7 us).
+// 1 row of bf16 by 16384 x 4096 with zero points (35 MB) takes 12.5 us on the
+// device, 2.8 TB/s; 8 rows by 8192 x 8192 (34 MB) 15.8. Of the 12.5 us the
+// loads alone take 8.7 and A's way to LDS 1, neither of which more loads in
+// flight shortened (A or codes, one to three steps further ahead: 13.9 to 16.7
+// us). With few columns most compute units have no work-group (K is not divided
+// over work-groups): 13 rows of float32 by 2047 x 4093 use 128 of 256 and take
+// 13.7 us for 5.8 MB, 16 rows by 1024 x 16384 use 64 and take 38.7 for 9.7 MB.
 template <class T, class ST, int GS, bool ZP, int U, bool Short, bool Run, bool Held>
 __global__ __launch_bounds__(64 * kRowsWaves) void w4_rows_kernel(W4Problem p, W4Layout l)
 {
@@ -545,10 +547,14 @@ template <class T, class ST, int GS, bool ZP, bool Run> hipError_t launch_rows(c
 // The matrix cores bound it: what shares their time is the conversion (7
 // cycles a code and column, so tall tiles) and the reads of A from LDS (4
 // cycles a row and 64 k for four waves against MT NT matrix instructions, so
-// wide ones). 2048 x 4096 x 4096 in bf16: 86 us in a run of calls (800
-// TFLOP/s), 99 in a replayed graph; matrix instructions take 37% of the cycles
+// wide ones). 2048 x 4096 x 4096 in bf16: 85 us in a run of calls (810
+// TFLOP/s), 98 in a replayed graph; matrix instructions take 37% of the cycles
 // a compute unit is busy, the other vector instructions 53%. 128 x 64 a wave,
 // one wave a SIMD: 121 us; 16x16x32 instructions: 571.
+// The shared-slab tile takes all 256 registers of two waves a SIMD: with 16-bit
+// rows it spills 5 to 20 vector registers (24 to 84 bytes of scratch a lane) for
+// groups of 128 and more, 1 to 15 for groups of 32 or 96 with zero points, none
+// for the others; float32 rows have a SIMD to themselves and spill none.
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 template <class T> __device__ inline f32x16 mfma32(const Frag &a, const Frag &b, f32x16 c)
 {
