@@ -82,3 +82,21 @@ def test_a_nan_scale_meets_scores_of_minus_infinity(heads, new):
             seen = V[:min(position + 1, 16)]
             # equal weights of 1: a float32 sum of up to 16 values and a division
             assert (np.abs(got[i] - seen.mean(axis=0)) <= 20 * 2.0**-24 * np.abs(seen).mean(axis=0)).all(), i
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 400), (False, 0)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rows_that_see_nothing_beside_split_sequences(dtype, causal, window):
+    # Long sequences are split over work-groups; the short ones between them have rows before token 0, or no token at all.
+    case = Case(37, [3000, 3, 0, 2500, 1], [4, 9, 5, 1, 2], 1, 32, 128)
+    cache, args = case.device(), case.args()
+    Q = case.normal(3, dtype)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        batch = sg.lowbit._batch(cache, *args, case.rows, 9)
+        assert sg.sgemm_kv8_attend_shape(cache._struct, batch, 3, window, 256)[3] == (1 if window else 11)
+    O, bound = case.ref.attend(Q.double().numpy(), case.table, case.lens, case.starts, 0.1, causal, window)
+    if causal:
+        assert (O[4:10] == 0).all() and (O[13:18] == 0).all() and (O[19] == 0).all()
+    for workspace in (None, torch.empty(0, device="cuda")):
+        got = sg.kv8_attend(Q.cuda(), cache, *args, scale=0.1, causal=causal, window=window, max_new=9, workspace=workspace)
+        close(got.cpu().double().numpy(), O, bound, f"{dtype} workspace={workspace is None}")

@@ -85,3 +85,31 @@ def test_long_sums_of_one_sign(M, N, K, dtype):
     worst = ((C - exact).abs().max() / exact).item()
     print(f"[w4 ranges] worst {worst:.2e}", flush=True)
     assert worst <= 1e-5 + 2.0**-29 * min(K, 65536) + 2.0**-40 * K
+
+
+@pytest.mark.parametrize("M,N,K", [(20, 40, 8 * 65536 + 500), (1030, 4100, 65536 + 300)])
+def test_pieces_in_a_captured_graph(M, N, K):
+    # Several launches that follow from one another through C: every replay on new inputs agrees with the call itself.
+    g = torch.Generator(device="cuda").manual_seed(M)
+    A = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    W = sg.W4(codes, torch.rand(N, -(-K // 128), generator=g, device="cuda"), None, K, 128)
+    out, eager = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    A.normal_(generator=g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sg.gemm_w4(A, W, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sg.gemm_w4(A, W, out)
+    for replay in range(3):
+        A.normal_(generator=g)
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        sg.gemm_w4(A, W, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.isfinite(out).all(), replay
+    del graph
