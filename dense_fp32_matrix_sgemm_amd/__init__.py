@@ -46,6 +46,17 @@ points sgemm_w4*, sgemm_kv8* with the C ABI's arguments):
     kv8_read(cache, table, lens, starts, rows=None, ...) -> K, V
     kv8_attend(Q, cache, table, lens, starts, scale=None, causal=True,
                window=0, out=None, max_new=None, workspace=None) -> O
+
+A serving step over such a cache (step.py; raw entry points sgemm_kv4*,
+sgemm_rope and sgemm_kv_tables):
+    kv_tables(table, lens, new, pool, taken, block, rows)
+        -> starts, positions, slots, taken_after
+    rope_frequencies(rot, base=10000.0, stretch=1.0, original=None)
+        -> freqs, amplitude
+    rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0,
+         inverse=False, dtype=None, out=None) -> Q', K'
+    KV4(K, V, Ks, Vs), KV4.empty(pages, heads, block, dim) -> cache in 4 bits
+    kv4_write, kv4_read, kv4_attend as their kv8_* namesakes
 """
 
 from __future__ import annotations
@@ -53,11 +64,15 @@ from __future__ import annotations
 import ctypes
 import os
 
-from . import lowbit
+from . import lowbit, step
 from .lowbit import (KV8, SGEMM_F32, W4, KV8Batch, KV8Cache, dequantize_w4, gemm_w4, kv8_attend, kv8_read, kv8_write,
                      quantize_w4, sgemm_kv8_attend, sgemm_kv8_attend_check_args, sgemm_kv8_attend_shape,
                      sgemm_kv8_attend_workspace_size, sgemm_kv8_check_args, sgemm_kv8_read, sgemm_kv8_write, sgemm_w4,
                      sgemm_w4_check_args, sgemm_w4_dequantize, sgemm_w4_pack_check_args, sgemm_w4_quantize, sgemm_w4_shape)
+from .step import (KV4, KV4Cache, KVStep, RopeRows, kv4_attend, kv4_read, kv4_write, kv_tables, rope, rope_frequencies,
+                   sgemm_kv4_attend, sgemm_kv4_attend_check_args, sgemm_kv4_attend_shape, sgemm_kv4_attend_workspace_size,
+                   sgemm_kv4_check_args, sgemm_kv4_read, sgemm_kv4_write, sgemm_kv_tables, sgemm_kv_tables_check_args,
+                   sgemm_rope, sgemm_rope_check_args)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libsgemm.so")
@@ -105,7 +120,7 @@ VARIANTS = {"best": SGEMM_BEST, "naive": SGEMM_NAIVE, "tiled": SGEMM_TILED,
 EXPORTS = ("sgemm", "sgemm_check_args", "sgemm_ex", "sgemm_ex_check_args", "sgemm_ex_ws", "sgemm_ex_ws_check_args",
            "sgemm_ex_workspace_size", "sgemm_ex_noalloc", "sgemm_ex_noalloc_check_args",
            "sgemm_ex_noalloc_scratch_bytes", "sgemm_lp", "sgemm_lp_check_args", "sgemm_status_string", "sgemm_variant_name",
-           "sgemm_best_variant", "sgemm_mfma_tile", "sgemm_mfma_shape", "sgemm_regblock_tile") + lowbit.EXPORTS
+           "sgemm_best_variant", "sgemm_mfma_tile", "sgemm_mfma_shape", "sgemm_regblock_tile") + lowbit.EXPORTS + step.EXPORTS
 
 _lib = None
 
@@ -170,6 +185,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sgemm_regblock_tile.argtypes = [i, i, i]
     lib.sgemm_regblock_tile.restype = i
     lowbit.declare(lib)
+    step.declare(lib)
     if path is None:
         _lib = lib
     return lib

@@ -124,7 +124,7 @@ extern "C" const char *sgemm_status_string(int status)
     case SGEMM_ERR_GROUP: return "group is not a positive multiple of 32";
     case SGEMM_ERR_CACHE: return "block, dim or alignment of the cache is not one the kernels take";
     case SGEMM_ERR_HEADS: return "query heads are not a positive multiple of the cache's heads";
-    case SGEMM_ERR_MASK: return "causal is neither 0 nor 1, or the window is negative or without causal";
+    case SGEMM_ERR_MASK: return "a flag is neither 0 nor 1, or the window is negative or without causal";
     default: return "unknown status";
     }
 }

@@ -1,0 +1,224 @@
+// Host-side argument checks of a serving step's entry points (the 4-bit cache,
+// rotary positions, page tables), and how attention over the 4-bit cache is
+// laid out over the device.
+//
+// Pure C++: no HIP header and no device call, like args.cpp.
+#include <cstddef>
+#include <cstdint>
+
+#include "args_util.hpp"
+#include "sgemm.h"
+#include "step_plan.hpp"
+
+using namespace sgemm_impl;
+
+namespace {
+
+int check_kv4(const sgemm_kv4_cache *c, const sgemm_kv8_batch *b)
+{
+    const int rc = check_cache_batch(c, b);
+    if (rc != SGEMM_OK) return rc;
+    // Four scales are read at once.
+    return aligned16(c->Ks) && aligned16(c->Vs) ? SGEMM_OK : SGEMM_ERR_CACHE;
+}
+
+struct CacheSpans {
+    Span s[4];
+};
+
+CacheSpans spans_of(const sgemm_kv4_cache *c)
+{
+    const i64 ph = i64(c->pages) * c->heads, codes = i64(c->block) * (c->dim / 2);
+    return {{span_of(c->K, ph, codes, codes, 1), span_of(c->V, ph, codes, codes, 1), span_of(c->Ks, ph, c->block, c->block, 2),
+             span_of(c->Vs, ph, c->block, c->block, 2)}};
+}
+
+bool overlaps_kv4(Span x, const sgemm_kv4_cache *c)
+{
+    for (const Span &s : spans_of(c).s)
+        if (overlap(x, s)) return true;
+    return false;
+}
+
+// Whether two rows x heads x dim operands (strides_ok) share a byte. Operands
+// of one row stride whose heads lie inside a row (parts of one buffer of
+// queries, keys and values, say) may be interleaved row by row.
+struct RowsOperand {
+    const void *p;
+    int rows, heads, dim, ld, hs, elem;
+    Span span() const { return rows_span(p, rows, heads, dim, ld, hs, elem); }
+    i64 width() const { return (i64(heads - 1) * (heads > 1 ? hs : 0) + dim) * elem; }
+};
+
+bool share(const RowsOperand &a, const RowsOperand &b)
+{
+    if (!overlap(a.span(), b.span())) return false;
+    const i64 pitch = i64(a.ld) * a.elem;
+    if (a.rows > 1 && pitch == i64(b.ld) * b.elem && a.width() <= pitch && b.width() <= pitch) {
+        // From the lower one on: a's width, then b's, within one pitch.
+        const std::uintptr_t pa = reinterpret_cast<std::uintptr_t>(a.p), pb = reinterpret_cast<std::uintptr_t>(b.p);
+        const RowsOperand &low = pa <= pb ? a : b, &high = pa <= pb ? b : a;
+        const i64 at = i64((pa <= pb ? pb - pa : pa - pb) % std::uintptr_t(pitch));
+        return !(at >= low.width() && at + high.width() <= pitch);
+    }
+    return true;
+}
+
+}  // namespace
+
+extern "C" int sgemm_kv4_check_args(const sgemm_kv4_cache *c, const sgemm_kv8_batch *b, int dtype, const void *K,
+                                    int ldk, int hsk, const void *V, int ldv, int hsv)
+{
+    if (!known_type(dtype)) return SGEMM_ERR_DTYPE;
+    const int rc = check_kv4(c, b);
+    if (rc != SGEMM_OK) return rc;
+    if (!strides_ok(b->rows, c->heads, c->dim, ldk, hsk) || !strides_ok(b->rows, c->heads, c->dim, ldv, hsv)) return SGEMM_ERR_LD;
+    if (b->seqs == 0 || b->rows == 0) return SGEMM_OK;
+    if (missing_arrays(c, b) || K == nullptr || V == nullptr) return SGEMM_ERR_NULL;
+    const Span k = rows_span(K, b->rows, c->heads, c->dim, ldk, hsk, size_of(dtype));
+    const Span v = rows_span(V, b->rows, c->heads, c->dim, ldv, hsv, size_of(dtype));
+    if (overlaps_kv4(k, c) || overlaps_kv4(v, c)) return SGEMM_ERR_ALIAS;
+    return SGEMM_OK;
+}
+
+extern "C" int sgemm_kv4_attend_check_args(const sgemm_kv4_cache *c, const sgemm_kv8_batch *b, int dtype, int heads_q,
+                                           const void *Q, int ldq, int hsq, float scale, int causal, int window,
+                                           const float *O, int ldo, int hso, const void *workspace,
+                                           std::size_t workspace_bytes)
+{
+    (void)scale;
+    if (!known_type(dtype)) return SGEMM_ERR_DTYPE;
+    const int rc = check_kv4(c, b);
+    if (rc != SGEMM_OK) return rc;
+    if (heads_q < 1 || heads_q % c->heads != 0) return SGEMM_ERR_HEADS;
+    if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && causal == 0)) return SGEMM_ERR_MASK;
+    if (!strides_ok(b->rows, heads_q, c->dim, ldq, hsq) || !strides_ok(b->rows, heads_q, c->dim, ldo, hso)) return SGEMM_ERR_LD;
+    if (b->seqs == 0 || b->rows == 0) return SGEMM_OK;
+    if (missing_arrays(c, b) || Q == nullptr || O == nullptr) return SGEMM_ERR_NULL;
+    const Span o = rows_span(O, b->rows, heads_q, c->dim, ldo, hso, 4);
+    const Span q = rows_span(Q, b->rows, heads_q, c->dim, ldq, hsq, size_of(dtype));
+    if (overlap(o, q) || overlaps_kv4(o, c) || overlaps_batch(o, b)) return SGEMM_ERR_ALIAS;
+    if (workspace != nullptr && workspace_bytes > 0) {
+        const std::uintptr_t base = reinterpret_cast<std::uintptr_t>(workspace);
+        const Span w{base, workspace_bytes > UINTPTR_MAX - base ? UINTPTR_MAX : base + workspace_bytes};
+        if (overlap(w, o) || overlap(w, q) || overlaps_kv4(w, c) || overlaps_batch(w, b)) return SGEMM_ERR_ALIAS;
+    }
+    return SGEMM_OK;
+}
+
+extern "C" int sgemm_rope_check_args(int dtype, int otype, int rows, int dim, int rot, int interleaved, int inverse,
+                                     float amplitude, const int *positions, const double *freqs,
+                                     const sgemm_rope_rows *first, const sgemm_rope_rows *second)
+{
+    (void)amplitude;
+    if (!known_type(dtype) || !known_type(otype)) return SGEMM_ERR_DTYPE;
+    if (first == nullptr) return SGEMM_ERR_NULL;
+    if (rows < 0 || dim < 1 || dim > kMostRopeDim || rot < 0 || rot > dim || rot % 2 != 0) return SGEMM_ERR_DIM;
+    const sgemm_rope_rows *const all[] = {first, second};
+    for (const sgemm_rope_rows *o : all)
+        if (o != nullptr && (o->heads < 1 || o->heads > kMostHeads)) return SGEMM_ERR_DIM;
+    if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return SGEMM_ERR_MASK;
+    for (const sgemm_rope_rows *o : all)
+        if (o != nullptr && (!strides_ok(rows, o->heads, dim, o->ldx, o->hsx) || !strides_ok(rows, o->heads, dim, o->ldy, o->hsy)))
+            return SGEMM_ERR_LD;
+    if (rows == 0) return SGEMM_OK;
+    if (positions == nullptr || (freqs == nullptr && rot > 0)) return SGEMM_ERR_NULL;
+    for (const sgemm_rope_rows *o : all)
+        if (o != nullptr && (o->X == nullptr || o->Y == nullptr)) return SGEMM_ERR_NULL;
+    for (int i = 0; i < 2; ++i) {
+        const sgemm_rope_rows *const o = all[i];
+        if (o == nullptr) continue;
+        const RowsOperand y{o->Y, rows, o->heads, dim, o->ldy, o->hsy, size_of(otype)};
+        if (overlap(y.span(), span_of(positions, 1, rows, rows, 4)) || overlap(y.span(), span_of(freqs, 1, rot / 2, rot / 2, 8)))
+            return SGEMM_ERR_ALIAS;
+        for (int j = 0; j < 2; ++j) {
+            const sgemm_rope_rows *const a = all[j];
+            if (a == nullptr) continue;
+            const RowsOperand x{a->X, rows, a->heads, dim, a->ldx, a->hsx, size_of(dtype)};
+            const bool in_place = i == j && o->Y == a->X && otype == dtype && (rows == 1 || o->ldy == a->ldx) &&
+                                  (o->heads == 1 || o->hsy == a->hsx);
+            if (!in_place && share(y, x)) return SGEMM_ERR_ALIAS;
+            if (i < j && share(y, RowsOperand{a->Y, rows, a->heads, dim, a->ldy, a->hsy, size_of(otype)})) return SGEMM_ERR_ALIAS;
+        }
+    }
+    return SGEMM_OK;
+}
+
+extern "C" int sgemm_kv_tables_check_args(const sgemm_kv_step *t)
+{
+    if (t == nullptr) return SGEMM_ERR_NULL;
+    if (t->seqs < 0 || t->table_ld < 0 || t->pool_size < 0 || t->rows < 0) return SGEMM_ERR_DIM;
+    if (t->block < 16 || t->block > 1024 || (t->block & (t->block - 1)) != 0) return SGEMM_ERR_CACHE;
+    if (t->starts == nullptr || t->taken == nullptr || t->taken_after == nullptr ||
+        (t->seqs > 0 && (t->lens == nullptr || t->news == nullptr || (t->table == nullptr && t->table_ld > 0))) ||
+        (t->pool == nullptr && t->pool_size > 0) || (t->rows > 0 && (t->positions == nullptr || t->slots == nullptr)))
+        return SGEMM_ERR_NULL;
+    const Span out[] = {span_of(t->table, t->seqs, t->table_ld, t->table_ld, 4), span_of(t->starts, 1, i64(t->seqs) + 1, i64(t->seqs) + 1, 4),
+                        span_of(t->positions, 1, t->rows, t->rows, 4), span_of(t->slots, 1, t->rows, t->rows, 8),
+                        span_of(t->taken_after, 1, 1, 1, 4)};
+    const Span in[] = {span_of(t->lens, 1, t->seqs, t->seqs, 4), span_of(t->news, 1, t->seqs, t->seqs, 4),
+                       span_of(t->pool, 1, t->pool_size, t->pool_size, 4), span_of(t->taken, 1, 1, 1, 4)};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return SGEMM_ERR_ALIAS;
+        for (int j = 0; j < 4; ++j)
+            if (overlap(out[i], in[j]) && !(i == 4 && j == 3 && t->taken == t->taken_after)) return SGEMM_ERR_ALIAS;
+    }
+    return SGEMM_OK;
+}
+
+namespace sgemm_impl {
+
+bool kv4_write_overlaps(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b)
+{
+    const CacheSpans own = spans_of(&c);
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps_batch(own.s[i], &b)) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlap(own.s[i], own.s[j])) return true;
+    }
+    return false;
+}
+
+bool kv4_read_overlaps(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int dtype, const void *K, int ldk, int hsk,
+                       const void *V, int ldv, int hsv)
+{
+    const RowsOperand k{K, b.rows, c.heads, c.dim, ldk, hsk, size_of(dtype)}, v{V, b.rows, c.heads, c.dim, ldv, hsv, size_of(dtype)};
+    return share(k, v) || overlaps_batch(k.span(), &b) || overlaps_batch(v.span(), &b);
+}
+
+Kv8Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus)
+{
+    const sgemm_kv8_cache like{c.K, c.V, nullptr, nullptr, c.pages, c.heads, c.block, c.dim};
+    return plan_kv8_attend(like, b, heads_q, window, cus);
+}
+
+}  // namespace sgemm_impl
+
+extern "C" size_t sgemm_kv4_attend_workspace_size(const sgemm_kv4_cache *c, const sgemm_kv8_batch *b, int heads_q,
+                                                  int window, int cus)
+{
+    if (check_kv4(c, b) != SGEMM_OK || heads_q < 1 || heads_q % c->heads != 0 || window < 0) return 0;
+    if (b->seqs == 0 || b->rows == 0) return 0;
+    const Kv8Plan plan = plan_kv4_attend(*c, *b, heads_q, window, cus);
+    if (plan.splits == 1) return 0;
+    // For each row of each split: the sums of its components, maximum and sum of the softmax.
+    return std::size_t(b->seqs) * std::size_t(c->heads) * std::size_t(plan.tiles) * std::size_t(plan.splits) * std::size_t(16 * plan.mt) *
+           std::size_t(c->dim + 4) * 4;
+}
+
+extern "C" int sgemm_kv4_attend_shape(const sgemm_kv4_cache *c, const sgemm_kv8_batch *b, int heads_q, int window, int cus,
+                                      int *shape)
+{
+    const int rc = check_kv4(c, b);
+    if (rc != SGEMM_OK) return rc;
+    if (heads_q < 1 || heads_q % c->heads != 0) return SGEMM_ERR_HEADS;
+    if (window < 0) return SGEMM_ERR_MASK;
+    if (shape == nullptr) return SGEMM_ERR_NULL;
+    const Kv8Plan plan = plan_kv4_attend(*c, *b, heads_q, window, cus);
+    shape[0] = 16 * plan.mt;
+    shape[1] = plan.rows ? 4 : 1;
+    shape[2] = plan.tiles;
+    shape[3] = plan.splits;
+    return SGEMM_OK;
+}

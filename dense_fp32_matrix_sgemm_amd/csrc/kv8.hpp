@@ -1,5 +1,5 @@
-// What the 8-bit cache's kernels read of the device's arrays, made safe: the
-// host has seen none of it.
+// What the kernels of the paged caches read of the device's arrays, made safe:
+// the host has seen none of it.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,7 +27,7 @@ __device__ inline Kv8Sequence kv8_sequence(const sgemm_kv8_batch &b, int seq)
 
 // The cache's page that holds page `page` of a sequence, or -1 where the
 // table has no such column or names no page of the cache.
-__device__ inline std::int64_t kv8_page(const sgemm_kv8_cache &c, const sgemm_kv8_batch &b, int seq, std::int64_t page)
+template <class Cache> __device__ inline std::int64_t kv8_page(const Cache &c, const sgemm_kv8_batch &b, int seq, std::int64_t page)
 {
     if (page >= b.table_ld) return -1;
     const int id = b.table[std::int64_t(seq) * b.table_ld + page];

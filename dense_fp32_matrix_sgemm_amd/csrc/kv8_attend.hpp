@@ -30,30 +30,12 @@
 
 #include <type_traits>
 
+#include "attend.hpp"
 #include "kv8.hpp"
 #include "lowbit.hpp"
 
 namespace sgemm_impl {
 namespace {
-
-constexpr int kAttendWaves = 4;
-constexpr float kLog2e = 1.4426950408889634f;
-
-// The larger (sum) of a value over the four lanes that hold one column.
-__device__ inline float column_max(float x)
-{
-    const auto a = __builtin_amdgcn_permlane16_swap(f32_bits(x), f32_bits(x), false, false);
-    const float y = __builtin_fmaxf(bits_f32(a[0]), bits_f32(a[1]));
-    const auto b = __builtin_amdgcn_permlane32_swap(f32_bits(y), f32_bits(y), false, false);
-    return __builtin_fmaxf(bits_f32(b[0]), bits_f32(b[1]));
-}
-__device__ inline float column_sum(float x)
-{
-    const auto a = __builtin_amdgcn_permlane16_swap(f32_bits(x), f32_bits(x), false, false);
-    const float y = bits_f32(a[0]) + bits_f32(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(f32_bits(y), f32_bits(y), false, false);
-    return bits_f32(b[0]) + bits_f32(b[1]);
-}
 
 __device__ inline std::uint32_t codes_bf16(std::uint32_t codes, bool upper)
 {
@@ -112,61 +94,10 @@ template <> struct QOperand<F32> {
     }
 };
 
-// An element that all lanes read, of an array that no kernel writes meanwhile:
-// through the constant address space it becomes a scalar load, which no wait
-// for a vector load holds up.
-template <class V> __device__ inline V uniform_load(const V *p, std::int64_t i)
-{
-    return reinterpret_cast<const __attribute__((address_space(4))) V *>(reinterpret_cast<std::uintptr_t>(p))[i];
-}
-
 // The bytes of a word that are e4m3 NaN, as 0x80 in each such byte.
 __device__ inline std::uint32_t nan_codes(std::uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 __device__ inline bool finite(float x) { return (f32_bits(x) & 0x7f800000u) != 0x7f800000u; }
-
-// Eight weights p * scale, p >= 0, as three bf16 parts that add up to them
-// exactly (split3 without its care for infinities: a weight that is not
-// finite makes its whole row NaN in any case).
-__device__ inline void split_weights(const float *w, Frag &hi, Frag &mid, Frag &lo)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float h[2], m[2], l[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float x = w[2 * i + j];
-            h[j] = bits_f32(f32_bits(x) & 0xffff0000u);
-            const float r = x - h[j];
-            m[j] = bits_f32(f32_bits(r) & 0xffff0000u);
-            l[j] = r - m[j];
-        }
-        hi.v[i] = pack_hi(h[0], h[1]);
-        mid.v[i] = pack_hi(m[0], m[1]);
-        lo.v[i] = pack_hi(l[0], l[1]);
-    }
-}
-
-// The factor that brings a sum with maximum m to maximum top.
-__device__ inline float rescale(float m, float top) { return m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top); }
-
-// What the rows of one tile see: row `row` of a sequence (row / R th new row,
-// query head row % R of the group) sees `count` tokens from `from` on, of
-// those that the table can name (from + count <= nameable).
-struct Kv8Seen {
-    std::int64_t first, len, nameable;  // position of new row 0, tokens, tokens that the table can name
-    int R, causal, window;
-    __device__ std::int64_t behind(std::int64_t row) const { return causal ? first + row / R + 1 : len; }
-    __device__ void operator()(std::int64_t row, int &from, int &count) const
-    {
-        const std::int64_t end = behind(row), begin = window > 0 ? end - window : 0;
-        const std::int64_t hi = end < 0 ? 0 : end < nameable ? end : nameable, lo = begin < 0 ? 0 : begin < hi ? begin : hi;
-        from = int(lo);
-        count = int(hi - lo);
-    }
-    // The last token seen lies behind the table's last column: the row is NaN.
-    __device__ bool beyond(std::int64_t row) const { return behind(row) > nameable; }
-};
 
 // Waves a SIMD has registers for: two, but for the longest heads and for two
 // groups of float32 rows (three parts of Q each).
@@ -178,7 +109,7 @@ template <class T> constexpr int kv8_waves_per_simd(int DC, int MT) { return DC 
 // unit's cache for all four). Otherwise they take the tokens of one row tile
 // in turns of 32 and add their sums through LDS in the waves' order, and
 // `splits` work-groups share the tile's tokens: each leaves its sums in the
-// workspace and kv8_join_kernel adds them.
+// workspace and kv_join_kernel adds them.
 //
 // Keys of the next 32 tokens are loaded into the registers of the last ones
 // as soon as their scores are formed, values likewise after their product:
@@ -222,7 +153,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
     for (unsigned seq = id / unsigned(p.c.heads); seq < unsigned(p.b.seqs); seq += seqs_at_once) {
         const Kv8Sequence s = kv8_sequence(p.b, int(seq));
         const std::int64_t all_rows = s.n * R;
-        const Kv8Seen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, R, p.causal, p.window};
+        const KvSeen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, R, p.causal, p.window};
         const int *const table = p.b.table + std::int64_t(seq) * p.b.table_ld;
         for (std::int64_t tile = tile0;; tile += p.plan.tiles) {
             const std::int64_t row0 = Rows ? (tile * kAttendWaves + wave) * kRows : tile * kRows;
@@ -506,51 +437,6 @@ __global__ __launch_bounds__(64 * kAttendWaves, kv8_waves_per_simd<T>(DC, MT)) v
     }
 }
 
-// Adds the sums that the splits of a row tile left in the workspace, in their
-// order: one wave for each row (32 sequences of 8192 tokens in 3 splits: 5 us,
-// most of it the launch).
-template <int MT> __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendProblem p)
-{
-    constexpr int kRows = 16 * MT;
-    const int lane = threadIdx.x & 63, R = p.heads_q / p.c.heads, dim = p.c.dim, splits = p.plan.splits;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const unsigned unit = blockIdx.x / (kRows / 4), i = blockIdx.x % (kRows / 4) * 4 + unsigned(wave);
-    const int tile = int(unit % unsigned(p.plan.tiles)), head = int(unit / unsigned(p.plan.tiles) % unsigned(p.c.heads));
-    const int seq = int(unit / unsigned(p.plan.tiles) / unsigned(p.c.heads));
-    const Kv8Sequence s = kv8_sequence(p.b, seq);
-    const std::int64_t row = std::int64_t(tile) * kRows + i;
-    if (row >= s.n * R) return;
-    const float *const part = p.ws + (std::int64_t(unit) * splits * kRows + i) * (dim + 4);
-    const std::int64_t pitch = std::int64_t(kRows) * (dim + 4);
-    // Lane x: split x's maximum and sum (at most 64 splits).
-    float m = -__builtin_inff(), l = 0.0f;
-    if (lane < splits) m = part[lane * pitch + dim], l = part[lane * pitch + dim + 1];
-    float top = m;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    // A split that saw nothing of its row weighs nothing, and its components were left as sums of nothing: zeros.
-    const float a = l == 0.0f ? 0.0f : rescale(m, top);
-    float sum = l * a;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-    f32x4 y = {0, 0, 0, 0};
-    const float *const at = part + (4 * lane < dim ? 4 * lane : 0);
-    int x = 0;
-    for (; x + 4 <= splits; x += 4) {
-        f32x4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const f32x4 *>(at + (x + i) * pitch);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y += v[i] * __shfl(a, x + i);
-    }
-    for (; x < splits; ++x) y += *reinterpret_cast<const f32x4 *>(at + x * pitch) * __shfl(a, x);
-    if (4 * lane >= dim) return;
-    y = y / sum;
-    const Kv8Seen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) * p.c.block, R, p.causal, p.window};
-    if (seen.beyond(row)) y = y * __builtin_nanf("");
-    __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + 4 * lane, &y, sizeof(y));
-}
-
 template <class T, int DC, bool Full, int MT, bool Rows> hipError_t launch_attend_kernel(const Kv8AttendProblem &p, hipStream_t stream)
 {
     const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads * p.plan.splits;
@@ -562,7 +448,7 @@ template <class T, int DC, bool Full, int MT, bool Rows> hipError_t launch_atten
                                    dim3(64 * kAttendWaves), args, 0, stream);
     if (e != hipSuccess || p.plan.splits == 1) return e;
     const unsigned units = unsigned(p.plan.tiles) * unsigned(p.c.heads) * unsigned(p.b.seqs);
-    return hipLaunchKernel(reinterpret_cast<const void *>(&kv8_join_kernel<MT>), dim3(units * (4 * MT)), dim3(256), args, 0, stream);
+    return hipLaunchKernel(reinterpret_cast<const void *>(&kv_join_kernel<Kv8AttendProblem, MT>), dim3(units * (4 * MT)), dim3(256), args, 0, stream);
 }
 
 template <class T, int DC, bool Full> hipError_t launch_attend_shape(const Kv8AttendProblem &p, hipStream_t stream)

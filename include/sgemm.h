@@ -53,12 +53,14 @@ typedef enum sgemm_status {
     SGEMM_ERR_SCRATCH = -10, /* sgemm_ex_noalloc: the product needs more scratch
                                 than the library's static buffer holds          */
     SGEMM_ERR_GROUP = -11,   /* sgemm_w4*: group not a positive multiple of 32   */
-    SGEMM_ERR_CACHE = -12,   /* sgemm_kv8*: block, dim or alignment of the cache
-                                not one the kernels take                        */
-    SGEMM_ERR_HEADS = -13,   /* sgemm_kv8_attend: query heads not a positive
-                                multiple of the cache's heads                   */
-    SGEMM_ERR_MASK = -14     /* sgemm_kv8_attend: causal not 0 or 1, window
-                                negative, or a window without causal            */
+    SGEMM_ERR_CACHE = -12,   /* sgemm_kv8*, sgemm_kv4*, sgemm_kv_tables: block,
+                                dim or alignment of the cache not one the
+                                kernels take                                    */
+    SGEMM_ERR_HEADS = -13,   /* sgemm_kv8_attend, sgemm_kv4_attend: query heads
+                                not a positive multiple of the cache's heads    */
+    SGEMM_ERR_MASK = -14     /* sgemm_kv8_attend, sgemm_kv4_attend: causal not 0
+                                or 1, window negative, or a window without
+                                causal; sgemm_rope: a flag not 0 or 1           */
 } sgemm_status;
 
 /* 16-bit operand types of sgemm_lp. */
@@ -68,7 +70,8 @@ typedef enum sgemm_lp_type {
 } sgemm_lp_type;
 
 /* Element types of the entry points that take float32 operands as well as
- * 16-bit ones (sgemm_w4*, sgemm_kv8*): SGEMM_F32 or an sgemm_lp_type. */
+ * 16-bit ones (sgemm_w4*, sgemm_kv8*, sgemm_kv4*, sgemm_rope): SGEMM_F32 or an
+ * sgemm_lp_type. */
 typedef enum sgemm_type {
     SGEMM_F32 = 0  /* IEEE binary32 */
 } sgemm_type;
@@ -633,6 +636,197 @@ size_t sgemm_kv8_attend_workspace_size(const sgemm_kv8_cache *cache, const sgemm
  */
 int sgemm_kv8_attend_shape(const sgemm_kv8_cache *cache, const sgemm_kv8_batch *batch, int heads_q, int window, int cus,
                            int *shape);
+
+/*
+ * A cache of keys and values in 4-bit floats (e2m1: 1 sign, 2 exponent and 1
+ * fraction bit; the codes 0 .. 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, with
+ * bit 3 for their negatives), in pages of `block` tokens, with one bfloat16
+ * scale for each token and head: the value at token t, component d is
+ * code[page][head][t][d] * scale[page][head][t]. A byte holds two components,
+ * the first one in its lower half.
+ *
+ * A token whose scale is not finite has no values: it reads NaN.
+ */
+typedef struct sgemm_kv4_cache {
+    void *K, *V;    /* pages x heads x block x dim / 2 bytes, 16-byte aligned   */
+    void *Ks, *Vs;  /* pages x heads x block bfloat16 scales, 16-byte aligned   */
+    int pages;      /* >= 1                                                     */
+    int heads;      /* 1 to 65536                                               */
+    int block;      /* tokens of a page: a power of two from 16 to 1024         */
+    int dim;        /* components of a head: a multiple of 16 from 16 to 256    */
+} sgemm_kv4_cache;
+
+/*
+ * Quantises the last rows of each sequence (sgemm_kv8_batch: the same
+ * sequences, tables and rules) into its pages. K and V are rows x heads x dim
+ * (dtype; strides as for sgemm_kv8_write). For each row and head, K and V
+ * apart:
+ *   scale = max |x| / 6, rounded to float32 and then to bfloat16, but at least
+ *           2^-100; 0 if all of the row's values are 0;
+ *   code  = x / scale rounded to e2m1, ties to even, at most 6 in size.
+ * A row of a head that holds a value that is not finite gets the scale NaN and
+ * codes of 0. Nothing else of a page changes: earlier tokens keep their codes
+ * and scales. A token that two rows of a call write (on a page that two
+ * sequences share, or that appears twice in a table) is left undefined, and
+ * nothing else.
+ *
+ * Checks, in this order: dtype, sizes, cache, strides, then (seqs > 0 and rows
+ * > 0) NULL pointers, overlap of the operand with the cache, and of the
+ * cache's arrays with one another or the batch's. One kernel is enqueued.
+ */
+int sgemm_kv4_write(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype,
+                    const void *K, int ldk, int hsk,
+                    const void *V, int ldv, int hsv,
+                    void *stream);
+
+/* The last rows of each sequence read back: code * scale in float32, rounded
+ * to dtype, into K and V (rows x heads x dim). A row whose page is not one of
+ * the cache's reads NaN; a row before token 0 is left as it was. The checks of
+ * sgemm_kv4_write() but for those of the cache's arrays; outputs that share
+ * elements with each other or overlap the batch's arrays are refused as well. */
+int sgemm_kv4_read(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype,
+                   void *K, int ldk, int hsk,
+                   void *V, int ldv, int hsv,
+                   void *stream);
+
+/* The host-side argument checks that sgemm_kv4_write() and sgemm_kv4_read()
+ * share. */
+int sgemm_kv4_check_args(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype,
+                         const void *K, int ldk, int hsk,
+                         const void *V, int ldv, int hsv);
+
+/*
+ * Softmax attention over the 4-bit cache: sgemm_kv8_attend() with the values
+ * of this cache. The same rows, masks, query heads, workspace rule and checks;
+ * a row that sees a token on a page that is not the cache's, or one whose scale
+ * of K or V is not finite, gets NaN. Tokens a row does not see do not reach it.
+ *
+ * Scores are <Q, code> in float32 times scale * log2(e) * K's scale, and have
+ * to stay within float32's normal numbers, as has p * V's scale.
+ */
+int sgemm_kv4_attend(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype, int heads_q,
+                     const void *Q, int ldq, int hsq,
+                     float scale, int causal, int window,
+                     float *O, int ldo, int hso,
+                     void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/* The host-side argument checks of sgemm_kv4_attend() alone. */
+int sgemm_kv4_attend_check_args(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype, int heads_q,
+                                const void *Q, int ldq, int hsq,
+                                float scale, int causal, int window,
+                                const float *O, int ldo, int hso,
+                                const void *workspace, size_t workspace_bytes);
+
+/* Workspace bytes with which sgemm_kv4_attend splits this call's sequences on
+ * a device with `cus` compute units (cus <= 0: 256), or 0 when it would not
+ * split them (or the sizes are invalid). Pure host logic; reads no array. */
+size_t sgemm_kv4_attend_workspace_size(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int heads_q,
+                                       int window, int cus);
+
+/* How sgemm_kv4_attend lays this call out, in shape[0..3]: as
+ * sgemm_kv8_attend_shape() says of sgemm_kv8_attend, with the same statuses. */
+int sgemm_kv4_attend_shape(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int heads_q, int window, int cus,
+                           int *shape);
+
+/* Rows of `heads` heads that sgemm_rope turns: X is read and Y written, rows x
+ * heads x dim with strides as for sgemm_kv8_write. Y may be X itself, with the
+ * same strides and type; it must share no element with any other X or Y. */
+typedef struct sgemm_rope_rows {
+    const void *X;
+    void *Y;
+    int heads;          /* 1 to 65536 */
+    int ldx, hsx, ldy, hsy;
+} sgemm_rope_rows;
+
+/*
+ * Rotary positions: turns pairs of components of each head by an angle that
+ * grows with the row's position. With t = positions[row] * freqs[i] radians,
+ * pair i of the first `rot` components becomes
+ *
+ *     a' = amplitude * (a cos t - b sin t)
+ *     b' = amplitude * (b cos t + a sin t)
+ *
+ * where (a, b) are components i and i + rot / 2 (interleaved == 0) or 2 i and
+ * 2 i + 1 (interleaved == 1). inverse == 1 turns back: the sign of sin changes,
+ * which is the product with the transposed matrix and so the gradient with
+ * respect to X, given the gradient with respect to Y. Components from rot on
+ * are copied.
+ *
+ * The angle is formed in float64 and brought into one turn before it is
+ * rounded, so that far positions keep full precision: cos and sin are good to
+ * 2^-22 for angles up to 2^30. Products and sums are float32, rounded once to
+ * the output's type.
+ *
+ * positions (rows, int32) and freqs (rot / 2, float64) are device arrays. second
+ * may be NULL; otherwise both operands (queries and keys, say) are turned by
+ * one launch. A row's angles come from its own position alone.
+ *
+ * Checks, in this order: dtype (of X) and otype (of Y; any pair of types), sizes
+ * (rows >= 0; 1 <= dim <= 1024; rot even, 0 to dim; heads), flags
+ * (SGEMM_ERR_MASK: interleaved or inverse not 0 or 1), strides, then (rows > 0)
+ * NULL pointers (freqs only with rot > 0) and overlap of a Y with positions,
+ * freqs or an X or Y that it may not meet. One kernel is enqueued.
+ */
+int sgemm_rope(int dtype, int otype, int rows, int dim, int rot, int interleaved, int inverse, float amplitude,
+               const int *positions, const double *freqs,
+               const sgemm_rope_rows *first, const sgemm_rope_rows *second,
+               void *stream);
+
+/* The host-side argument checks of sgemm_rope() alone. */
+int sgemm_rope_check_args(int dtype, int otype, int rows, int dim, int rot, int interleaved, int inverse, float amplitude,
+                          const int *positions, const double *freqs,
+                          const sgemm_rope_rows *first, const sgemm_rope_rows *second);
+
+/*
+ * The tables of a step over a paged cache, from the sequences' lengths.
+ *
+ * Sequence b holds lens[b] tokens (negative: 0), of which news[b] (cut to 0 ..
+ * lens[b]) are new: n_b. The calls over the cache then take table, lens and the
+ * starts that come out.
+ *   starts[b]        = n_0 + .. + n_{b-1}, b = 0 .. seqs (at most 2^31 - 1);
+ *   table row b      columns ceil((lens[b] - n_b) / block) .. ceil(lens[b] /
+ *                    block) - 1, of those that the table has, get the next
+ *                    pages of the pool, sequence after sequence: the k-th of
+ *                    the call is pool[taken + k], or -1 where the pool has no
+ *                    such entry. Other columns are left as they were;
+ *   *taken_after     = *taken + the columns so filled (at most 2^31 - 1): more
+ *                    than pool_size says that pages were missing;
+ *   positions[r]     of row r = starts[b] + i: lens[b] - n_b + i;
+ *   slots[r]         its place in the cache, page * block + position % block,
+ *                    or -1 where the table has no such column or a negative
+ *                    page in it.
+ * positions and slots have room for `rows` rows: rows from starts[seqs] on are
+ * left as they were, and rows that do not fit are not written (starts count
+ * them all the same).
+ *
+ * All arrays are device arrays; taken_after may be taken itself. Pages that a
+ * sequence no longer needs are the caller's to put into a pool again.
+ */
+typedef struct sgemm_kv_step {
+    const int *lens;      /* seqs                                        */
+    const int *news;      /* seqs                                        */
+    const int *pool;      /* pool_size page numbers                      */
+    const int *taken;     /* entries of the pool that are used up        */
+    int *table;           /* seqs x table_ld, read and written           */
+    int *starts;          /* seqs + 1                                    */
+    int *positions;       /* rows                                        */
+    long long *slots;     /* rows                                        */
+    int *taken_after;
+    int seqs, table_ld, block, pool_size, rows;
+} sgemm_kv_step;
+
+/*
+ * Checks, in this order: step NULL, sizes (seqs, table_ld, pool_size or rows
+ * negative), block (SGEMM_ERR_CACHE: not a power of two from 16 to 1024), NULL
+ * pointers (of arrays that have elements), overlap of an output with another
+ * array (but taken_after with taken). seqs == 0 still writes starts[0] and
+ * *taken_after. One kernel is enqueued, two for more than 16384 rows.
+ */
+int sgemm_kv_tables(const sgemm_kv_step *step, void *stream);
+
+/* The host-side argument checks of sgemm_kv_tables() alone. */
+int sgemm_kv_tables_check_args(const sgemm_kv_step *step);
 
 /* Static English text for a status code ("unknown status" otherwise). */
 const char *sgemm_status_string(int status);
