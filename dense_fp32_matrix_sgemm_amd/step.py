@@ -16,8 +16,8 @@ from __future__ import annotations
 import ctypes
 import math
 
-from .lowbit import (_INT32_MAX, KV8Batch, _batch, _cus, _heads, _int32, _launch, _lib, _need, _operand, _pair, _shape, _type_code,
-                     _types)
+from . import lowbit
+from .lowbit import _INT32_MAX, KV8Batch, _cus, _heads, _int32, _launch, _lib, _need, _shape, _type_code, _types
 
 EXPORTS = ("sgemm_kv4_write", "sgemm_kv4_read", "sgemm_kv4_check_args", "sgemm_kv4_attend", "sgemm_kv4_attend_check_args",
            "sgemm_kv4_attend_workspace_size", "sgemm_kv4_attend_shape", "sgemm_rope", "sgemm_rope_check_args",
@@ -109,6 +109,57 @@ def sgemm_kv_tables_check_args(*args) -> int:
 
 
 # ------------------------------------------------------------ tensor helpers
+#
+# A serving program makes these calls once per layer and token. The usual
+# operands are therefore checked in as few steps as tell that nothing is wrong
+# with them; all others go through the checks that say what is.
+
+
+def _batch(cache, table, lens, starts, rows, max_new):
+    """The sequences of a call over `cache`."""
+    try:
+        seqs, columns = table.shape
+        i32, index = table.dtype, cache._index
+        if (lens.dtype is i32 and starts.dtype is i32 and i32 is cache._i32 and table.get_device() == index
+                and lens.get_device() == index and starts.get_device() == index and lens.shape == (seqs,)
+                and starts.shape == (seqs + 1,) and table.is_contiguous() and lens.is_contiguous() and starts.is_contiguous()
+                and columns <= _INT32_MAX and 0 <= (rows if max_new is None else max_new) <= _INT32_MAX and rows <= _INT32_MAX):
+            return KV8Batch(table.data_ptr() or None, lens.data_ptr() or None, starts.data_ptr() or None, seqs, columns, rows,
+                            rows if max_new is None else int(max_new))
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return lowbit._batch(cache, table, lens, starts, rows, max_new)
+
+
+def _usual(t, index, heads, dim):
+    """Row and head strides of a rows x heads x dim tensor on device `index`, or None if it is not one as usual."""
+    try:
+        rows, h, d = t.shape
+        if h == heads and d == dim and t.get_device() == index:
+            ld, hs, step = t.stride()
+            if step == 1 and ld <= _INT32_MAX and hs <= _INT32_MAX:
+                return (ld if rows > 1 else heads * dim or 1), (hs if heads > 1 else dim)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return None
+
+
+def _pair(cache, K, V):
+    """Type, places and strides of K and V, rows x heads x dim of one type."""
+    k, v = _usual(K, cache._index, cache._heads, cache._dim), _usual(V, cache._index, cache._heads, cache._dim)
+    if k is not None and v is not None and K.dtype is V.dtype and K.shape[0] == V.shape[0]:
+        code = _types().get(K.dtype)
+        if code is not None:
+            return code, K.data_ptr() or None, *k, V.data_ptr() or None, *v
+    return lowbit._pair(cache, K, V)
+
+
+def _operand(t, name, cache, heads, dtypes):
+    """Row and head strides of a rows x heads x dim tensor of one of `dtypes`."""
+    strides = _usual(t, cache._index, heads, cache._dim) if heads is not None else None
+    if strides is not None and t.dtype in dtypes:
+        return strides
+    return lowbit._operand(t, name, cache, heads, dtypes)
 
 
 class KV4:
@@ -122,7 +173,7 @@ class KV4:
     to 256. K and V may be one tensor (so may Ks and Vs) to read and attend,
     but not for :func:`kv4_write`."""
 
-    __slots__ = ("_tensors", "_struct", "_device", "_heads", "_dim")
+    __slots__ = ("_tensors", "_struct", "_device", "_index", "_i32", "_heads", "_dim")
 
     def __init__(self, K, V, Ks, Vs):
         import torch
@@ -147,6 +198,7 @@ class KV4:
             raise ValueError("K, V, Ks and Vs must begin at a multiple of 16 bytes")
         _int32(pages=pages, heads=heads)
         self._tensors, self._device, self._heads, self._dim = (K, V, Ks, Vs), K.device, heads, dim
+        self._index, self._i32 = K.get_device(), torch.int32
         self._struct = KV4Cache(K.data_ptr(), V.data_ptr(), Ks.data_ptr(), Vs.data_ptr(), pages, heads, block, dim)
 
     K = property(lambda self: self._tensors[0])
@@ -193,8 +245,8 @@ def kv4_read(cache, table, lens, starts, rows=None, dtype=None, K=None, V=None, 
     if K is None:
         dtype = torch.float32 if dtype is None else dtype
         _type_code(dtype, "dtype")
-        shape = (int(rows), cache._heads, cache._dim)
-        K, V = torch.empty(shape, dtype=dtype, device=cache._device), torch.empty(shape, dtype=dtype, device=cache._device)
+        K = torch.empty((int(rows), cache._heads, cache._dim), dtype=dtype, device=cache._device)
+        V = torch.empty_like(K)
     operand = _pair(cache, K, V)
     if (rows is not None and K.shape[0] != rows) or (dtype is not None and K.dtype != dtype):
         raise ValueError("K is not of the rows and dtype asked for")
@@ -213,13 +265,16 @@ def kv4_attend(Q, cache, table, lens, starts, scale=None, causal=True, window=0,
 
     if not isinstance(cache, KV4):
         raise TypeError("cache must be a KV4")
-    ldq, hsq = _operand(Q, "Q", cache, None, _types())
+    heads_q = Q.shape[1] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else None
+    ldq, hsq = _operand(Q, "Q", cache, heads_q, _types())
     rows, heads_q, dim = Q.shape
     if out is None:
         out = torch.empty((rows, heads_q, dim), dtype=torch.float32, device=cache._device)
-    ldo, hso = _operand(out, "out", cache, heads_q, (torch.float32,))
-    if out.shape[0] != rows:
-        raise ValueError(f"out must have Q's shape {tuple(Q.shape)}, is {tuple(out.shape)}")
+        ldo, hso = heads_q * dim or 1, dim
+    else:
+        ldo, hso = _operand(out, "out", cache, heads_q, (torch.float32,))
+        if out.shape[0] != rows:
+            raise ValueError(f"out must have Q's shape {tuple(Q.shape)}, is {tuple(out.shape)}")
     if not 0 <= window <= _INT32_MAX or heads_q > _INT32_MAX:
         _int32(window=window, heads_q=heads_q)
     batch = _batch(cache, table, lens, starts, rows, max_new)
@@ -271,20 +326,24 @@ def _rope_rows(X, Y, dtype, name):
     """(RopeRows, Y) of an operand X and its output Y (allocated when None)."""
     import torch
 
-    _need(X, name, 3, _types())
-    ldx, hsx = _heads(X, name)
+    index = X.get_device()
     rows, heads, dim = X.shape
+    x = _usual(X, index, heads, dim)
+    if x is None:
+        x = _heads(X, name)
     if Y is None:
         Y = torch.empty((rows, heads, dim), dtype=dtype, device=X.device)
-        ldy, hsy = heads * dim, dim
+        y = heads * dim or 1, dim
     else:
-        _need(Y, f"{name}'s output", 3, (dtype,), X.device)
-        if Y.shape != X.shape:
-            raise ValueError(f"{name}'s output must be {tuple(X.shape)}, is {tuple(Y.shape)}")
-        ldy, hsy = _heads(Y, f"{name}'s output")
-    if heads > _INT32_MAX or ldy > _INT32_MAX:
-        _int32(heads=heads, row_stride=ldy)
-    return RopeRows(X.data_ptr() or None, Y.data_ptr() or None, heads, ldx, hsx, ldy, hsy), Y
+        y = _usual(Y, index, heads, dim)
+        if y is None or Y.dtype is not dtype or Y.shape[0] != rows:
+            _need(Y, f"{name}'s output", 3, (dtype,), X.device)
+            if Y.shape != X.shape:
+                raise ValueError(f"{name}'s output must be {tuple(X.shape)}, is {tuple(Y.shape)}")
+            y = _heads(Y, f"{name}'s output")
+    if heads > _INT32_MAX or y[0] > _INT32_MAX:
+        _int32(heads=heads, row_stride=y[0])
+    return RopeRows(X.data_ptr() or None, Y.data_ptr() or None, heads, *x, *y), Y
 
 
 def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False, dtype=None, out=None):
@@ -305,14 +364,18 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
     """
     import torch
 
-    _need(Q, "Q", 3, _types())
-    device, rows, dim = Q.device, Q.shape[0], Q.shape[2]
-    _need(positions, "positions", 1, (torch.int32,), device)
-    _need(freqs, "freqs", 1, (torch.float64,), device)
-    if positions.shape[0] != rows or not positions.is_contiguous() or not freqs.is_contiguous():
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or not Q.is_cuda or Q.dtype not in _types():
+        _need(Q, "Q", 3, _types())
+    index, (rows, _, dim) = Q.get_device(), Q.shape
+    if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.get_device() == index
+            and positions.shape == (rows,) and positions.is_contiguous() and isinstance(freqs, torch.Tensor)
+            and freqs.dtype is torch.float64 and freqs.get_device() == index and freqs.dim() == 1 and freqs.is_contiguous()):
+        _need(positions, "positions", 1, (torch.int32,), Q.device)
+        _need(freqs, "freqs", 1, (torch.float64,), Q.device)
         raise ValueError(f"positions must be {rows} contiguous elements (has {positions.shape[0]}), freqs contiguous")
-    if 2 * freqs.shape[0] > dim:
-        raise ValueError(f"{freqs.shape[0]} pairs do not fit heads of {dim} components")
+    pairs = freqs.shape[0]
+    if 2 * pairs > dim:
+        raise ValueError(f"{pairs} pairs do not fit heads of {dim} components")
     if out is None:
         outs = (None, None)
     elif K is None:
@@ -329,13 +392,14 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
     first, Y = _rope_rows(Q, outs[0], dtype, "Q")
     second = Z = None
     if K is not None:
-        _need(K, "K", 3, (Q.dtype,), device)
+        if not isinstance(K, torch.Tensor) or K.dim() != 3 or K.get_device() != index or K.dtype is not Q.dtype:
+            _need(K, "K", 3, (Q.dtype,), Q.device)
         if K.shape[0] != rows or K.shape[2] != dim:
             raise ValueError(f"K must be {rows} x heads x {dim}, is {tuple(K.shape)}")
         second, Z = _rope_rows(K, outs[1], dtype, "K")
     if rows > _INT32_MAX:
         _int32(rows=rows)
-    _launch(device.index, _lib().sgemm_rope, _types()[Q.dtype], otype, rows, dim, 2 * freqs.shape[0], 1 if interleaved else 0,
+    _launch(index, _lib().sgemm_rope, _types()[Q.dtype], otype, rows, dim, 2 * pairs, 1 if interleaved else 0,
             1 if inverse else 0, amplitude, positions.data_ptr() or None, freqs.data_ptr() or None, first, second)
     return Y if K is None else (Y, Z)
 
@@ -361,29 +425,41 @@ def kv_tables(table, lens, new, pool, taken, block, rows, starts=None, positions
     """
     import torch
 
-    i32 = (torch.int32,)
-    _need(table, "table", 2, i32)
-    device, (seqs, columns), rows = table.device, table.shape, int(rows)
-    for name, t in (("lens", lens), ("new", new), ("pool", pool), ("taken", taken)):
-        _need(t, name, 1, i32, device)
-    if lens.shape[0] != seqs or new.shape[0] != seqs or taken.shape[0] != 1:
-        raise ValueError(f"a table of {seqs} rows needs {seqs} lens and new and one taken, got {lens.shape[0]}, {new.shape[0]}, {taken.shape[0]}")
-    if not 0 <= rows <= _INT32_MAX or not 0 <= block <= _INT32_MAX or seqs >= _INT32_MAX or columns > _INT32_MAX or pool.shape[0] > _INT32_MAX:
-        _int32(rows=rows, block=block, seqs=seqs + 1, columns=columns, pool=pool.shape[0])
-    outs = []
-    for name, t, size, kind in (("starts", starts, seqs + 1, torch.int32), ("positions", positions, rows, torch.int32),
-                                ("slots", slots, rows, torch.int64), ("taken_after", taken_after, 1, torch.int32)):
-        if t is None:
-            t = torch.empty(size, dtype=kind, device=device)
-        else:
-            _need(t, name, 1, (kind,), device)
-            if t.shape[0] != size:
-                raise ValueError(f"{name} must have {size} elements, has {t.shape[0]}")
-        outs.append(t)
-    if not all(t.is_contiguous() for t in (table, lens, new, pool, taken, *outs)):
-        raise ValueError("the arrays must be contiguous")
+    i32, rows = torch.int32, int(rows)
+    try:
+        (seqs, columns), index, (entries,) = table.shape, table.get_device(), pool.shape
+        usual = (table.dtype is i32 and lens.dtype is i32 and new.dtype is i32 and pool.dtype is i32 and taken.dtype is i32 and index >= 0
+                 and lens.get_device() == index and new.get_device() == index and pool.get_device() == index and taken.get_device() == index
+                 and lens.shape == (seqs,) and new.shape == (seqs,) and taken.shape == (1,) and table.is_contiguous()
+                 and lens.is_contiguous() and new.is_contiguous() and pool.is_contiguous() and taken.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        _need(table, "table", 2, (i32,))
+        for name, t in (("lens", lens), ("new", new), ("pool", pool), ("taken", taken)):
+            _need(t, name, 1, (i32,), table.device)
+        if not all(t.is_contiguous() for t in (table, lens, new, pool, taken)):
+            raise ValueError("table, lens, new, pool and taken must be contiguous")
+        raise ValueError(f"a table of {table.shape[0]} rows needs as many lens and new and one taken, got {lens.shape[0]}, "
+                         f"{new.shape[0]}, {taken.shape[0]}")
+    if not 0 <= rows <= _INT32_MAX or not 0 <= block <= _INT32_MAX or seqs >= _INT32_MAX or columns > _INT32_MAX or entries > _INT32_MAX:
+        _int32(rows=rows, block=block, seqs=seqs + 1, columns=columns, pool=entries)
+    if starts is None and positions is None and slots is None and taken_after is None:
+        # One allocation for the three of one type.
+        starts, positions, taken_after = torch.empty(seqs + rows + 2, dtype=i32, device=table.device).split_with_sizes((seqs + 1, rows, 1))
+        outs = starts, positions, torch.empty(rows, dtype=torch.int64, device=table.device), taken_after
+    else:
+        outs = []
+        for name, t, size, kind in (("starts", starts, seqs + 1, i32), ("positions", positions, rows, i32),
+                                    ("slots", slots, rows, torch.int64), ("taken_after", taken_after, 1, i32)):
+            if t is None:
+                t = torch.empty(size, dtype=kind, device=table.device)
+            elif not isinstance(t, torch.Tensor) or t.dtype is not kind or t.get_device() != index or t.shape != (size,) or not t.is_contiguous():
+                _need(t, name, 1, (kind,), table.device)
+                raise ValueError(f"{name} must have {size} contiguous elements, has {t.shape[0]}")
+            outs.append(t)
     step = KVStep(lens.data_ptr() or None, new.data_ptr() or None, pool.data_ptr() or None, taken.data_ptr(), table.data_ptr() or None,
                   outs[0].data_ptr(), outs[1].data_ptr() or None, outs[2].data_ptr() or None, outs[3].data_ptr(), seqs, columns, block,
-                  pool.shape[0], rows)
-    _launch(device.index, _lib().sgemm_kv_tables, step)
+                  entries, rows)
+    _launch(index, _lib().sgemm_kv_tables, step)
     return tuple(outs)
