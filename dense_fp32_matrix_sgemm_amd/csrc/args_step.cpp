@@ -187,10 +187,47 @@ bool kv4_read_overlaps(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int d
     return share(k, v) || overlaps_batch(k.span(), &b) || overlaps_batch(v.span(), &b);
 }
 
-Kv8Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus)
+Kv4Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus)
 {
-    const sgemm_kv8_cache like{c.K, c.V, nullptr, nullptr, c.pages, c.heads, c.block, c.dim};
-    return plan_kv8_attend(like, b, heads_q, window, cus);
+    cus = cus <= 0 ? 256 : cus < 4096 ? cus : 4096;
+    const i64 new_rows = b.max_new < b.rows ? b.max_new : b.rows, rows = at_least_1(new_rows * (heads_q / c.heads));
+    const i64 heads = i64(b.seqs) * c.heads;  // of all sequences
+    const auto tiles_of = [&](i64 tile) { return (rows + tile - 1) / tile; };
+    // A launch covers at most 2^22 work-groups at once; kernels walk the rest.
+    const i64 most = at_least_1((i64(1) << 22) / c.heads);
+    const auto cut = [&](i64 tiles) { return int(tiles < most ? tiles : most); };
+
+    Kv4Plan plan = {};
+    plan.copies = 1;
+    // Waves take row tiles of their own once that gives every compute unit a work-group.
+    const int most_mt = c.dim > 128 ? 1 : 2;  // longer heads have no registers for two
+    plan.rows = rows >= 64 * most_mt && (heads >= cus || tiles_of(64 * most_mt) * heads >= cus);
+    if (plan.rows) {
+        plan.mt = most_mt;
+        plan.tiles = cut(tiles_of(64 * most_mt));
+        return plan;
+    }
+    // Two groups of 16 rows a wave halve the work on codes a row, once the
+    // device is full without them.
+    plan.mt = rows > 16 && tiles_of(16) * heads >= 2 * i64(cus) ? most_mt : 1;
+    if (plan.mt == 1) plan.copies = rows <= 4 ? 4 : rows <= 8 ? 2 : 1;
+    plan.tiles = cut(tiles_of(plan.tile_rows()));
+    // As many work-groups as the compute units hold at once share the tokens of
+    // all sequences, each with at least 256 of those that the longest sequences
+    // can have, unless there are many times as many sequences and heads in any case.
+    const int resident = c.dim <= 128 && plan.mt == 1 ? 3 : 2;
+    const i64 units = i64(plan.tiles) * c.heads;
+    if (b.seqs > kMostShared || units * b.seqs >= 4 * resident * i64(cus)) return plan;
+    i64 tokens = i64(b.table_ld) * c.block;
+    if (window > 0 && tokens > window + new_rows) tokens = window + new_rows;
+    i64 slots = resident * i64(cus) / units, room = i64(b.seqs) * (tokens / (32 * kKv4LeastTurns));
+    if (slots > room) slots = room;
+    if (slots > 64 * i64(b.seqs)) slots = 64 * i64(b.seqs);
+    if (slots <= b.seqs && room <= b.seqs) return plan;  // no sequence long enough to be shared
+    if (slots < 1) return plan;
+    plan.slots = int(slots);
+    plan.parts = plan.slots + b.seqs;
+    return plan;
 }
 
 }  // namespace sgemm_impl
@@ -200,11 +237,9 @@ extern "C" size_t sgemm_kv4_attend_workspace_size(const sgemm_kv4_cache *c, cons
 {
     if (check_kv4(c, b) != SGEMM_OK || heads_q < 1 || heads_q % c->heads != 0 || window < 0) return 0;
     if (b->seqs == 0 || b->rows == 0) return 0;
-    const Kv8Plan plan = plan_kv4_attend(*c, *b, heads_q, window, cus);
-    if (plan.splits == 1) return 0;
-    // For each row of each split: the sums of its components, maximum and sum of the softmax.
-    return std::size_t(b->seqs) * std::size_t(c->heads) * std::size_t(plan.tiles) * std::size_t(plan.splits) * std::size_t(16 * plan.mt) *
-           std::size_t(c->dim + 4) * 4;
+    const Kv4Plan plan = plan_kv4_attend(*c, *b, heads_q, window, cus);
+    // For each row of each part: the sums of its components, maximum and sum of the softmax.
+    return std::size_t(c->heads) * std::size_t(plan.tiles) * std::size_t(plan.parts) * std::size_t(plan.tile_rows()) * std::size_t(c->dim + 4) * 4;
 }
 
 extern "C" int sgemm_kv4_attend_shape(const sgemm_kv4_cache *c, const sgemm_kv8_batch *b, int heads_q, int window, int cus,
@@ -215,10 +250,10 @@ extern "C" int sgemm_kv4_attend_shape(const sgemm_kv4_cache *c, const sgemm_kv8_
     if (heads_q < 1 || heads_q % c->heads != 0) return SGEMM_ERR_HEADS;
     if (window < 0) return SGEMM_ERR_MASK;
     if (shape == nullptr) return SGEMM_ERR_NULL;
-    const Kv8Plan plan = plan_kv4_attend(*c, *b, heads_q, window, cus);
-    shape[0] = 16 * plan.mt;
+    const Kv4Plan plan = plan_kv4_attend(*c, *b, heads_q, window, cus);
+    shape[0] = plan.tile_rows();
     shape[1] = plan.rows ? 4 : 1;
     shape[2] = plan.tiles;
-    shape[3] = plan.splits;
+    shape[3] = plan.slots;
     return SGEMM_OK;
 }

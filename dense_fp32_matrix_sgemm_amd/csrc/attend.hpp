@@ -71,16 +71,19 @@ __device__ inline float rescale(float m, float top) { return m == top ? 1.0f : _
 struct KvSeen {
     std::int64_t first, len, nameable;  // position of new row 0, tokens, tokens that the table can name
     int R, causal, window;
-    __device__ std::int64_t behind(std::int64_t row) const { return causal ? first + row / R + 1 : len; }
-    __device__ void operator()(std::int64_t row, int &from, int &count) const
+    // By the new row itself: where what it sees ends, what it sees, and whether
+    // the last token seen lies behind the table's last column (the row is NaN).
+    __device__ std::int64_t end_of(std::int64_t fresh) const { return causal ? first + fresh + 1 : len; }
+    __device__ void by_new(std::int64_t fresh, int &from, int &count) const
     {
-        const std::int64_t end = behind(row), begin = window > 0 ? end - window : 0;
+        const std::int64_t end = end_of(fresh), begin = window > 0 ? end - window : 0;
         const std::int64_t hi = end < 0 ? 0 : end < nameable ? end : nameable, lo = begin < 0 ? 0 : begin < hi ? begin : hi;
         from = int(lo);
         count = int(hi - lo);
     }
-    // The last token seen lies behind the table's last column: the row is NaN.
-    __device__ bool beyond(std::int64_t row) const { return behind(row) > nameable; }
+    __device__ bool beyond_new(std::int64_t fresh) const { return end_of(fresh) > nameable; }
+    __device__ void operator()(std::int64_t row, int &from, int &count) const { by_new(row / R, from, count); }
+    __device__ bool beyond(std::int64_t row) const { return beyond_new(row / R); }
 };
 
 // Adds the sums that the splits of a row tile left in the workspace, in their

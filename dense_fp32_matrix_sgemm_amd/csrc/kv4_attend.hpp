@@ -58,11 +58,6 @@ template <int At> __device__ inline std::uint32_t fp4_f16(std::uint32_t codes)
 template <class T> struct QOperand4;
 template <> struct QOperand4<BF16> {
     Frag f;
-    __device__ void load(const std::uint16_t *q, bool there)
-    {
-        f.v = u32x4{0, 0, 0, 0};
-        if (there) f.v = load_any<u32x4>(q);
-    }
     __device__ f32x4 scores(std::uint32_t k, f32x4 acc) const
     {
         const Frag a{{fp4_bf16<0>(k), fp4_bf16<1>(k), fp4_bf16<2>(k), fp4_bf16<3>(k)}};
@@ -71,11 +66,6 @@ template <> struct QOperand4<BF16> {
 };
 template <> struct QOperand4<F16> {
     Frag f;
-    __device__ void load(const std::uint16_t *q, bool there)
-    {
-        f.v = u32x4{0, 0, 0, 0};
-        if (there) f.v = load_any<u32x4>(q);
-    }
     __device__ f32x4 scores(std::uint32_t k, f32x4 acc) const
     {
         const Frag a{{fp4_f16<0>(k), fp4_f16<1>(k), fp4_f16<2>(k), fp4_f16<3>(k)}};
@@ -102,29 +92,39 @@ __device__ inline void split2(float a, float b, std::uint32_t &hi, std::uint32_t
     lo = __builtin_bit_cast(std::uint32_t, f16x2{_Float16(ra), _Float16(rb)});
 }
 
-// A lane's pieces of one query row (eight components each, of those that are
-// `there`), and the factor that its scores are to be multiplied by. float32
-// rows are brought to a largest component of 2^14 to 2^15 by a power of two,
-// so that their parts hold each component to 2^-22 of itself or 2^-39 of the
-// largest. (A row with a component that is not finite has no finite score.)
-template <class T, int DC, class There> __device__ inline float load_query(QOperand4<T> (&q)[DC], const typename T::elem *src, There &&there)
+// A lane's pieces of one query row, eight components each, of those that are
+// `there`.
+template <class T, int DC> struct QueryPieces {
+    struct Piece {
+        typename T::elem x[8];
+    } r[DC];
+    template <class There> __device__ void load(const typename T::elem *src, There &&there)
+    {
+#pragma unroll
+        for (int i = 0; i < DC; ++i) {
+            __builtin_memset(&r[i], 0, sizeof(Piece));
+            if (there(i)) r[i] = load_any<Piece>(src + 8 * i);
+        }
+    }
+};
+
+// The same as operands, and the factor that the row's scores are to be
+// multiplied by. float32 rows are brought to a largest component of 2^14 to
+// 2^15 by a power of two, so that their parts hold each component to 2^-22 of
+// itself or 2^-39 of the largest. (A row with a component that is not finite
+// has no finite score.)
+template <class T, int DC> __device__ inline float query_operands(const QueryPieces<T, DC> &raw, QOperand4<T> (&q)[DC])
 {
     if constexpr (sizeof(typename T::elem) == 2) {
 #pragma unroll
-        for (int i = 0; i < DC; ++i) q[i].load(src + 8 * i, there(i));
+        for (int i = 0; i < DC; ++i) q[i].f.v = __builtin_bit_cast(u32x4, raw.r[i]);
         return 1.0f;
     } else {
-        struct Raw {
-            float x[8];
-        } r[DC];
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < DC; ++i) {
-            __builtin_memset(&r[i], 0, sizeof(Raw));
-            if (there(i)) r[i] = load_any<Raw>(src + 8 * i);
+        for (int i = 0; i < DC; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(r[i].x[j]));
-        }
+            for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(raw.r[i].x[j]));
         top = column_max(top);
         int field = 127 + 14 + 127 - int(f32_bits(top) >> 23);
         field = field > 253 ? 253 : field;
@@ -134,7 +134,7 @@ template <class T, int DC, class There> __device__ inline float load_query(QOper
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 std::uint32_t hi, lo;
-                split2(r[i].x[2 * j] * up, r[i].x[2 * j + 1] * up, hi, lo);
+                split2(raw.r[i].x[2 * j] * up, raw.r[i].x[2 * j + 1] * up, hi, lo);
                 q[i].hi.v[j] = hi;
                 q[i].lo.v[j] = lo;
             }
@@ -161,12 +161,612 @@ __device__ inline void exponents_of(std::uint32_t s, float &lower, float &upper)
     upper = float(u >> 24);
 }
 
-template <class T, int DC, bool Full, int MT, bool Rows>
-__global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4AttendProblem p)
+// The largest (sum) of a value over the P copies of a column's row.
+template <int N> __device__ inline float turned(float x)  // from the lane N places before, around the 16 lanes of a row
 {
-    constexpr int PD = 32 * DC, kRows = 16 * MT, kDTiles = 2 * DC, kLd = PD + 4, kVWords = (DC + 3) / 4;
+    const int u = __builtin_bit_cast(int, x);
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(u, 0x120 + N, 0xf, 0xf, true));
+}
+template <int P> __device__ inline float copies_max(float x)
+{
+    if constexpr (P == 4) x = __builtin_fmaxf(x, turned<4>(x));
+    if constexpr (P >= 2) x = __builtin_fmaxf(x, turned<8>(x));
+    return x;
+}
+template <int P> __device__ inline float copies_sum(float x)
+{
+    if constexpr (P == 4) x += turned<4>(x);
+    if constexpr (P >= 2) x += turned<8>(x);
+    return x;
+}
+
+// Pair e of the four pairs of weights of a row that its P copies hold in order,
+// in the lanes of the first copy. (What the others get is another row's.)
+template <int P, int N> __device__ inline std::uint32_t from_copy(const std::uint32_t (&own)[N], int e)
+{
+    const std::uint32_t x = own[e % N];
+    if (e / N == 0) return x;
+    const int u = int(x);
+    if (P == 2 || e / N == 2) return std::uint32_t(__builtin_amdgcn_mov_dpp(u, 0x120 + 8, 0xf, 0xf, true));
+    return std::uint32_t(e / N == 1 ? __builtin_amdgcn_mov_dpp(u, 0x120 + 12, 0xf, 0xf, true)
+                                    : __builtin_amdgcn_mov_dpp(u, 0x120 + 4, 0xf, 0xf, true));
+}
+
+__device__ inline std::int64_t broadcast(std::int64_t x, int lane)
+{
+    const std::uint32_t lo = std::uint32_t(__builtin_amdgcn_readlane(int(std::uint32_t(x)), lane));
+    const std::uint32_t hi = std::uint32_t(__builtin_amdgcn_readlane(int(std::uint32_t(std::uint64_t(x) >> 32)), lane));
+    return std::int64_t(std::uint64_t(hi) << 32 | lo);
+}
+
+// a / b, by 32 bits where they are enough: a division of 64 takes over a
+// hundred instructions.
+__device__ inline std::int64_t divide(std::int64_t a, int b) { return a >> 31 ? a / b : std::int64_t(unsigned(a) / unsigned(b)); }
+
+// kv8_sequence for a sequence that is the same in all lanes: by scalar loads,
+// so that all that follows from it stays in scalar registers.
+__device__ inline Kv8Sequence uniform_sequence(const sgemm_kv8_batch &b, int seq)
+{
+    auto cut = [&](int row) { return std::int64_t(row < 0 ? 0 : row < b.rows ? row : b.rows); };
+    const std::int64_t row0 = cut(uniform_load(b.starts, seq)), end = cut(uniform_load(b.starts, std::int64_t(seq) + 1));
+    const int len = uniform_load(b.lens, seq);
+    return {seq, len > 0 ? len : 0, end > row0 ? end - row0 : 0, row0};
+}
+
+// How the turns (32 tokens each) that a tile of rows sees are shared out when
+// rows are few: those of all sequences in one row, in equal parts to `slots`
+// work-groups, whatever the sequences' lengths. A part may end within a
+// sequence and go on in the next. Slot g takes turns g T / G .. (g + 1) T / G;
+// turn x belongs to slot ((x + 1) G - 1) / T. A part of a sequence that slot g
+// does has the number g + seq, which no other part of the tile has.
+struct Kv4Shares {
+    std::int64_t total;  // T
+    int slots;           // G: every slot has a turn
+    __device__ std::int64_t begin(int slot) const { return divide(total * slot, slots); }
+    __device__ int slot_of(std::int64_t turn) const { return int(total >> 31 ? ((turn + 1) * slots - 1) / total : divide((turn + 1) * slots - 1, int(total))); }
+};
+
+// Turns of a sequence that new rows `r_first` .. `r_last` see; one where it has
+// rows but they see nothing (somebody has to say so), none without rows.
+__device__ inline int kv4_turns(const Kv4AttendProblem &p, const Kv8Sequence &s, std::int64_t r_first, std::int64_t r_last, int shift)
+{
+    if (r_first >= s.n) return 0;
+    const KvSeen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, 1, p.causal, p.window};
+    int from, count, last, more;
+    seen.by_new(r_first, from, count);
+    seen.by_new(r_last < s.n ? r_last : s.n - 1, last, more);
+    const int turns = int((unsigned(last + more) + 31u) >> 5) - (from >> 5);
+    return turns < 1 ? 1 : turns;
+}
+
+// A value of the lane that the data-parallel primitive `Ctrl` names, in the rows
+// of 16 lanes of `Rows`; 0 elsewhere and past a row's first lane.
+template <int Ctrl, int Rows> __device__ inline std::int64_t shifted(std::int64_t x)
+{
+    const std::uint32_t lo = std::uint32_t(__builtin_amdgcn_update_dpp(0, int(std::uint32_t(x)), Ctrl, Rows, 0xf, false));
+    const std::uint32_t hi = std::uint32_t(__builtin_amdgcn_update_dpp(0, int(std::uint32_t(std::uint64_t(x) >> 32)), Ctrl, Rows, 0xf, false));
+    return std::int64_t(std::uint64_t(hi) << 32 | lo);
+}
+
+// 64 sequences from `first` on, one a lane: the sequence (none past the last),
+// its turns, and those of all sequences up to it.
+struct Kv4Group {
+    Kv8Sequence s;
+    int turns;
+    std::int64_t upto;
+};
+__device__ inline Kv4Group kv4_group(const Kv4AttendProblem &p, int first, std::int64_t before, std::int64_t r_first, std::int64_t r_last, int shift, int lane)
+{
+    Kv4Group g = {{first + lane, 0, 0, 0}, 0, 0};
+    if (first + lane < p.b.seqs) {
+        g.s = kv8_sequence(p.b, first + lane);
+        g.turns = kv4_turns(p, g.s, r_first, r_last, shift);
+    }
+    // Sums over the lanes before within each 16, then the last lanes' of the 16 and of the 32 before.
+    std::int64_t x = g.turns;
+    x += shifted<0x111, 0xf>(x);
+    x += shifted<0x112, 0xf>(x);
+    x += shifted<0x114, 0xf>(x);
+    x += shifted<0x118, 0xf>(x);
+    x += shifted<0x142, 0xa>(x);
+    x += shifted<0x143, 0xc>(x);
+    g.upto = x;
+    g.upto += before;
+    return g;
+}
+
+// The shares, given the first group.
+__device__ inline Kv4Shares kv4_shares(const Kv4AttendProblem &p, const Kv4Group &g0, std::int64_t r_first, std::int64_t r_last, int shift, int lane)
+{
+    std::int64_t total = broadcast(g0.upto, 63);
+    for (int first = 64; first < p.b.seqs; first += 64) total = broadcast(kv4_group(p, first, total, r_first, r_last, shift, lane).upto, 63);
+    const std::int64_t most = total / kKv4LeastTurns;
+    return {total, int(most < 1 ? 1 : most < p.plan.slots ? most : p.plan.slots)};
+}
+
+// Few rows: the four waves of a work-group take the turns of one row tile in
+// turn and add their sums through LDS, and the tile's turns over all sequences
+// are shared out to `slots` work-groups (Kv4Shares): what a work-group does of
+// a sequence that others work on too is left in the workspace, and
+// kv4_join_kernel adds it.
+//
+// A tile has 16 MT rows, or 16 / P where there are no more: the columns of the
+// matrix instruction then hold each row P times over, every copy takes a P-th of
+// the tokens through the softmax, and the weights come back to the first copy
+// for the second product.
+//
+// Codes and scales of the next turn are loaded as soon as this one's have gone
+// into the first product and been regrouped, before its softmax; nothing that
+// is loaded is looked at before its turn, so that no wait comes early. Pages
+// that may not be read are replaced by page 0 and their scores by NaN.
+//
+// 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 query heads each
+// (0.21 GB): 45.6 us, 4.6 TB/s, and 4.9 for the join; with equal splits of each
+// sequence instead of equal shares, and no copies, 50.0 and 5.0. Bound by
+// memory: the loads alone take 42.
+template <class T, int DC, bool Full, int MT, int P>
+__global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4AttendProblem p)
+{
+    static_assert(P == 1 || MT == 1, "copies only of one group of rows");
+    constexpr int PD = 32 * DC, kCols = 16 / P, kRows = kCols * MT, kDTiles = 2 * DC, kLd = PD + 4, kVWords = (DC + 3) / 4, E = 8 / P;
     __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows];
-    __shared__ __align__(16) float sm_o[Rows ? 4 : kRows * kLd];
+    __shared__ __align__(16) float sm_o[kAttendWaves][kRows * kLd];
+    typedef typename T::elem elem;
+    const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4, copy = c / kCols;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int dim = Full ? PD : p.c.dim, R = p.heads_q / p.c.heads;
+    const int shift = 31 - __builtin_clz(unsigned(p.c.block)), block = 1 << shift;
+
+    unsigned id = blockIdx.x;
+    const unsigned slots = p.plan.slots ? unsigned(p.plan.slots) : 1u;
+    const int slot = int(id % slots);
+    id /= slots;
+    const int tile0 = int(id % unsigned(p.plan.tiles));
+    id /= unsigned(p.plan.tiles);
+    const int head = int(id % unsigned(p.c.heads));
+    const unsigned seq0 = id / unsigned(p.c.heads), seqs_at_once = gridDim.x / (slots * unsigned(p.plan.tiles) * unsigned(p.c.heads));
+    const float factor = p.scale * kLog2e;
+    const std::uint8_t *const codes_k = static_cast<const std::uint8_t *>(p.c.K), *const codes_v = static_cast<const std::uint8_t *>(p.c.V);
+    const std::uint16_t *const scales_k = static_cast<const std::uint16_t *>(p.c.Ks), *const scales_v = static_cast<const std::uint16_t *>(p.c.Vs);
+    // Lanes past the head's components read its first ones: their queries are
+    // zero, their values give components that are not stored.
+    const int v_at = 4 * kq * (dim / 2) + (Full || c * 2 * DC < dim ? c * DC : 0);
+    int k_at[(DC + 1) / 2];  // of 16 components each
+#pragma unroll
+    for (int i = 0; i < DC; i += 2) k_at[i / 2] = c * (dim / 2) + (Full || (kq * DC + i) * 8 < dim ? (kq * DC + i) * 4 : 0);
+
+    // Turns `from` .. `to` of those that a sequence's rows `tile` see; `part`: the workspace's, or -1 for all of them.
+    auto piece = [&](const Kv8Sequence &s, std::int64_t tile, int from, int to, int part) {
+        const int seq = s.seq;
+        const std::int64_t all_rows = s.n * R, row0 = tile * kRows;
+        const KvSeen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, 1, p.causal, p.window};
+        const int *const table = p.b.table + std::int64_t(seq) * p.b.table_ld;
+        const int rows = int(all_rows - row0 < kRows ? all_rows - row0 : kRows);
+        const std::int64_t fresh0 = divide(row0, R);
+        const int rest0 = int(row0 - fresh0 * R);  // row i of the tile: new row fresh0 + (rest0 + i) / R, its query head (rest0 + i) % R
+
+        // Each lane's rows: what they see, and their operands. Rows past the
+        // last repeat it; what they give is not stored.
+        int lo_t[MT], n_t[MT];  // first token seen, tokens seen
+        QueryPieces<T, DC> raw[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            int row = 16 * t + c % kCols;
+            row = rest0 + (row < rows ? row : rows - 1);
+            const int fresh = int(unsigned(row) / unsigned(R));
+            seen.by_new(fresh0 + fresh, lo_t[t], n_t[t]);
+            const elem *src = static_cast<const elem *>(p.Q) + (s.row0 + fresh0 + fresh) * p.ldq + (head * R + row - fresh * R) * p.hsq;
+            raw[t].load(src + kq * DC * 8, [&](int i) { return Full || (kq * DC + i) * 8 < dim; });
+        }
+        int first_lo, first_n, last_lo, last_n;
+        seen.by_new(fresh0, first_lo, first_n);
+        seen.by_new(fresh0 + unsigned(rest0 + rows - 1) / unsigned(R), last_lo, last_n);
+        // Turns of 32 tokens: begin .. end sees some row; inner .. outer every row in full.
+        // (Positions reach 2^31 - 1, so that rounding up needs the sign bit.)
+        const int limit = last_lo + last_n, begin = first_lo >> 5, last = int((unsigned(limit) + 31u) >> 5);
+        const int inner = int((unsigned(last_lo) + 31u) >> 5), outer = (first_lo + first_n) >> 5;
+        const int end = to < last - begin ? begin + to : last;
+
+        f32x4 o[MT][kDTiles] = {};
+        float m[MT], l[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = 0.0f;
+
+        QOperand4<T> q[MT][DC];
+        float row_factor[MT];
+        // One turn's codes and scales, and whether its halves' pages may be read.
+        std::uint32_t k[2][DC], v[8][kVWords];
+        struct Scales {
+            std::uint32_t k[E / 2], v[E / 2];
+            bool good[2];
+        } scales;
+        struct Place {
+            std::int64_t token[2];
+            bool good[2];
+        };
+        auto place_of = [&](int turn) {
+            Place w;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                // Past the tokens seen (limit <= nameable) any page of the table will do; none is named by an empty one.
+                const int t = 32 * turn + 16 * x, page = uniform_load(table, (t < limit ? t : limit - 1) >> shift);
+                w.good[x] = unsigned(page) < unsigned(p.c.pages);
+                w.token[x] = ((std::int64_t(w.good[x] ? page : 0) * p.c.heads + head) << shift) + (t & (block - 1));
+            }
+            return w;
+        };
+        auto load_keys = [&](const Place &w) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const std::uint8_t *const at = codes_k + w.token[x] * (dim / 2);
+                if (Full) {
+                    __builtin_memcpy(k[x], at + k_at[0], 4 * DC);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < DC; i += 2) __builtin_memcpy(&k[x][i], at + k_at[i / 2], 8);
+                }
+            }
+        };
+        auto load_values = [&](const Place &w) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const std::uint8_t *const at = codes_v + w.token[x] * (dim / 2) + v_at;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (DC == 2) v[4 * x + e][0] = load_any<std::uint16_t>(at + e * (dim / 2));
+                    else __builtin_memcpy(v[4 * x + e], at + e * (dim / 2), DC);
+                }
+            }
+        };
+        auto load_scales = [&](const Place &w) {
+            Scales r;
+            r.good[0] = w.good[0];
+            r.good[1] = w.good[1];
+            // Those of this lane's copy: E adjacent ones of a half, or four of both.
+            if constexpr (P == 1) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    __builtin_memcpy(&r.k[2 * x], scales_k + w.token[x] + 4 * kq, 8);
+                    __builtin_memcpy(&r.v[2 * x], scales_v + w.token[x] + 4 * kq, 8);
+                }
+            } else {
+                const std::int64_t at = (copy * 2 / P ? w.token[1] : w.token[0]) + 4 * kq + copy * E % 4;
+                __builtin_memcpy(r.k, scales_k + at, 2 * E);
+                __builtin_memcpy(r.v, scales_v + at, 2 * E);
+            }
+            return r;
+        };
+
+        auto work = [&](int turn, int next) {
+            const bool cut = turn < inner || turn >= outer;  // some row does not see all of the turn
+            const Place then = place_of(next);
+            f32x4 acc[2][MT];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    acc[x][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < DC; ++i) acc[x][t] = q[t][i].scores(k[x][i], acc[x][t]);
+                }
+            load_keys(then);
+            // Byte x of even (odd): component 2 x (2 x + 1) of the word, of tokens 2 e and 2 e + 1.
+            std::uint32_t even[kVWords][4], odd[kVWords][4];
+#pragma unroll
+            for (int i = 0; i < kVWords; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const std::uint32_t a = v[2 * e][i], b = v[2 * e + 1][i];
+                    even[i][e] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+                    odd[i][e] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+                }
+            load_values(then);
+            const Scales own = scales;
+            scales = load_scales(then);
+            // Token i of this lane: number 16 * half + 4 kq + i % 4 of the turn.
+            float g[E], ev[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                // x * 0 + x: a scale that is not finite becomes NaN.
+                const float f = bits_f32(i & 1 ? own.k[i / 2] & 0xffff0000u : own.k[i / 2] << 16);
+                g[i] = __builtin_fmaf(f, 0.0f, f) * factor;
+            }
+            if (!(own.good[0] && own.good[1])) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const bool good = P == 1 ? own.good[i / 4] : copy * 2 / P ? own.good[1] : own.good[0];
+                    if (!good) g[i] = __builtin_nanf("");
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) exponents_of(own.v[i], ev[2 * i], ev[2 * i + 1]);
+            Frag ph[MT], pl[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                float z[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    if constexpr (P == 1) z[i] = acc[i / 4][t][i % 4];
+                    else if constexpr (P == 2) z[i] = copy ? acc[1][t][i] : acc[0][t][i];
+                    else {
+                        const float a = copy & 1 ? acc[0][t][2 + i] : acc[0][t][i], b = copy & 1 ? acc[1][t][2 + i] : acc[1][t][i];
+                        z[i] = copy & 2 ? b : a;
+                    }
+                    if (sizeof(elem) == 4) z[i] *= row_factor[t];
+                }
+                float y[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) y[i] = __builtin_fmaf(z[i], g[i], ev[i]);
+                unsigned sees = ~0u;  // bits of the tokens that the row sees
+                if (cut) {
+                    sees = 0;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const int half = P == 1 ? i / 4 : copy * 2 / P, at = P == 1 ? i % 4 : copy * E % 4 + i;
+                        const bool yes = unsigned(32 * turn + 16 * half + 4 * kq + at - lo_t[t]) < unsigned(n_t[t]);
+                        y[i] = yes ? y[i] : -__builtin_inff();
+                        sees |= yes ? 1u << i : 0u;
+                    }
+                }
+                float top = y[0];
+#pragma unroll
+                for (int i = 1; i < E; ++i) top = __builtin_fmaxf(top, y[i]);
+                top = column_max(copies_max<P>(top));
+                if (__ballot(top > m[t]) != 0) {
+                    const float risen = __builtin_fmaxf(m[t], top), a = rescale(m[t], risen);
+                    m[t] = risen;
+                    l[t] *= a;
+#pragma unroll
+                    for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
+                }
+                const float base = m[t] == -__builtin_inff() ? 0.0f : m[t] - (127.0f + 14.0f);
+                float w[E], pe[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    pe[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], g[i], -base));
+                    // A scale that is not finite makes the whole row NaN, by w or by its parts.
+                    w[i] = pe[i] * bits_f32(i & 1 ? own.v[i / 2] & 0xffff0000u : own.v[i / 2] << 16);
+                }
+                if (cut) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        if (!(sees >> i & 1)) pe[i] = w[i] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < E; ++i) l[t] += pe[i];
+                std::uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) split2(w[2 * i], w[2 * i + 1], hi[i], lo[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    ph[t].v[e] = from_copy<P>(hi, e);
+                    pl[t].v[e] = from_copy<P>(lo, e);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kVWords; ++i) {
+                auto byte = [&](auto at_) {
+                    constexpr int At = decltype(at_)::value;
+                    Frag f[2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[0].v[e] = fp4_f16<At>(even[i][e]), f[1].v[e] = fp4_f16<At>(odd[i][e]);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            f32x4 &sum = o[t][8 * i + 2 * At + j];
+                            sum = mfma_f16(f[j], ph[t], mfma_f16(f[j], pl[t], sum));
+                        }
+                };
+                byte(std::integral_constant<int, 0>{});
+                byte(std::integral_constant<int, 1>{});
+                if constexpr (DC > 2) {
+                    byte(std::integral_constant<int, 2>{});
+                    byte(std::integral_constant<int, 3>{});
+                }
+            }
+        };
+        int turn = begin + from + wave;
+        if (turn < end) {
+            // The first turn's codes are on their way before the queries, which came with the table, are looked at.
+            const Place first = place_of(turn);
+            load_keys(first);
+            load_values(first);
+            scales = load_scales(first);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) row_factor[t] = query_operands<T, DC>(raw[t], q[t]);
+            for (; turn < end; turn += kAttendWaves) {
+                const int next = turn + kAttendWaves < end ? turn + kAttendWaves : turn;
+                work(turn, next);
+            }
+        }
+
+        // The waves' sums, in LDS; then all onto the largest maximum.
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            // A row that sees no token is 0 / 1; one whose scores are all -inf is 0 / 0.
+            const float sum = column_sum(copies_sum<P>(l[t]));
+            if (c < kCols) {
+                if (kq == 0) sm_m[wave][16 * t + c] = m[t], sm_l[wave][16 * t + c] = n_t[t] == 0 ? 1.0f : sum;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int j = 0; j < kDTiles; j += 4)
+                        *reinterpret_cast<f32x4 *>(&sm_o[wave][(16 * t + c) * kLd + (4 * kq + r) * kDTiles + j]) =
+                            f32x4{o[t][j][r], o[t][j + 1][r], o[t][j + 2][r], o[t][j + 3][r]};
+            }
+        }
+        __syncthreads();
+        // A thread keeps one component quad of every 4 * 64 / (PD / 4)-th row.
+        constexpr int kQuads = PD / 4, kStep = 64 * kAttendWaves / kQuads;
+        const int d = int(threadIdx.x) % kQuads * 4;
+        for (int i = int(threadIdx.x) / kQuads; i < rows; i += kStep) {
+            float top = sm_m[0][i], sum = 0.0f;
+#pragma unroll
+            for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][i]);
+            f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < kAttendWaves; ++w) {
+                const float a = rescale(sm_m[w][i], top);
+                sum += sm_l[w][i] * a;
+                x += *reinterpret_cast<const f32x4 *>(&sm_o[w][i * kLd + d]) * a;
+            }
+            if (!Full && d >= dim) continue;
+            if (part < 0) {
+                const int fresh = int(unsigned(rest0 + i) / unsigned(R));
+                x = x / sum;
+                if (seen.beyond_new(fresh0 + fresh)) x = x * __builtin_nanf("");
+                __builtin_memcpy(p.O + (s.row0 + fresh0 + fresh) * p.ldo + (head * R + rest0 + i - fresh * R) * p.hso + d, &x, sizeof(x));
+            } else {
+                const std::int64_t at = ((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + part) * kRows + i;
+                *reinterpret_cast<f32x4 *>(p.ws + at * (dim + 4) + d) = x;
+                if (d == 0) p.ws[at * (dim + 4) + dim] = top, p.ws[at * (dim + 4) + dim + 1] = sum;
+            }
+        }
+        __syncthreads();
+    };
+
+    // Which pieces: first this work-group's share of the turns of tile `tile0`
+    // of all sequences, then whole tiles: all of them without shares, those
+    // beyond what the grid and the workspace were laid out for with them.
+    constexpr int kAll = 1 << 30;
+    const bool shared = p.plan.slots > 0;
+    const std::int64_t r_first = divide(std::int64_t(tile0) * kRows, R), r_last = divide(std::int64_t(tile0) * kRows + kRows - 1, R);
+    std::int64_t lo = 0, hi = 0, tile = tile0;
+    Kv4Group g = {};
+    std::uint64_t mine = 0;  // sequences of the 64 from `first` on that the share meets
+    int first = 0;
+    if (shared) {
+        g = kv4_group(p, 0, 0, r_first, r_last, shift, lane);
+        const Kv4Shares shares = kv4_shares(p, g, r_first, r_last, shift, lane);
+        if (slot < shares.slots) lo = shares.begin(slot), hi = shares.begin(slot + 1);
+        mine = __ballot(g.turns > 0 && g.upto > lo && g.upto - g.turns < hi);
+    }
+    bool whole = !shared;
+    int seq = shared ? slot : int(seq0);
+    const int step = shared ? p.plan.slots : int(seqs_at_once);
+    if (shared) tile += p.plan.tiles;
+    for (;;) {
+        int from = 0, to = kAll, part = -1;
+        Kv8Sequence s;
+        std::int64_t at = tile0;
+        if (!whole) {
+            while (mine == 0) {
+                const std::int64_t before = broadcast(g.upto, 63);
+                first += 64;
+                if (first >= p.b.seqs || before >= hi) {
+                    whole = true;
+                    break;
+                }
+                g = kv4_group(p, first, before, r_first, r_last, shift, lane);
+                mine = __ballot(g.turns > 0 && g.upto > lo && g.upto - g.turns < hi);
+            }
+        }
+        if (!whole) {
+            const int b = __builtin_ctzll(mine);
+            mine &= mine - 1;
+            const int count = __builtin_amdgcn_readlane(g.turns, b);
+            const std::int64_t start = broadcast(g.upto, b) - count;
+            from = int(start < lo ? lo - start : 0);
+            to = int(start + count > hi ? hi - start : count);
+            part = from == 0 && to == count ? -1 : slot + first + b;
+            s = {first + b, broadcast(g.s.len, b), broadcast(g.s.n, b), broadcast(g.s.row0, b)};
+        } else {
+            if (seq >= p.b.seqs) break;
+            s = uniform_sequence(p.b, seq);
+            at = tile;
+            tile += p.plan.tiles;
+            if (at * kRows >= s.n * R) {
+                seq += step;
+                tile = shared ? std::int64_t(tile0) + p.plan.tiles : tile0;
+                continue;
+            }
+        }
+        piece(s, at, from, to, part);
+    }
+}
+
+// Adds the sums that several work-groups left of one sequence's tile of rows: W
+// waves for each row, which take the parts in turn. One does for the few parts
+// that sequences have on average when there are many (4 parts of 1872 rows: 8.5
+// us with four waves a row); with few sequences four wait for a quarter of the
+// parts each.
+template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendProblem p)
+{
+    constexpr int kAtOnce = 4, kRowsHere = kAttendWaves / W;
+    __shared__ float sm_top[kAttendWaves], sm_sum[kAttendWaves];
+    __shared__ __align__(16) float sm_x[W > 1 ? kAttendWaves : 1][256];
+    const int lane = threadIdx.x & 63, R = p.heads_q / p.c.heads, dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block));
+    const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all_waves % W;
+    const int i = int(blockIdx.x % (Rows / kRowsHere)) * kRowsHere + all_waves / W;
+    unsigned id = blockIdx.x / (Rows / kRowsHere);
+    const int tile = int(id % unsigned(p.plan.tiles));
+    id /= unsigned(p.plan.tiles);
+    const int head = int(id % unsigned(p.c.heads)), seq = int(id / unsigned(p.c.heads));
+    const std::int64_t row = std::int64_t(tile) * Rows + i;
+    const std::int64_t r_first = divide(std::int64_t(tile) * Rows, R), r_last = divide(std::int64_t(tile) * Rows + Rows - 1, R);
+    const Kv4Group g0 = kv4_group(p, 0, 0, r_first, r_last, shift, lane);
+    const Kv4Shares shares = kv4_shares(p, g0, r_first, r_last, shift, lane);
+    Kv4Group g = g0;
+    for (int first = 64; first <= seq; first += 64) g = kv4_group(p, first, broadcast(g.upto, 63), r_first, r_last, shift, lane);
+    const int own = seq & 63, turns = __builtin_amdgcn_readlane(g.turns, own);
+    const Kv8Sequence s = {seq, broadcast(g.s.len, own), broadcast(g.s.n, own), broadcast(g.s.row0, own)};
+    if (row >= s.n * R) return;
+    const std::int64_t start = broadcast(g.upto, own) - turns;
+    const int first = shares.slot_of(start), parts = shares.slot_of(start + turns - 1) - first + 1;
+    if (parts == 1) return;  // written by the work-group itself (with W > 1 this is the same for all waves)
+    const std::int64_t pitch = std::int64_t(Rows) * (dim + 4);
+    const float *const part = p.ws + (((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + first + seq) * Rows + i) * (dim + 4);
+    float top = -__builtin_inff(), sum = 0.0f;
+    f32x4 y = {0, 0, 0, 0};
+    const float *const at = part + (4 * lane < dim ? 4 * lane : 0);
+    for (int x0 = wave; x0 < parts; x0 += W * kAtOnce) {
+        f32x4 v[kAtOnce];
+        float pm[kAtOnce], pl[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int x = x0 + W * j < parts ? x0 + W * j : x0;
+            v[j] = *reinterpret_cast<const f32x4 *>(at + x * pitch);
+            pm[j] = part[x * pitch + dim];
+            pl[j] = part[x * pitch + dim + 1];
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (x0 + W * j >= parts) continue;
+            // A part that saw nothing of its row weighs nothing: its sums are zeros.
+            const float risen = __builtin_fmaxf(top, pm[j]), a = rescale(top, risen), b = rescale(pm[j], risen);
+            top = risen;
+            sum = sum * a + pl[j] * b;
+            y = y * a + v[j] * b;
+        }
+    }
+    if constexpr (W > 1) {
+        if (lane == 0) sm_top[wave] = top, sm_sum[wave] = sum;
+        if (4 * lane < dim) *reinterpret_cast<f32x4 *>(&sm_x[wave][4 * lane]) = y;
+        __syncthreads();
+        if (wave != 0) return;
+        for (int w = 0; w < W; ++w) top = __builtin_fmaxf(top, sm_top[w]);
+        sum = 0.0f;
+        y = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float a = rescale(sm_top[w], top);
+            sum += sm_sum[w] * a;
+            if (4 * lane < dim) y += *reinterpret_cast<const f32x4 *>(&sm_x[w][4 * lane]) * a;
+        }
+    }
+    if (4 * lane >= dim) return;
+    y = y / sum;
+    const std::int64_t fresh = divide(row, R);
+    const KvSeen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, 1, p.causal, p.window};
+    if (seen.beyond_new(fresh)) y = y * __builtin_nanf("");
+    __builtin_memcpy(p.O + (s.row0 + fresh) * p.ldo + (std::int64_t(head) * R + row - fresh * R) * p.hso + 4 * lane, &y, sizeof(y));
+}
+
+template <class T, int DC, bool Full, int MT>
+__global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4AttendProblem p)
+{
+    constexpr int PD = 32 * DC, kRows = 16 * MT, kDTiles = 2 * DC, kVWords = (DC + 3) / 4;
     typedef typename T::elem elem;
     const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -174,12 +774,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
     const int shift = 31 - __builtin_clz(unsigned(p.c.block)), block = 1 << shift;
 
     unsigned id = blockIdx.x;
-    const int split = int(id % unsigned(p.plan.splits));
-    id /= unsigned(p.plan.splits);
     const int tile0 = int(id % unsigned(p.plan.tiles));
     id /= unsigned(p.plan.tiles);
     const int head = int(id % unsigned(p.c.heads));
-    const unsigned seqs_at_once = gridDim.x / (unsigned(p.plan.splits) * unsigned(p.plan.tiles) * unsigned(p.c.heads));
+    const unsigned seqs_at_once = gridDim.x / (unsigned(p.plan.tiles) * unsigned(p.c.heads));
     const float factor = p.scale * kLog2e;
     const std::uint8_t *const codes_k = static_cast<const std::uint8_t *>(p.c.K), *const codes_v = static_cast<const std::uint8_t *>(p.c.V);
     const std::uint16_t *const scales_k = static_cast<const std::uint16_t *>(p.c.Ks), *const scales_v = static_cast<const std::uint16_t *>(p.c.Vs);
@@ -188,17 +786,14 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
     const int k_at = c * (dim / 2), v_at = 4 * kq * (dim / 2) + (Full || c * 2 * DC < dim ? c * DC : 0);
 
     for (unsigned seq = id / unsigned(p.c.heads); seq < unsigned(p.b.seqs); seq += seqs_at_once) {
-        const Kv8Sequence s = kv8_sequence(p.b, int(seq));
+        const Kv8Sequence s = uniform_sequence(p.b, int(seq));
         const std::int64_t all_rows = s.n * R;
         const KvSeen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, R, p.causal, p.window};
         const int *const table = p.b.table + std::int64_t(seq) * p.b.table_ld;
         for (std::int64_t tile = tile0;; tile += p.plan.tiles) {
-            const std::int64_t row0 = Rows ? (tile * kAttendWaves + wave) * kRows : tile * kRows;
-            if ((Rows ? tile * kAttendWaves * kRows : row0) >= all_rows) break;
-            // Tiles beyond those the grid (and the workspace) was laid out for are not split.
-            const bool whole = p.plan.splits == 1 || tile >= p.plan.tiles;
-            if (whole && split > 0) break;
-            if (Rows && row0 >= all_rows) continue;  // no barrier below when Rows
+            const std::int64_t row0 = (tile * kAttendWaves + wave) * kRows;
+            if (tile * kAttendWaves * kRows >= all_rows) break;
+            if (row0 >= all_rows) continue;
 
             // Each lane's rows: what they see, and their operands. Rows past
             // the last repeat it; what they give is not stored.
@@ -211,7 +806,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
                 row = row < all_rows ? row : all_rows - 1;
                 seen(row, lo_t[t], n_t[t]);
                 const elem *src = static_cast<const elem *>(p.Q) + (s.row0 + row / R) * p.ldq + (head * R + row % R) * p.hsq;
-                row_factor[t] = load_query<T, DC>(q[t], src + kq * DC * 8, [&](int i) { return Full || (kq * DC + i) * 8 < dim; });
+                QueryPieces<T, DC> raw;
+                raw.load(src + kq * DC * 8, [&](int i) { return Full || (kq * DC + i) * 8 < dim; });
+                row_factor[t] = query_operands<T, DC>(raw, q[t]);
             }
             int first_lo, first_n, last_lo, last_n;
             seen(row0, first_lo, first_n);
@@ -219,13 +816,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
             // Turns of 32 tokens: begin .. end sees some row; inner .. outer every row in full.
             // (Positions reach 2^31 - 1, so that rounding up needs the sign bit.)
             const int limit = last_lo + last_n;
-            int begin = first_lo >> 5, end = int((unsigned(limit) + 31u) >> 5);
+            const int begin = first_lo >> 5, end = int((unsigned(limit) + 31u) >> 5);
             const int inner = int((unsigned(last_lo) + 31u) >> 5), outer = (first_lo + first_n) >> 5;
-            if (!whole) {
-                const int turns = end - begin, b = begin;
-                begin = b + int(std::int64_t(turns) * split / p.plan.splits);
-                end = b + int(std::int64_t(turns) * (split + 1) / p.plan.splits);
-            }
 
             f32x4 o[MT][kDTiles] = {};
             float m[MT], l[MT];
@@ -277,23 +869,22 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
                 }
             };
 
-            // Turns from .. to, this wave's among them; Cut: some row does not see all of a turn.
+            // Turns from .. to; Cut: some row does not see all of a turn.
             auto turns = [&](int from, int to, auto cut_) {
                 constexpr bool Cut = decltype(cut_)::value;
-                constexpr int kStride = Rows ? 1 : kAttendWaves;
-                int turn = from + (Rows ? 0 : (wave - from) & (kAttendWaves - 1));
+                int turn = from;
                 if (turn >= to) return;
                 {
                     const Half first[2] = {half_at(32 * turn), half_at(32 * turn + 16)};
                     load_keys(first);
                     load_values(first);
                 }
-                for (; turn < to; turn += kStride) {
-                    const int t0 = 32 * turn, tn = turn + kStride < to ? 32 * (turn + kStride) : t0;
+                for (; turn < to; ++turn) {
+                    const int t0 = 32 * turn, tn = turn + 1 < to ? t0 + 32 : t0;
                     const Half next[2] = {half_at(tn), half_at(tn + 16)};
                     f32x4 acc[2][MT];
                     float g[8], ev[8];
-                    if (Rows) __builtin_amdgcn_s_setprio(1);
+                    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
@@ -312,7 +903,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
 #pragma unroll
                         for (int r = 0; r < 2; ++r) exponents_of(vs[x][r], ev[4 * x + 2 * r], ev[4 * x + 2 * r + 1]);
                     }
-                    if (Rows) __builtin_amdgcn_s_setprio(0);
+                    __builtin_amdgcn_s_setprio(0);
                     load_keys(next);
                     Frag ph[MT], pl[MT];
 #pragma unroll
@@ -356,7 +947,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
                             pl[t].v[e] = lo;
                         }
                     }
-                    if (Rows) __builtin_amdgcn_s_setprio(1);
+                    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                     for (int i = 0; i < kVWords; ++i) {
                         // Byte x of even (odd): component 2 x (2 x + 1) of the word, of tokens 2 e and 2 e + 1.
@@ -387,7 +978,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
                             byte(std::integral_constant<int, 3>{});
                         }
                     }
-                    if (Rows) __builtin_amdgcn_s_setprio(0);
+                    __builtin_amdgcn_s_setprio(0);
                     load_values(next);
                 }
             };
@@ -406,102 +997,61 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_attend_kernel(Kv4Att
                 l[t] = n_t[t] == 0 ? 1.0f : sum;
             }
 
-            if constexpr (Rows) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const std::int64_t row = row0 + 16 * t + c;
-                    if (row >= all_rows) continue;
-                    float inverse = 1.0f / l[t];
-                    if (seen.beyond(row)) inverse = __builtin_nanf("");
-                    float *dst = p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + kq * 8 * DC;
-#pragma unroll
-                    for (int x = 0; x < 4 * kDTiles; x += 4) {
-                        if (!Full && kq * 8 * DC + x >= dim) continue;
-                        f32x4 y;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) y[j] = o[t][(x + j) % kDTiles][x / kDTiles] * inverse;
-                        __builtin_memcpy(dst + x, &y, sizeof(y));
-                    }
-                }
-                continue;
-            }
-
-            // The waves' sums: all onto the largest maximum.
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-                if (kq == 0) sm_m[wave][16 * t + c] = m[t], sm_l[wave][16 * t + c] = l[t];
-            __syncthreads();
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                float top = sm_m[0][16 * t + c];
+                const std::int64_t row = row0 + 16 * t + c;
+                if (row >= all_rows) continue;
+                float inverse = 1.0f / l[t];
+                if (seen.beyond(row)) inverse = __builtin_nanf("");
+                float *dst = p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + kq * 8 * DC;
 #pragma unroll
-                for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][16 * t + c]);
-                const float a = rescale(m[t], top);
+                for (int x = 0; x < 4 * kDTiles; x += 4) {
+                    if (!Full && kq * 8 * DC + x >= dim) continue;
+                    f32x4 y;
 #pragma unroll
-                for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
-            }
-            for (int w = 0; w < kAttendWaves; ++w) {
-                if (w == wave) {
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int j = 0; j < kDTiles; j += 4) {
-                                f32x4 *at = reinterpret_cast<f32x4 *>(&sm_o[(16 * t + c) * kLd + (4 * kq + r) * kDTiles + j]);
-                                const f32x4 x = {o[t][j][r], o[t][j + 1][r], o[t][j + 2][r], o[t][j + 3][r]};
-                                *at = w == 0 ? x : *at + x;
-                            }
-                }
-                __syncthreads();
-            }
-            const int rows = int(all_rows - row0 < kRows ? all_rows - row0 : kRows);
-            // A thread keeps one component quad of every 4 * 64 / (PD / 4)-th row.
-            constexpr int kQuads = PD / 4, kStep = 64 * kAttendWaves / kQuads;
-            const int d = int(threadIdx.x) % kQuads * 4;
-            for (int i = threadIdx.x / kQuads; i < rows; i += kStep) {
-                float top = sm_m[0][i], sum = 0.0f;
-#pragma unroll
-                for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][i]);
-#pragma unroll
-                for (int w = 0; w < kAttendWaves; ++w) sum += sm_l[w][i] * rescale(sm_m[w][i], top);
-                if (!Full && d >= dim) continue;
-                f32x4 x = *reinterpret_cast<const f32x4 *>(&sm_o[i * kLd + d]);
-                if (whole) {
-                    const std::int64_t row = row0 + i;
-                    x = x / sum;
-                    if (seen.beyond(row)) x = x * __builtin_nanf("");
-                    __builtin_memcpy(p.O + (s.row0 + row / R) * p.ldo + (head * R + row % R) * p.hso + d, &x, sizeof(x));
-                } else {
-                    const std::int64_t at = (((std::int64_t(seq) * p.c.heads + head) * p.plan.tiles + tile) * p.plan.splits + split) * kRows + i;
-                    *reinterpret_cast<f32x4 *>(p.ws + at * (dim + 4) + d) = x;
-                    if (d == 0) p.ws[at * (dim + 4) + dim] = top, p.ws[at * (dim + 4) + dim + 1] = sum;
+                    for (int j = 0; j < 4; ++j) y[j] = o[t][(x + j) % kDTiles][x / kDTiles] * inverse;
+                    __builtin_memcpy(dst + x, &y, sizeof(y));
                 }
             }
-            __syncthreads();
         }
     }
 }
 
-template <class T, int DC, bool Full, int MT, bool Rows> hipError_t launch_kv4_kernel(const Kv4AttendProblem &p, hipStream_t stream)
+template <class K> hipError_t launch_kv4_grid(K kernel, const Kv4AttendProblem &p, unsigned groups, unsigned threads, hipStream_t stream)
 {
-    const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads * p.plan.splits;
-    std::int64_t seqs = (std::int64_t(1) << 23) / per_seq;  // splits > 1: all of them (plan_kv4_attend)
-    seqs = seqs < 1 ? 1 : seqs < p.b.seqs ? seqs : p.b.seqs;
     Kv4AttendProblem q = p;
     void *args[] = {&q};
-    hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&kv4_attend_kernel<T, DC, Full, MT, Rows>), dim3(unsigned(per_seq * seqs)),
-                                   dim3(64 * kAttendWaves), args, 0, stream);
-    if (e != hipSuccess || p.plan.splits == 1) return e;
-    const unsigned units = unsigned(p.plan.tiles) * unsigned(p.c.heads) * unsigned(p.b.seqs);
-    return hipLaunchKernel(reinterpret_cast<const void *>(&kv_join_kernel<Kv4AttendProblem, MT>), dim3(units * (4 * MT)), dim3(256), args, 0, stream);
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(groups), dim3(threads), args, 0, stream);
+}
+
+template <class T, int DC, bool Full, int MT, int P> hipError_t launch_kv4_few(const Kv4AttendProblem &p, hipStream_t stream)
+{
+    constexpr int kRows = 16 * MT / P;
+    const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads;
+    if (p.plan.slots == 0) {
+        std::int64_t seqs = (std::int64_t(1) << 22) / per_seq;
+        seqs = seqs < 1 ? 1 : seqs < p.b.seqs ? seqs : p.b.seqs;
+        return launch_kv4_grid(&kv4_few_kernel<T, DC, Full, MT, P>, p, unsigned(per_seq * seqs), 64 * kAttendWaves, stream);
+    }
+    const hipError_t e = launch_kv4_grid(&kv4_few_kernel<T, DC, Full, MT, P>, p, unsigned(per_seq * p.plan.slots), 64 * kAttendWaves, stream);
+    if (e != hipSuccess) return e;
+    if (p.plan.slots > 8 * p.b.seqs) return launch_kv4_grid(&kv4_join_kernel<kRows, 4>, p, unsigned(per_seq * p.b.seqs * kRows), 256, stream);
+    return launch_kv4_grid(&kv4_join_kernel<kRows, 1>, p, unsigned(per_seq * p.b.seqs * (kRows / 4)), 256, stream);
 }
 
 template <class T, int DC, bool Full> hipError_t launch_kv4_shape(const Kv4AttendProblem &p, hipStream_t stream)
 {
     constexpr int kMost = DC > 4 ? 1 : 2;  // plan_kv4_attend gives no more
-    if (p.plan.rows) return launch_kv4_kernel<T, DC, Full, kMost, true>(p, stream);
-    return p.plan.mt == 1 ? launch_kv4_kernel<T, DC, Full, 1, false>(p, stream) : launch_kv4_kernel<T, DC, Full, kMost, false>(p, stream);
+    if (p.plan.rows) {
+        const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads;
+        std::int64_t seqs = (std::int64_t(1) << 22) / per_seq;
+        seqs = seqs < 1 ? 1 : seqs < p.b.seqs ? seqs : p.b.seqs;
+        return launch_kv4_grid(&kv4_rows_kernel<T, DC, Full, kMost>, p, unsigned(per_seq * seqs), 64 * kAttendWaves, stream);
+    }
+    if (p.plan.mt > 1) return launch_kv4_few<T, DC, Full, kMost, 1>(p, stream);
+    return p.plan.copies == 4   ? launch_kv4_few<T, DC, Full, 1, 4>(p, stream)
+           : p.plan.copies == 2 ? launch_kv4_few<T, DC, Full, 1, 2>(p, stream)
+                                : launch_kv4_few<T, DC, Full, 1, 1>(p, stream);
 }
 
 template <class T> hipError_t launch_kv4(const Kv4AttendProblem &p, hipStream_t stream)

@@ -33,7 +33,7 @@ struct Kv4AttendProblem {
     int heads_q;
     float scale;
     int causal, window;
-    Kv8Plan plan;
+    Kv4Plan plan;
 };
 hipError_t launch_kv4_attend_f32(const Kv4AttendProblem &p, hipStream_t stream);
 hipError_t launch_kv4_attend_bf16(const Kv4AttendProblem &p, hipStream_t stream);

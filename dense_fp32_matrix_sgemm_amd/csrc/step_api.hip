@@ -49,10 +49,10 @@ extern "C" int sgemm_kv4_attend(const sgemm_kv4_cache *cache, const sgemm_kv8_ba
     if (batch->seqs == 0 || batch->rows == 0) return SGEMM_OK;
     const int cus = sgemm_impl::current_gfx950_cus();
     if (cus == 0) return SGEMM_ERR_DEVICE;
-    sgemm_impl::Kv8Plan plan = sgemm_impl::plan_kv4_attend(*cache, *batch, heads_q, window, cus);
+    sgemm_impl::Kv4Plan plan = sgemm_impl::plan_kv4_attend(*cache, *batch, heads_q, window, cus);
     const std::size_t need = sgemm_kv4_attend_workspace_size(cache, batch, heads_q, window, cus);
     const bool usable = workspace != nullptr && reinterpret_cast<std::uintptr_t>(workspace) % 16 == 0 && workspace_bytes >= need;
-    if (!usable) plan.splits = 1;
+    if (!usable) plan.slots = 0;
     const sgemm_impl::Kv4AttendProblem p{*cache, *batch, Q, O, static_cast<float *>(workspace), ldq, hsq, ldo, hso, heads_q,
                                          scale, causal, window, plan};
     const hipStream_t s = static_cast<hipStream_t>(stream);

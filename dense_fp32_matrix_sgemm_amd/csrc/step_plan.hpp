@@ -7,8 +7,27 @@
 
 namespace sgemm_impl {
 
-// How attention over the 4-bit cache is laid out, as for the 8-bit one.
-Kv8Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus);
+// How attention over the 4-bit cache is laid out over the device; from sizes
+// the host knows, so that the workspace's size needs no device.
+struct Kv4Plan {
+    int rows;    // 1: a work-group's waves take row tiles of their own; 0: the tokens of one row tile
+    int mt;      // groups of 16 rows a wave holds
+    int copies;  // mt == 1: how often the 16 columns of a group hold each row (4, 2 or 1)
+    int tiles;   // row tiles (of one wave, or four when rows) per sequence and head the grid covers at once
+    int slots;   // work-groups that share the tokens that a row tile of all sequences sees; 0: one for each sequence
+    int parts;   // parts of sequences that they may leave in the workspace
+    int tile_rows() const { return 16 * mt / copies; }
+};
+
+// Turns of 32 tokens that a work-group which shares a tile's tokens has at
+// least, on average.
+constexpr int kKv4LeastTurns = 8;
+
+// Sequences whose turns are shared out together at most: each work-group adds
+// them all up.
+constexpr int kMostShared = 1024;
+
+Kv4Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus);
 
 // Whether sgemm_kv4_write's arrays overlap one another or the batch's.
 bool kv4_write_overlaps(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b);

@@ -700,9 +700,15 @@ int sgemm_kv4_check_args(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *ba
  * of this cache. The same rows, masks, query heads, workspace rule and checks;
  * a row that sees a token on a page that is not the cache's, or one whose scale
  * of K or V is not finite, gets NaN. Tokens a row does not see do not reach it.
+ * With the workspace the tokens of all sequences are shared out evenly, whatever
+ * their lengths: the last bits of a row then depend on the lengths in the batch,
+ * and are the same on every run.
  *
- * Scores are <Q, code> in float32 times scale * log2(e) * K's scale, and have
- * to stay within float32's normal numbers, as has p * V's scale.
+ * Scores are <Q, code> in float32 times scale * log2(e) * K's scale, and have to
+ * stay within float32's normal numbers, as has a value itself. float32 queries
+ * are held to 2^-22 of a component or 2^-39 of the row's largest, products of a
+ * weight and a value's scale to 2^-22 of themselves or 2^-39 of the row's
+ * largest, whichever is more; scales of V below 2^-90 count as 2^-90 there.
  */
 int sgemm_kv4_attend(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype, int heads_q,
                      const void *Q, int ldq, int hsq,
@@ -718,14 +724,22 @@ int sgemm_kv4_attend_check_args(const sgemm_kv4_cache *cache, const sgemm_kv8_ba
                                 const float *O, int ldo, int hso,
                                 const void *workspace, size_t workspace_bytes);
 
-/* Workspace bytes with which sgemm_kv4_attend splits this call's sequences on
+/* Workspace bytes with which sgemm_kv4_attend shares this call's tokens out on
  * a device with `cus` compute units (cus <= 0: 256), or 0 when it would not
- * split them (or the sizes are invalid). Pure host logic; reads no array. */
+ * (or the sizes are invalid). Pure host logic; reads no array. */
 size_t sgemm_kv4_attend_workspace_size(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int heads_q,
                                        int window, int cus);
 
-/* How sgemm_kv4_attend lays this call out, in shape[0..3]: as
- * sgemm_kv8_attend_shape() says of sgemm_kv8_attend, with the same statuses. */
+/*
+ * How sgemm_kv4_attend lays this call out on a device with `cus` compute units
+ * (cus <= 0: 256), in shape[0..3]: the rows (new rows times query heads of a
+ * cache head) of a wave's tile, the row tiles of a work-group (4: its waves
+ * take tiles of their own; 1: they share one tile's tokens), the work-groups
+ * along the rows of a sequence and head, and those that share out the tokens
+ * that a row tile sees of all sequences (given the workspace; 0: each sequence
+ * has its own). Pure host logic; reads no array. The statuses of
+ * sgemm_kv8_attend_shape().
+ */
 int sgemm_kv4_attend_shape(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int heads_q, int window, int cus,
                            int *shape);
 

@@ -392,7 +392,7 @@ def prompt_runs(case, Q, ratio, dtype, causal, window, want, what, hints=(130, 3
         if cus == 256:
             batch = sg.lowbit._batch(cache, *args, case.rows, max_new)
             shape = sg.sgemm_kv4_attend_shape(cache._struct, batch, 8 * ratio, window, cus)
-            assert shape[1] == 4 and shape[3] == 1
+            assert shape[1] == 4 and shape[3] == 0
         layout = ("packed", "padded", "heads")[i]
         out = views(torch.full(Q.shape, 3.25), layout)
         sg.kv4_attend(views(q, layout), cache, *args, scale=0.11, causal=causal, window=window, out=out, max_new=max_new)

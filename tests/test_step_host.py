@@ -126,13 +126,18 @@ def test_kv4_attend_shapes():
         return sg.sgemm_kv4_attend_shape(cache(heads=heads, dim=dim, block=64), batch(seqs=seqs, rows=rows, max_new=max_new, table_ld=columns),
                                          heads_q, window, cus)
 
-    assert shape(32, 32, 1, 128)[:3] == (16, 1, 1) and shape(32, 32, 1, 128)[3] > 1   # few rows: tokens split
-    assert shape(1000, 1000, 1, 128)[3] == 1                                          # sequences enough
-    assert shape(2, 2048, 1024, 80)[1:] == (4, shape(2, 2048, 1024, 80)[2], 1)        # prompts: row tiles a wave
-    assert shape(1, 1, 1, 1)[3] == 1 and shape(1, 1, 1, 128, window=64)[3] == 1       # few tokens to see
+    # Few rows: copies in the columns of a tile, and the tokens of all sequences shared out.
+    assert shape(32, 32, 1, 128)[:3] == (4, 1, 1) and shape(32, 32, 1, 128, heads_q=64)[:3] == (8, 1, 1)
+    assert shape(32, 32, 1, 128, heads_q=72)[:3] == (16, 1, 1) and shape(31, 31, 1, 128, heads_q=160)[:3] == (16, 1, 2)
+    assert shape(200, 200, 1, 128, heads_q=160)[:3] == (32, 1, 1) and shape(200, 200, 1, 128, heads_q=160, dim=256)[:3] == (16, 1, 2)
+    assert shape(32, 32, 1, 128)[3] == 96 and shape(32, 32, 1, 128, dim=256)[3] == 64
+    assert shape(1000, 1000, 1, 128)[3] == 0 and shape(1025, 1025, 1, 128, heads=1, heads_q=4)[3] == 0   # sequences enough
+    assert shape(1, 1, 1, 1)[3] == 0 and shape(1, 1, 1, 128, window=64)[3] == 0                         # few tokens to see
+    assert shape(1, 1, 1, 2**20, heads=1, heads_q=1)[3] == 64                                           # not all for one sequence
+    assert shape(2, 2048, 1024, 80)[:2] == (32, 4) and shape(2, 2048, 1024, 80)[3] == 0                 # prompts: row tiles a wave
     for s in ((32, 32, 1, 128), (2, 2048, 1024, 80), (1, 1, 1, 1)):
         b = batch(seqs=s[0], rows=s[1], max_new=s[2], table_ld=s[3])
-        assert (sg.sgemm_kv4_attend_workspace_size(cache(heads=8, dim=128, block=64), b, 32, 0, 256) > 0) == (shape(*s)[3] > 1)
+        assert (sg.sgemm_kv4_attend_workspace_size(cache(heads=8, dim=128, block=64), b, 32, 0, 256) > 0) == (shape(*s)[3] > 0)
 
 
 def rows_of(X=Q, Y=O, heads=2, ldx=128, hsx=64, ldy=128, hsy=64):
