@@ -687,10 +687,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
 }
 
 // Adds the sums that several work-groups left of one sequence's tile of rows: W
-// waves for each row, which take the parts in turn. One does for the few parts
-// that sequences have on average when there are many (4 parts of 1872 rows: 8.5
-// us with four waves a row); with few sequences four wait for a quarter of the
-// parts each.
+// waves for each row, which take the parts in turn. One does while sequences have
+// few parts on average (1820 rows of 4 parts: 4.8 us, with four waves a row 8.5);
+// with more of them four wait for a quarter each.
 template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendProblem p)
 {
     constexpr int kAtOnce = 4, kRowsHere = kAttendWaves / W;
@@ -763,6 +762,16 @@ template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kerne
     __builtin_memcpy(p.O + (s.row0 + fresh) * p.ldo + (std::int64_t(head) * R + row - fresh * R) * p.hso + 4 * lane, &y, sizeof(y));
 }
 
+// Prompts: the waves of a work-group take row tiles of their own; the same keys
+// and values pass through the compute unit's cache for all four. A wave keeps 32
+// rows, so that a code is converted once for them.
+//
+// 2 prompts of 1024 rows behind 4096 tokens in f16: 214 us, 558 TFLOP/s, bound by
+// the SIMDs: vector instructions take 75% of the cycles a compute unit is busy,
+// matrix instructions 37%, two of three of those for the second part of the
+// weights and the first. Codes converted once for the four waves and laid in LDS
+// need a quarter fewer vector instructions, but their barriers and reads cost
+// more than that: 233 to 246 us, with four waves or eight and two to four a SIMD.
 template <class T, int DC, bool Full, int MT>
 __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4AttendProblem p)
 {
@@ -781,8 +790,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
     const float factor = p.scale * kLog2e;
     const std::uint8_t *const codes_k = static_cast<const std::uint8_t *>(p.c.K), *const codes_v = static_cast<const std::uint8_t *>(p.c.V);
     const std::uint16_t *const scales_k = static_cast<const std::uint16_t *>(p.c.Ks), *const scales_v = static_cast<const std::uint16_t *>(p.c.Vs);
-    // Lanes past the head's components read its first ones: keys are then
-    // zeroed, values give components that are not stored.
+    // Lanes past the head's components read its first ones: their queries are
+    // zero, their values give components that are not stored.
     const int k_at = c * (dim / 2), v_at = 4 * kq * (dim / 2) + (Full || c * 2 * DC < dim ? c * DC : 0);
 
     for (unsigned seq = id / unsigned(p.c.heads); seq < unsigned(p.b.seqs); seq += seqs_at_once) {
@@ -848,12 +857,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                         for (int i = 0; i < DC; i += 2) {
                             const bool there = (kq * DC + i) * 8 < dim;
                             __builtin_memcpy(&k[x][i], at + (there ? (kq * DC + i) * 4 : 0), 8);
-                            k[x][i] = there ? k[x][i] : 0;
-                            k[x][i + 1] = there ? k[x][i + 1] : 0;
                         }
                     }
                     ks[x] = *reinterpret_cast<const u32x2 *>(scales_k + h[x].token + 4 * kq);
-                    if (!h[x].good) ks[x] = u32x2{~0u, ~0u};  // NaN
                 }
             };
             auto load_values = [&](const Half (&h)[2]) {
@@ -874,10 +880,12 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                 constexpr bool Cut = decltype(cut_)::value;
                 int turn = from;
                 if (turn >= to) return;
+                bool good[2];  // of this turn's halves
                 {
                     const Half first[2] = {half_at(32 * turn), half_at(32 * turn + 16)};
                     load_keys(first);
                     load_values(first);
+                    good[0] = first[0].good, good[1] = first[1].good;
                 }
                 for (; turn < to; ++turn) {
                     const int t0 = 32 * turn, tn = turn + 1 < to ? t0 + 32 : t0;
@@ -900,11 +908,16 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                             const float f = scale_of(ks[x], r);
                             g[4 * x + r] = __builtin_fmaf(f, 0.0f, f) * factor;
                         }
+                        if (!good[x]) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) g[4 * x + r] = __builtin_nanf("");
+                        }
 #pragma unroll
                         for (int r = 0; r < 2; ++r) exponents_of(vs[x][r], ev[4 * x + 2 * r], ev[4 * x + 2 * r + 1]);
                     }
                     __builtin_amdgcn_s_setprio(0);
                     load_keys(next);
+                    good[0] = next[0].good, good[1] = next[1].good;
                     Frag ph[MT], pl[MT];
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
