@@ -54,25 +54,63 @@ Lay lay_of(const Kv4Problem &p)
     return l;
 }
 
-// The largest value of a unit's lanes, in all of them.
+// The largest value of a unit's 2 to 32 lanes, in all of them: from the other
+// lane of a pair, the other pair of four, then the lanes of an eight and of a
+// sixteen in reverse, then the other sixteen.
+template <int Ctrl> __device__ inline std::uint32_t max_with(std::uint32_t m)
+{
+    const std::uint32_t o = std::uint32_t(__builtin_amdgcn_mov_dpp(int(m), Ctrl, 0xf, 0xf, true));
+    return o > m ? o : m;
+}
 __device__ inline std::uint32_t unit_max(std::uint32_t m, int group)
 {
-    for (int d = group / 2; d > 0; d >>= 1) {
-        const std::uint32_t o = std::uint32_t(__shfl_xor(int(m), d));
-        m = o > m ? o : m;
+    m = max_with<0xb1>(m);
+    if (group > 2) m = max_with<0x4e>(m);
+    if (group > 4) m = max_with<0x141>(m);
+    if (group > 8) m = max_with<0x140>(m);
+    if (group > 16) {
+        const auto x = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+        m = x[0] > x[1] ? x[0] : x[1];
     }
     return m;
 }
 
+// The largest size of eight elements, as the bits of a float32 (at least those
+// of infinity if one is not finite). The bits of a size grow with it in every
+// type, so the 16-bit ones are compared as they are, two at a time.
+template <class T> struct Eight {
+    typename T::elem x[8];
+};
+template <class T> __device__ inline std::uint32_t largest(const Eight<T> &v)
+{
+    if constexpr (sizeof(typename T::elem) == 4) {
+        std::uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const std::uint32_t a = f32_bits(v.x[j]) & 0x7fffffffu;
+            m = a > m ? a : m;
+        }
+        return m;
+    } else {
+        typedef __attribute__((ext_vector_type(2))) std::uint16_t u16x2;
+        const u32x4 w = __builtin_bit_cast(u32x4, v) & 0x7fff7fffu;
+        u16x2 m = __builtin_bit_cast(u16x2, w[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, std::uint32_t(w[j])));
+        return f32_bits(to_f32<T>(m[0] > m[1] ? m[0] : m[1]));
+    }
+}
+
 // The bits of a row's scale, from those of its largest size (at least those of
-// infinity: some value is not finite).
+// infinity: some value is not finite). The quotient by 6 is corrected by its
+// residual as the elements' are, and so rounded as a division's is (where it is
+// not among the subnormals, which are far below the least scale).
 __device__ inline std::uint16_t scale_bits(std::uint32_t amax)
 {
-    if (amax >= 0x7f800000u) return 0x7fc0u;
-    if (amax == 0) return 0;
-    const std::uint16_t s = from_f32<BF16>(bits_f32(amax) / 6.0f);
+    const float a = bits_f32(amax), sixth = 1.0f / 6.0f, y = a * sixth;
+    const std::uint16_t s = from_f32<BF16>(__builtin_fmaf(__builtin_fmaf(-y, 6.0f, a), sixth, y));
     constexpr std::uint16_t kLeast = 27u << 7;  // 2^-100
-    return s < kLeast ? kLeast : s;
+    return amax >= 0x7f800000u ? 0x7fc0u : amax == 0 ? 0u : s < kLeast ? kLeast : s;
 }
 
 __device__ inline std::uint32_t to_codes(const float *y)
@@ -91,18 +129,35 @@ __device__ inline void from_codes(std::uint32_t v, float *x)
     x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1], x[4] = c[0], x[5] = c[1], x[6] = d[0], x[7] = d[1];
 }
 
-template <class T> struct Eight {
-    typename T::elem x[8];
-};
+// Eight values times s, rounded to T.
+template <class T> __device__ inline void rounded(const float *x, float s, Eight<T> &out)
+{
+    if constexpr (sizeof(typename T::elem) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out.x[j] = x[j] * s;
+    } else {
+        u32x4 w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = rounded2<T>(x[2 * j] * s, x[2 * j + 1] * s);
+        out = __builtin_bit_cast(Eight<T>, w);
+    }
+}
 
-// Where a work-group's thread works, and the walk over the sequences, chunks
-// and heads that fall to it: body(sequence, head, first row of the thread).
+// A thread's place among its work-group's units, and a chunk of rows: the
+// sequence, where its table is, the chunk's first row and its position, and the
+// rows of the chunk. All but the thread's place is the same for a work-group.
 struct Place {
     int at, head, row, kv;  // first element; head and row within the work-group's; K (0) or V (1)
     bool there;
 };
+struct Chunk {
+    const int *table;
+    std::int64_t row0;
+    int t0, rows;
+};
 
-template <class Body> __device__ inline void for_each_chunk(const Kv4Problem &p, const Lay &l, Body &&body)
+// Calls body(chunk, place, head) for the chunks and heads that fall to this work-group.
+template <class Body> __device__ inline void for_each_chunk(const Kv4Problem &p, const Lay &l, int shift, Body &&body)
 {
     const int lane = int(threadIdx.x) & (l.group - 1), unit = int(threadIdx.x) / l.group;
     Place w;
@@ -116,55 +171,60 @@ template <class Body> __device__ inline void for_each_chunk(const Kv4Problem &p,
     const unsigned piece = id % l.pieces;
     for (unsigned seq = id / l.pieces; seq < unsigned(p.b.seqs); seq += l.seqs) {
         const Kv8Sequence s = kv8_sequence(p.b, int(seq));
-        for (std::int64_t row = std::int64_t(piece) * l.chunk; row < s.n; row += std::int64_t(l.pieces) * l.chunk)
-            for (int head = w.head; head - w.head < p.c.heads; head += l.across) body(s, w, head, row + w.row);
+        for (std::int64_t row = std::int64_t(piece) * l.chunk; row < s.n; row += std::int64_t(l.pieces) * l.chunk) {
+            const Chunk c = {p.b.table + std::int64_t(seq) * p.b.table_ld, s.row0 + row, int(s.len - s.n + row),
+                             int(s.n - row < l.chunk ? s.n - row : l.chunk)};
+            for (int head = 0; head < p.c.heads; head += l.across) body(c, w, head + w.head);
+        }
     }
+}
+
+// The page of position t, or -1 where there is none or the table names none of the cache's.
+__device__ inline int page_of(const Kv4Problem &p, const Chunk &c, int t, int shift)
+{
+    const int column = t >> shift;
+    if (t < 0 || column >= p.b.table_ld) return -1;
+    const int page = c.table[column];
+    return unsigned(page) < unsigned(p.c.pages) ? page : -1;
 }
 
 template <class T> __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Kv4Problem p, Lay l)
 {
     typedef typename T::elem elem;
-    const int dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block));
-    for_each_chunk(p, l, [&](const Kv8Sequence &s, const Place &w, int head, std::int64_t row0) {
+    const int dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block)), mask = p.c.block - 1;
+    const std::int64_t page_tokens = std::int64_t(p.c.heads) << shift;
+    for_each_chunk(p, l, shift, [&](const Chunk &c, const Place &w, int head) {
         const std::int64_t ld = w.kv ? p.ldv : p.ldk;
         const bool there = w.there && head < p.c.heads, mine = there && w.at < dim;
-        const elem *src = static_cast<const elem *>(w.kv ? p.V : p.K) + s.row0 * ld + (there ? head : 0) * (w.kv ? p.hsv : p.hsk) +
-                          (mine ? w.at : 0);
+        const elem *const src = static_cast<const elem *>(w.kv ? p.V : p.K) + c.row0 * ld + (there ? head : 0) * (w.kv ? p.hsv : p.hsk) +
+                                (mine ? w.at : 0);
         // All loads first, without conditions: rows past the last repeat it.
         Eight<T> v[kHeld];
-        std::int64_t page[kHeld];
+        int page[kHeld];
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            const std::int64_t r = row0 + i * l.deep;
-            v[i] = load_any<Eight<T>>(src + (r < s.n ? r : s.n - 1) * ld);
+            const int r = w.row + i * l.deep;
+            v[i] = load_any<Eight<T>>(src + (r < c.rows ? r : c.rows - 1) * ld);
         }
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            const std::int64_t r = row0 + i * l.deep, t = s.len - s.n + r;
-            page[i] = there && r < s.n && t >= 0 ? kv8_page(p.c, p.b, s.seq, t >> shift) : -1;
+            const int r = w.row + i * l.deep;
+            page[i] = there && r < c.rows ? page_of(p, c, c.t0 + r, shift) : -1;
         }
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            float x[8];
-            std::uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = to_f32<T>(v[i].x[j]);
-                const std::uint32_t a = f32_bits(x[j]) & 0x7fffffffu;
-                m = a > m ? a : m;
-            }
-            m = unit_max(mine ? m : 0, l.group);
+            const std::uint32_t m = unit_max(mine ? largest(v[i]) : 0u, l.group);
             const std::uint16_t sb = scale_bits(m);
-            const float scale = to_f32<BF16>(sb), r = m == 0 || m >= 0x7f800000u ? 0.0f : 1.0f / scale;
+            const float scale = to_f32<BF16>(sb), inverse = m == 0 ? 0.0f : __builtin_amdgcn_rcpf(scale);
+            float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float y = x[j] * r;
-                x[j] = __builtin_fmaf(__builtin_fmaf(-y, scale, x[j]), r, y);
+                const float x = to_f32<T>(v[i].x[j]), q = x * inverse;
+                y[j] = __builtin_fmaf(__builtin_fmaf(-q, scale, x), inverse, q);
             }
             if (page[i] < 0) continue;
-            const std::int64_t t = s.len - s.n + row0 + i * l.deep;
-            const std::int64_t token = ((page[i] * p.c.heads + head) << shift) + (t & ((1 << shift) - 1));
-            const std::uint32_t codes = m >= 0x7f800000u ? 0u : to_codes(x);
+            const std::int64_t token = page[i] * page_tokens + ((std::int64_t(head) << shift) + ((c.t0 + w.row + i * l.deep) & mask));
+            const std::uint32_t codes = m >= 0x7f800000u ? 0u : to_codes(y);
             if (mine) *reinterpret_cast<std::uint32_t *>(static_cast<std::uint8_t *>(w.kv ? p.c.V : p.c.K) + token * (dim / 2) + w.at / 2) = codes;
             if (w.at == 0) static_cast<std::uint16_t *>(w.kv ? p.c.Vs : p.c.Ks)[token] = sb;
         }
@@ -174,38 +234,39 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
 template <class T> __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4Problem p, Lay l)
 {
     typedef typename T::elem elem;
-    const int dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block));
-    for_each_chunk(p, l, [&](const Kv8Sequence &s, const Place &w, int head, std::int64_t row0) {
+    const int dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block)), mask = p.c.block - 1;
+    const std::int64_t page_tokens = std::int64_t(p.c.heads) << shift;
+    for_each_chunk(p, l, shift, [&](const Chunk &c, const Place &w, int head) {
         if (!w.there || head >= p.c.heads || w.at >= dim) return;
         const std::int64_t ld = w.kv ? p.ldv : p.ldk;
-        elem *dst = static_cast<elem *>(w.kv ? p.V : p.K) + s.row0 * ld + head * (w.kv ? p.hsv : p.hsk) + w.at;
-        std::int64_t page[kHeld], t[kHeld];
+        elem *const dst = static_cast<elem *>(w.kv ? p.V : p.K) + c.row0 * ld + head * (w.kv ? p.hsv : p.hsk) + w.at;
+        const std::uint8_t *const codes = static_cast<const std::uint8_t *>(w.kv ? p.c.V : p.c.K) + w.at / 2;
+        const std::uint16_t *const scales = static_cast<const std::uint16_t *>(w.kv ? p.c.Vs : p.c.Ks);
+        int page[kHeld];
         std::uint32_t v[kHeld];
-        float scale[kHeld];
+        std::uint16_t scale[kHeld];
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            const std::int64_t r = row0 + i * l.deep;
-            t[i] = r < s.n ? s.len - s.n + r : -1;
-            page[i] = t[i] >= 0 ? kv8_page(p.c, p.b, s.seq, t[i] >> shift) : -1;
+            const int r = w.row + i * l.deep;
+            page[i] = page_of(p, c, c.t0 + (r < c.rows ? r : c.rows - 1), shift);
         }
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             // A page that is not the cache's is not read: page 0 is in its place, and the rows are NaN.
-            const std::int64_t token = (((page[i] < 0 ? 0 : page[i]) * p.c.heads + head) << shift) + (t[i] & ((1 << shift) - 1));
-            v[i] = *reinterpret_cast<const std::uint32_t *>(static_cast<const std::uint8_t *>(w.kv ? p.c.V : p.c.K) + token * (dim / 2) + w.at / 2);
-            scale[i] = to_f32<BF16>(static_cast<const std::uint16_t *>(w.kv ? p.c.Vs : p.c.Ks)[token]);
+            const std::int64_t token = (page[i] < 0 ? 0 : page[i]) * page_tokens + ((std::int64_t(head) << shift) + ((c.t0 + w.row + i * l.deep) & mask));
+            v[i] = *reinterpret_cast<const std::uint32_t *>(codes + token * (dim / 2));
+            scale[i] = scales[token];
         }
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            if (t[i] < 0) continue;
-            float s1 = scale[i];
-            if (page[i] < 0 || (f32_bits(s1) & 0x7f800000u) == 0x7f800000u) s1 = __builtin_nanf("");
+            const int r = w.row + i * l.deep;
+            if (r >= c.rows || c.t0 + r < 0) continue;
+            const float s = page[i] < 0 || (scale[i] & 0x7f80u) == 0x7f80u ? __builtin_nanf("") : to_f32<BF16>(scale[i]);
             float x[8];
             from_codes(v[i], x);
             Eight<T> out;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) out.x[j] = from_f32<T>(x[j] * s1);
-            __builtin_memcpy(dst + (row0 + i * l.deep) * ld, &out, sizeof(out));
+            rounded<T>(x, s, out);
+            __builtin_memcpy(dst + r * ld, &out, sizeof(out));
         }
     });
 }

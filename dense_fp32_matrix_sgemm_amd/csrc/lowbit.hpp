@@ -109,6 +109,20 @@ template <> __device__ inline std::uint16_t from_f32<F16>(float x)
     return __builtin_bit_cast(std::uint16_t, _Float16(x));
 }
 
+// Two float32 rounded to a pair of a 16-bit type, the first in the low half.
+template <class T> __device__ inline std::uint32_t rounded2(float a, float b);
+template <> __device__ inline std::uint32_t rounded2<BF16>(float a, float b)
+{
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    return __builtin_bit_cast(std::uint32_t, bf16x2{__bf16(a), __bf16(b)});
+}
+template <> __device__ inline std::uint32_t rounded2<F16>(float a, float b)
+{
+    // As from_f32<F16>: a product is rounded to float32 first.
+    asm("" : "+v"(a), "+v"(b));
+    return __builtin_bit_cast(std::uint32_t, f16x2{_Float16(a), _Float16(b)});
+}
+
 // A scale of a runtime type.
 __device__ inline float load_scale(const void *S, int stype, std::int64_t i)
 {
