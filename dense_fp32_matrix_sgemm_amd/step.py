@@ -144,6 +144,15 @@ def _usual(t, index, heads, dim):
     return None
 
 
+def _like(t, dtype):
+    """A new contiguous tensor of t's shape and device."""
+    import torch
+
+    if t.dtype is dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
 def _pair(cache, K, V):
     """Type, places and strides of K and V, rows x heads x dim of one type."""
     k, v = _usual(K, cache._index, cache._heads, cache._dim), _usual(V, cache._index, cache._heads, cache._dim)
@@ -173,7 +182,7 @@ class KV4:
     to 256. K and V may be one tensor (so may Ks and Vs) to read and attend,
     but not for :func:`kv4_write`."""
 
-    __slots__ = ("_tensors", "_struct", "_device", "_index", "_i32", "_heads", "_dim")
+    __slots__ = ("_tensors", "_struct", "_device", "_index", "_i32", "_cus", "_heads", "_dim")
 
     def __init__(self, K, V, Ks, Vs):
         import torch
@@ -198,7 +207,7 @@ class KV4:
             raise ValueError("K, V, Ks and Vs must begin at a multiple of 16 bytes")
         _int32(pages=pages, heads=heads)
         self._tensors, self._device, self._heads, self._dim = (K, V, Ks, Vs), K.device, heads, dim
-        self._index, self._i32 = K.get_device(), torch.int32
+        self._index, self._i32, self._cus = K.get_device(), torch.int32, _cus(K.device)
         self._struct = KV4Cache(K.data_ptr(), V.data_ptr(), Ks.data_ptr(), Vs.data_ptr(), pages, heads, block, dim)
 
     K = property(lambda self: self._tensors[0])
@@ -269,7 +278,7 @@ def kv4_attend(Q, cache, table, lens, starts, scale=None, causal=True, window=0,
     ldq, hsq = _operand(Q, "Q", cache, heads_q, _types())
     rows, heads_q, dim = Q.shape
     if out is None:
-        out = torch.empty((rows, heads_q, dim), dtype=torch.float32, device=cache._device)
+        out = _like(Q, torch.float32)
         ldo, hso = heads_q * dim or 1, dim
     else:
         ldo, hso = _operand(out, "out", cache, heads_q, (torch.float32,))
@@ -281,7 +290,7 @@ def kv4_attend(Q, cache, table, lens, starts, scale=None, causal=True, window=0,
     lib = _lib()
     ws, ws_bytes = None, 0
     if workspace is None:
-        ws_bytes = lib.sgemm_kv4_attend_workspace_size(cache._struct, batch, heads_q, window, _cus(cache._device))
+        ws_bytes = lib.sgemm_kv4_attend_workspace_size(cache._struct, batch, heads_q, window, cache._cus)
         if ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=cache._device)
             ws = workspace.data_ptr()
@@ -324,15 +333,13 @@ def rope_frequencies(rot, base=10000.0, stretch=1.0, original=None, device="cuda
 
 def _rope_rows(X, Y, dtype, name):
     """(RopeRows, Y) of an operand X and its output Y (allocated when None)."""
-    import torch
-
     index = X.get_device()
     rows, heads, dim = X.shape
     x = _usual(X, index, heads, dim)
     if x is None:
         x = _heads(X, name)
     if Y is None:
-        Y = torch.empty((rows, heads, dim), dtype=dtype, device=X.device)
+        Y = _like(X, dtype)
         y = heads * dim or 1, dim
     else:
         y = _usual(Y, index, heads, dim)
@@ -364,16 +371,19 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
     """
     import torch
 
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or not Q.is_cuda or Q.dtype not in _types():
-        _need(Q, "Q", 3, _types())
-    index, (rows, _, dim) = Q.get_device(), Q.shape
-    if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.get_device() == index
-            and positions.shape == (rows,) and positions.is_contiguous() and isinstance(freqs, torch.Tensor)
-            and freqs.dtype is torch.float64 and freqs.get_device() == index and freqs.dim() == 1 and freqs.is_contiguous()):
+    types = _types()
+    try:
+        (rows, _, dim), index, (pairs,), code = Q.shape, Q.get_device(), freqs.shape, types[Q.dtype]
+        usual = (index >= 0 and positions.dtype is torch.int32 and positions.get_device() == index and positions.shape == (rows,)
+                 and positions.is_contiguous() and freqs.dtype is torch.float64 and freqs.get_device() == index and freqs.is_contiguous())
+    except (AttributeError, KeyError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        _need(Q, "Q", 3, types)
+        rows = Q.shape[0]
         _need(positions, "positions", 1, (torch.int32,), Q.device)
         _need(freqs, "freqs", 1, (torch.float64,), Q.device)
         raise ValueError(f"positions must be {rows} contiguous elements (has {positions.shape[0]}), freqs contiguous")
-    pairs = freqs.shape[0]
     if 2 * pairs > dim:
         raise ValueError(f"{pairs} pairs do not fit heads of {dim} components")
     if out is None:
@@ -388,7 +398,7 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
             raise TypeError("out must be a pair of tensors")
     if dtype is None:
         dtype = Q.dtype if out is None else outs[0].dtype
-    otype = _type_code(dtype, "dtype")
+    otype = code if dtype is Q.dtype else _type_code(dtype, "dtype")
     first, Y = _rope_rows(Q, outs[0], dtype, "Q")
     second = Z = None
     if K is not None:
@@ -399,7 +409,7 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
         second, Z = _rope_rows(K, outs[1], dtype, "K")
     if rows > _INT32_MAX:
         _int32(rows=rows)
-    _launch(index, _lib().sgemm_rope, _types()[Q.dtype], otype, rows, dim, 2 * pairs, 1 if interleaved else 0,
+    _launch(index, _lib().sgemm_rope, code, otype, rows, dim, 2 * pairs, 1 if interleaved else 0,
             1 if inverse else 0, amplitude, positions.data_ptr() or None, freqs.data_ptr() or None, first, second)
     return Y if K is None else (Y, Z)
 
