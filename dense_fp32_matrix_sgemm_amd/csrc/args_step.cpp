@@ -199,6 +199,7 @@ Kv4Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int 
 
     Kv4Plan plan = {};
     plan.copies = 1;
+    plan.cus = cus;
     // Waves take row tiles of their own once that gives every compute unit a work-group.
     const int most_mt = c.dim > 128 ? 1 : 2;  // longer heads have no registers for two
     plan.rows = rows >= 64 * most_mt && (heads >= cus || tiles_of(64 * most_mt) * heads >= cus);

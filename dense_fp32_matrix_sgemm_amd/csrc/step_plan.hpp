@@ -16,6 +16,7 @@ struct Kv4Plan {
     int tiles;   // row tiles (of one wave, or four when rows) per sequence and head the grid covers at once
     int slots;   // work-groups that share the tokens that a row tile of all sequences sees; 0: one for each sequence
     int parts;   // parts of sequences that they may leave in the workspace
+    int cus;     // compute units
     int tile_rows() const { return 16 * mt / copies; }
 };
 

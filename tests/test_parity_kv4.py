@@ -441,3 +441,27 @@ def test_prompts_with_rising_scales():
     want = case.ref.attend(Q, case.table, case.lens, case.starts, 0.11, True, 0)
     for dtype in ("f32", "bf16", "f16"):
         prompt_runs(case, Q, 1, dtype, True, 0, want, "rising")
+
+
+def test_prompts_whose_tiles_go_both_ways():
+    # Tiles of sequences and heads that begin in one round of work-groups and end in the next.
+    lens = [500, 420, 390, 17, 333, 470, 128, 256, 64]
+    case = Case4(51, lens, lens, 7, 16, 64)
+    Q = queries(case, 3)
+    q = torch.from_numpy(Q).to(torch.bfloat16)
+    cache, args = case.device(), case.args()
+    got = sg.kv4_attend(q.cuda(), cache, *args, max_new=500).cpu().double().numpy()
+    first = 0
+    for b, l in enumerate(lens):  # the last rows of each sequence, and its first: every tile has one of them or lies between
+        for part in (slice(0, min(l, 40)), slice(max(0, l - 90), l)):
+            rows = np.arange(l)[part]
+            one = np.array([0, len(rows)])
+            O, bound = case.ref.attend(Q[first + rows], case.table[b:b + 1], [int(rows[-1]) + 1], one, 64**-0.5, True, 0)
+            close(got[first + rows], O, bound, f"sequence {b}")
+        first += l
+    # And all rows against the same by tiles of one work-group each.
+    again = torch.zeros(q.shape, device="cuda")
+    for b in range(len(lens)):
+        a, e = int(case.starts[b]), int(case.starts[b + 1])
+        again[a:e] = sg.kv4_attend(q[a:e].cuda(), cache, args[0][b:b + 1], args[1][b:b + 1], torch.tensor([0, e - a], dtype=torch.int32).cuda(), max_new=1)
+    assert np.allclose(got, again.cpu().double().numpy(), rtol=1e-4, atol=1e-5)
