@@ -18,18 +18,21 @@
 //
 // Codes are exact in f16, so the weights may be held in two parts of f16, 22
 // bits, where bf16 would need three for as many, and a matrix instruction of
-// four is saved (prompts 259 -> 228 us). f16's range is made enough by a
+// four is saved. f16's range is made enough by a
 // common power of two for each row: the running maximum m is that of z +
 // exponent(V's scale) over the tokens seen, and weights are 2^(z - m + 14), so
 // that the largest product of a weight and a scale lies between 2^14 and 2^15
-// whatever the scales are. The sum l counts weights of the same factor, which
+// whatever the scales are (rows of scores beyond 2^14: far_exponents). The sum l counts weights of the same factor, which
 // the quotient drops. A product is held to 2^-22 of itself, or to 2^-39 of the
 // row's largest where that is more. Tokens that a row does not see take no part
 // in its maximum, so their scales do not cost it precision.
 //
 // While a wave feeds the matrix cores in a prompt its priority is raised: the
 // other wave of the SIMD then finds its vector instructions' turn while those
-// run (228 -> 216 us).
+// run.
+//
+// Both steps at 2 prompts of 1024 rows behind 4096 tokens, in f16: three parts
+// of bf16 259 us, two of f16 228, with the priority 216.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -180,6 +183,50 @@ template <int P> __device__ inline float copies_sum(float x)
     return x;
 }
 
+// What a row's weights are relative to: a token's weight is held as
+// 2^(x - far - m + kTarget), m being the largest x - far + ev over the tokens
+// seen, x a score and ev the exponent of its value's scale. `far` is 0 while m
+// lies within 2^14 of 0, and the score of the largest weight beyond, where m
+// would be rounded by more than 2^-10: differences of scores are formed before
+// an exponent is added to them, so that equal scores have equal weights however
+// large they are, and none leaves f16's range by a rounding.
+constexpr float kTarget = 127.0f + 14.0f;  // 127: the offset of exponents_of
+__device__ inline bool beyond_near(float m) { return __ballot(__builtin_fabsf(m) >= 16384.0f && m != -__builtin_inff()) != 0; }
+
+// What is left of a row's sums where m is raised to `risen` and far moved to `to`.
+__device__ inline float rescale_far(float far, float m, float to, float risen) { return rescale(far - to + m, risen); }
+
+// The larger of two such places, for sums that are to be joined.
+__device__ inline void raise(float &far, float &m, float far2, float m2)
+{
+    if (m2 == -__builtin_inff()) return;
+    const float to = m == -__builtin_inff() ? far2 : __builtin_fmaxf(far, far2);
+    m = __builtin_fmaxf(far - to + m, far2 - to + m2);
+    far = to;
+}
+
+// N scores (-inf where a row does not see the token) and exponents of far rows:
+// raises far and m, turns each score into its weight's exponent, and returns
+// what is left of the sums.
+template <int P, int N> __device__ inline float far_exponents(float (&x)[N], const float (&ev)[N], float &far, float &m)
+{
+    float score = x[0], top = -__builtin_inff();
+#pragma unroll
+    for (int i = 1; i < N; ++i) score = __builtin_fmaxf(score, x[i]);
+    score = column_max(copies_max<P>(score));
+    // A row that has seen nothing stands nowhere yet.
+    const float to = m == -__builtin_inff() ? (score == -__builtin_inff() ? far : score) : __builtin_fmaxf(far, score);
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = __builtin_fmaxf(top, x[i] - to + ev[i]);
+    const float risen = __builtin_fmaxf(far - to + m, column_max(copies_max<P>(top)));
+    const float a = rescale_far(far, m, to, risen), base = risen == -__builtin_inff() ? 0.0f : risen - kTarget;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = x[i] - to - base;
+    far = to;
+    m = risen;
+    return a;
+}
+
 // Pair e of the four pairs of weights of a row that its P copies hold in order,
 // in the lanes of the first copy. (What the others get is another row's.)
 template <int P, int N> __device__ inline std::uint32_t from_copy(const std::uint32_t (&own)[N], int e)
@@ -309,7 +356,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
 {
     static_assert(P == 1 || MT == 1, "copies only of one group of rows");
     constexpr int PD = 32 * DC, kCols = 16 / P, kRows = kCols * MT, kDTiles = 2 * DC, kLd = PD + 4, kVWords = (DC + 3) / 4, E = 8 / P;
-    __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows];
+    __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows], sm_far[kAttendWaves][kRows];
     __shared__ __align__(16) float sm_o[kAttendWaves][kRows * kLd];
     typedef typename T::elem elem;
     const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4, copy = c / kCols;
@@ -368,9 +415,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
         const int end = to < last - begin ? begin + to : last;
 
         f32x4 o[MT][kDTiles] = {};
-        float m[MT], l[MT];
+        float m[MT], l[MT], far[MT];
+        bool is_far[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = 0.0f;
+        for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = far[t] = 0.0f, is_far[t] = false;
 
         QOperand4<T> q[MT][DC];
         float row_factor[MT];
@@ -508,22 +556,38 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
                         sees |= yes ? 1u << i : 0u;
                     }
                 }
-                float top = y[0];
-#pragma unroll
-                for (int i = 1; i < E; ++i) top = __builtin_fmaxf(top, y[i]);
-                top = column_max(copies_max<P>(top));
-                if (__ballot(top > m[t]) != 0) {
-                    const float risen = __builtin_fmaxf(m[t], top), a = rescale(m[t], risen);
-                    m[t] = risen;
+                float x[E], w[E], pe[E];
+                auto shrink = [&](float a) {
                     l[t] *= a;
 #pragma unroll
                     for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
+                };
+                if (!is_far[t]) {
+                    float top = y[0];
+#pragma unroll
+                    for (int i = 1; i < E; ++i) top = __builtin_fmaxf(top, y[i]);
+                    top = column_max(copies_max<P>(top));
+                    if (__ballot(top > m[t]) != 0) {
+                        const float risen = __builtin_fmaxf(m[t], top);
+                        is_far[t] = beyond_near(risen);
+                        if (!is_far[t]) {
+                            const float a = rescale(m[t], risen);
+                            m[t] = risen;
+                            shrink(a);
+                        }
+                    }
+                    const float base = m[t] == -__builtin_inff() ? 0.0f : m[t] - kTarget;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) x[i] = __builtin_fmaf(z[i], g[i], -base);
                 }
-                const float base = m[t] == -__builtin_inff() ? 0.0f : m[t] - (127.0f + 14.0f);
-                float w[E], pe[E];
+                if (is_far[t]) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) x[i] = sees >> i & 1 ? z[i] * g[i] : -__builtin_inff();
+                    shrink(far_exponents<P>(x, ev, far[t], m[t]));
+                }
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    pe[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i], g[i], -base));
+                    pe[i] = __builtin_amdgcn_exp2f(x[i]);
                     // A scale that is not finite makes the whole row NaN, by w or by its parts.
                     w[i] = pe[i] * bits_f32(i & 1 ? own.v[i / 2] & 0xffff0000u : own.v[i / 2] << 16);
                 }
@@ -587,7 +651,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
             // A row that sees no token is 0 / 1; one whose scores are all -inf is 0 / 0.
             const float sum = column_sum(copies_sum<P>(l[t]));
             if (c < kCols) {
-                if (kq == 0) sm_m[wave][16 * t + c] = m[t], sm_l[wave][16 * t + c] = n_t[t] == 0 ? 1.0f : sum;
+                if (kq == 0) sm_m[wave][16 * t + c] = m[t], sm_far[wave][16 * t + c] = far[t], sm_l[wave][16 * t + c] = n_t[t] == 0 ? 1.0f : sum;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -601,13 +665,13 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
         constexpr int kQuads = PD / 4, kStep = 64 * kAttendWaves / kQuads;
         const int d = int(threadIdx.x) % kQuads * 4;
         for (int i = int(threadIdx.x) / kQuads; i < rows; i += kStep) {
-            float top = sm_m[0][i], sum = 0.0f;
+            float far = sm_far[0][i], top = sm_m[0][i], sum = 0.0f;
 #pragma unroll
-            for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][i]);
+            for (int w = 1; w < kAttendWaves; ++w) raise(far, top, sm_far[w][i], sm_m[w][i]);
             f32x4 x = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < kAttendWaves; ++w) {
-                const float a = rescale(sm_m[w][i], top);
+                const float a = rescale_far(sm_far[w][i], sm_m[w][i], far, top);
                 sum += sm_l[w][i] * a;
                 x += *reinterpret_cast<const f32x4 *>(&sm_o[w][i * kLd + d]) * a;
             }
@@ -620,7 +684,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
             } else {
                 const std::int64_t at = ((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + part) * kRows + i;
                 *reinterpret_cast<f32x4 *>(p.ws + at * (dim + 4) + d) = x;
-                if (d == 0) p.ws[at * (dim + 4) + dim] = top, p.ws[at * (dim + 4) + dim + 1] = sum;
+                if (d == 0) p.ws[at * (dim + 4) + dim] = top, p.ws[at * (dim + 4) + dim + 1] = sum, p.ws[at * (dim + 4) + dim + 2] = far;
             }
         }
         __syncthreads();
@@ -693,7 +757,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
 template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendProblem p)
 {
     constexpr int kAtOnce = 4, kRowsHere = kAttendWaves / W;
-    __shared__ float sm_top[kAttendWaves], sm_sum[kAttendWaves];
+    __shared__ float sm_top[kAttendWaves], sm_sum[kAttendWaves], sm_far[kAttendWaves];
     __shared__ __align__(16) float sm_x[W > 1 ? kAttendWaves : 1][256];
     const int lane = threadIdx.x & 63, R = p.heads_q / p.c.heads, dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block));
     const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all_waves % W;
@@ -716,40 +780,40 @@ template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kerne
     if (parts == 1) return;  // written by the work-group itself (with W > 1 this is the same for all waves)
     const std::int64_t pitch = std::int64_t(Rows) * (dim + 4);
     const float *const part = p.ws + (((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + first + seq) * Rows + i) * (dim + 4);
-    float top = -__builtin_inff(), sum = 0.0f;
+    float top = -__builtin_inff(), far = 0.0f, sum = 0.0f;
     f32x4 y = {0, 0, 0, 0};
     const float *const at = part + (4 * lane < dim ? 4 * lane : 0);
     for (int x0 = wave; x0 < parts; x0 += W * kAtOnce) {
         f32x4 v[kAtOnce];
-        float pm[kAtOnce], pl[kAtOnce];
+        f32x4 stand[kAtOnce];  // m, sum and far
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int x = x0 + W * j < parts ? x0 + W * j : x0;
             v[j] = *reinterpret_cast<const f32x4 *>(at + x * pitch);
-            pm[j] = part[x * pitch + dim];
-            pl[j] = part[x * pitch + dim + 1];
+            stand[j] = *reinterpret_cast<const f32x4 *>(part + x * pitch + dim);
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             if (x0 + W * j >= parts) continue;
             // A part that saw nothing of its row weighs nothing: its sums are zeros.
-            const float risen = __builtin_fmaxf(top, pm[j]), a = rescale(top, risen), b = rescale(pm[j], risen);
-            top = risen;
-            sum = sum * a + pl[j] * b;
+            const float from = far, m = top;
+            raise(far, top, stand[j][2], stand[j][0]);
+            const float a = rescale_far(from, m, far, top), b = rescale_far(stand[j][2], stand[j][0], far, top);
+            sum = sum * a + stand[j][1] * b;
             y = y * a + v[j] * b;
         }
     }
     if constexpr (W > 1) {
-        if (lane == 0) sm_top[wave] = top, sm_sum[wave] = sum;
+        if (lane == 0) sm_top[wave] = top, sm_sum[wave] = sum, sm_far[wave] = far;
         if (4 * lane < dim) *reinterpret_cast<f32x4 *>(&sm_x[wave][4 * lane]) = y;
         __syncthreads();
         if (wave != 0) return;
-        for (int w = 0; w < W; ++w) top = __builtin_fmaxf(top, sm_top[w]);
+        for (int w = 1; w < W; ++w) raise(far, top, sm_far[w], sm_top[w]);
         sum = 0.0f;
         y = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float a = rescale(sm_top[w], top);
+            const float a = rescale_far(sm_far[w], sm_top[w], far, top);
             sum += sm_sum[w] * a;
             if (4 * lane < dim) y += *reinterpret_cast<const f32x4 *>(&sm_x[w][4 * lane]) * a;
         }
@@ -766,12 +830,16 @@ template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kerne
 // and values pass through the compute unit's cache for all four. A wave keeps 32
 // rows, so that a code is converted once for them.
 //
-// 2 prompts of 1024 rows behind 4096 tokens in f16: 214 us, 558 TFLOP/s, bound by
+// 2 prompts of 1024 rows behind 4096 tokens in f16: 211 us, 564 TFLOP/s, bound by
 // the SIMDs: vector instructions take 75% of the cycles a compute unit is busy,
 // matrix instructions 37%, two of three of those for the second part of the
 // weights and the first. Codes converted once for the four waves and laid in LDS
 // need a quarter fewer vector instructions, but their barriers and reads cost
 // more than that: 233 to 246 us, with four waves or eight and two to four a SIMD.
+//
+// Rows that are far are found when m rises, and a tile that had one is done once
+// more with care for them: within the loop that care costs every tile 7%, the
+// look at m 1.5%.
 template <class T, int DC, bool Full, int MT>
 __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4AttendProblem p)
 {
@@ -835,9 +903,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
             const int inner = int((unsigned(last_lo) + 31u) >> 5), outer = (first_lo + first_n) >> 5;
 
             f32x4 o[MT][kDTiles] = {};
-            float m[MT], l[MT];
+            float m[MT], l[MT], far[MT];
+            bool far_off = false;  // some row has gone where it ought to be far
 #pragma unroll
-            for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = 0.0f;
+            for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = far[t] = 0.0f;
 
             // The page of a half turn, and where its first token lies; `good`: it may be read.
             struct Half {
@@ -881,9 +950,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                 }
             };
 
-            // Turns from .. to; Cut: some row does not see all of a turn.
-            auto turns = [&](int from, int to, auto cut_) {
-                constexpr bool Cut = decltype(cut_)::value;
+            // Turns from .. to; Cut: some row does not see all of a turn; Far: some
+            // row is far.
+            auto turns = [&](int from, int to, auto cut_, auto far_) {
+                constexpr bool Cut = decltype(cut_)::value, Far = decltype(far_)::value;
                 int turn = from;
                 if (turn >= to) return;
                 bool good[2];  // of this turn's halves
@@ -927,35 +997,51 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                     Frag ph[MT], pl[MT];
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
-                        unsigned seen = 0;  // bits of the tokens that the row sees
-                        float top = -__builtin_inff();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float y = __builtin_fmaf(acc[e / 4][t][e % 4], g[e], ev[e]);
-                            if (Cut) {
-                                const unsigned j = unsigned(t0 + 16 * (e / 4) + 4 * kq + e % 4 - lo_t[t]);
-                                const bool sees = j < unsigned(n_t[t]);
-                                y = sees ? y : -__builtin_inff();
-                                seen |= sees ? 1u << e : 0u;
-                            }
-                            top = __builtin_fmaxf(top, y);
-                        }
-                        top = column_max(top);
-                        if (__ballot(top > m[t]) != 0) {
-                            const float risen = __builtin_fmaxf(m[t], top), a = rescale(m[t], risen);
-                            m[t] = risen;
+                        unsigned sees = 0;  // bits of the tokens that the row sees
+                        float x[8], w[8];
+                        auto shrink = [&](float a) {
                             l[t] *= a;
 #pragma unroll
                             for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
+                        };
+                        auto sees_token = [&](int e) { return unsigned(t0 + 16 * (e / 4) + 4 * kq + e % 4 - lo_t[t]) < unsigned(n_t[t]); };
+                        if constexpr (!Far) {
+                            float top = -__builtin_inff();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float y = __builtin_fmaf(acc[e / 4][t][e % 4], g[e], ev[e]);
+                                if (Cut) {
+                                    const bool yes = sees_token(e);
+                                    y = yes ? y : -__builtin_inff();
+                                    sees |= yes ? 1u << e : 0u;
+                                }
+                                top = __builtin_fmaxf(top, y);
+                            }
+                            top = column_max(top);
+                            if (__ballot(top > m[t]) != 0) {
+                                const float risen = __builtin_fmaxf(m[t], top), a = rescale(m[t], risen);
+                                far_off |= beyond_near(risen);
+                                m[t] = risen;
+                                shrink(a);
+                            }
+                            const float base = m[t] == -__builtin_inff() ? 0.0f : m[t] - kTarget;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(acc[e / 4][t][e % 4], g[e], -base);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const bool yes = !Cut || sees_token(e);
+                                x[e] = yes ? acc[e / 4][t][e % 4] * g[e] : -__builtin_inff();
+                                sees |= yes ? 1u << e : 0u;
+                            }
+                            shrink(far_exponents<1>(x, ev, far[t], m[t]));
                         }
-                        const float base = m[t] == -__builtin_inff() ? 0.0f : m[t] - (127.0f + 14.0f);
-                        float w[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            float pe = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[e / 4][t][e % 4], g[e], -base));
+                            float pe = __builtin_amdgcn_exp2f(x[e]);
                             // A scale that is not finite makes the whole row NaN, by w or by its parts.
                             w[e] = pe * scale_of(vs[e / 4], e % 4);
-                            if (Cut && !(seen >> e & 1)) pe = w[e] = 0.0f;
+                            if (Cut && !(sees >> e & 1)) pe = w[e] = 0.0f;
                             l[t] += pe;
                         }
 #pragma unroll
@@ -1003,11 +1089,21 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
             };
             if (inner < outer) {
                 const int a = inner < end ? (inner > begin ? inner : begin) : end, b = outer < end ? (outer > a ? outer : a) : end;
-                turns(begin, a, std::true_type{});
-                turns(a, b, std::false_type{});
-                turns(b, end, std::true_type{});
+                turns(begin, a, std::true_type{}, std::false_type{});
+                turns(a, b, std::false_type{}, std::false_type{});
+                turns(b, end, std::true_type{}, std::false_type{});
             } else {
-                turns(begin, end, std::true_type{});
+                turns(begin, end, std::true_type{}, std::false_type{});
+            }
+            if (far_off) {
+                // Seldom: once more from the start.
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    m[t] = -__builtin_inff(), l[t] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < kDTiles; ++j) o[t][j] = f32x4{0, 0, 0, 0};
+                }
+                turns(begin, end, std::true_type{}, std::true_type{});
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t) {

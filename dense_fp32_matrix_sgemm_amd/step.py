@@ -88,7 +88,7 @@ def sgemm_kv4_attend_workspace_size(*args) -> int:
 
 
 def sgemm_kv4_attend_shape(cache, batch, heads_q, window=0, cus=0) -> tuple:
-    """Rows of a wave's tile, row tiles of a work-group, work-groups along the rows, splits of the tokens."""
+    """Rows of a wave's tile, row tiles of a work-group, work-groups along the rows, work-groups that share out the tokens of all sequences (0: none do)."""
     return _shape(_lib().sgemm_kv4_attend_shape, 4, cache, batch, heads_q, window, cus)
 
 

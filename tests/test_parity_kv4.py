@@ -465,3 +465,56 @@ def test_prompts_whose_tiles_go_both_ways():
         a, e = int(case.starts[b]), int(case.starts[b + 1])
         again[a:e] = sg.kv4_attend(q[a:e].cuda(), cache, args[0][b:b + 1], args[1][b:b + 1], torch.tensor([0, e - a], dtype=torch.int32).cuda(), max_new=1)
     assert np.allclose(got, again.cpu().double().numpy(), rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_equal_scores_of_every_size(layout, dtype):
+    # Every token has the same score, however large: the mean of the values seen. The
+    # weights are then equal to the bit, so that what is left are the roundings of a
+    # weight's parts (2^-22), of its product with a scale and of float32 sums over the
+    # tokens (2^-24 each a term). Where one token's key is twice the others', it takes
+    # all the weight of positive scores.
+    lens, new, heads = LAYOUTS[layout]
+    print(f"[kv4 equal] {layout} {dtype}", flush=True)
+    case = Case4(61, lens, new, heads, 16, 64)
+    case.ref.codes[0][:] = 0x22
+    case.ref.scales[0][:] = 0.75
+    Q = torch.ones((case.rows, heads, 64)).to(TYPES[dtype]).cuda()
+    V = [case.ref.tokens(case.table, b, lens[b], 1) for b in range(len(lens))]
+    args = case.args()
+    for twice in (None, 11):
+        if twice is not None:
+            for b in range(len(lens)):
+                if lens[b] > twice:
+                    case.ref.scales[0][case.table[b, twice // 16], :, twice % 16] = 1.5
+        cache = case.device()
+        for size in (0, 7, 13, 14, 15, 20, 22, 23, 24, 26, 30, 40, 100):
+            for sign in (1, -1) if twice is None else (1,):
+                got = sg.kv4_attend(Q, cache, *args, scale=sign * 2.0**size, max_new=max(new)).cpu().double().numpy()
+                for b in range(len(lens)):
+                    for i in range(new[b]):
+                        seen = V[b][:lens[b] - new[b] + i + 1]
+                        if twice is not None and len(seen) > twice:
+                            seen = seen[twice:twice + 1]
+                        close(got[case.starts[b] + i], seen.mean(axis=0), (len(seen) + 16) * 2.0**-22 * np.abs(seen).mean(axis=0) + 2.0**-37 * np.abs(seen).max(),
+                              f"{layout} {dtype} 2^{size} sign {sign} sequence {b} row {i}")
+
+
+@pytest.mark.parametrize("heads,ratio,dim", [(1, 2, 64), (2, 5, 80)])
+def test_many_sequences_share_their_tokens(heads, ratio, dim):
+    # More sequences than lanes of a wave, from empty to long, whose tokens are shared
+    # out together; parts that end within a sequence, and work-groups without one.
+    rng = np.random.default_rng(dim)
+    lens = [int(x) for x in rng.integers(0, 60, 150)]
+    for b in (0, 63, 64, 70, 149):
+        lens[b] = int(rng.integers(1500, 3000))
+    new = [min(l, int(n)) for l, n in zip(lens, rng.integers(0, 4, 150))]
+    new[64], new[149] = 9, 9
+    case = Case4(71, lens, new, heads, 16, dim)
+    shape = sg.sgemm_kv4_attend_shape(case.device()._struct, sg.KV8Batch(None, None, None, 150, case.table.shape[1], case.rows, 3), heads * ratio, 0)
+    assert shape[3] > 64
+    for max_new in (9, 3, 1):
+        attends(case, ratio, "bf16", max_new=max_new, what=f"max_new {max_new}")
+        attends(case, ratio, "f32", max_new=max_new, window=900, what=f"window, max_new {max_new}")
+    attends(case, ratio, "f16", causal=False, max_new=9, what="not causal")
