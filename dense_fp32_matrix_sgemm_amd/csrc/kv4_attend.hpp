@@ -273,6 +273,18 @@ struct Kv4Shares {
     __device__ int slot_of(std::int64_t turn) const { return int(total >> 31 ? ((turn + 1) * slots - 1) / total : divide((turn + 1) * slots - 1, int(total))); }
 };
 
+// How a sequence's tile of rows was shared out, behind the parts in the
+// workspace: the work-group that does its first part leaves this for the join.
+struct Kv4Split {
+    int slot, count;  // first slot; parts, or 0 if that one did all of it
+};
+static_assert(sizeof(Kv4Split) == kKv4SplitBytes, "the workspace has room for it");
+__device__ inline Kv4Split *kv4_split(const Kv4AttendProblem &p, int tile_rows, std::int64_t unit, int seq)
+{
+    const std::int64_t floats = std::int64_t(p.c.heads) * p.plan.tiles * p.plan.parts * tile_rows * (p.c.dim + 4);
+    return reinterpret_cast<Kv4Split *>(p.ws + floats) + unit * p.b.seqs + seq;
+}
+
 // Turns of a sequence that new rows `r_first` .. `r_last` see; one where it has
 // rows but they see nothing (somebody has to say so), none without rows.
 __device__ inline int kv4_turns(const Kv4AttendProblem &p, const Kv8Sequence &s, std::int64_t r_first, std::int64_t r_last, int shift)
@@ -700,9 +712,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
     Kv4Group g = {};
     std::uint64_t mine = 0;  // sequences of the 64 from `first` on that the share meets
     int first = 0;
+    Kv4Shares shares = {};
     if (shared) {
         g = kv4_group(p, 0, 0, r_first, r_last, shift, lane);
-        const Kv4Shares shares = kv4_shares(p, g, r_first, r_last, shift, lane);
+        shares = kv4_shares(p, g, r_first, r_last, shift, lane);
         if (slot < shares.slots) lo = shares.begin(slot), hi = shares.begin(slot + 1);
         mine = __ballot(g.turns > 0 && g.upto > lo && g.upto - g.turns < hi);
     }
@@ -735,6 +748,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
             to = int(start + count > hi ? hi - start : count);
             part = from == 0 && to == count ? -1 : slot + first + b;
             s = {first + b, broadcast(g.s.len, b), broadcast(g.s.n, b), broadcast(g.s.row0, b)};
+            if (from == 0 && threadIdx.x == 0)
+                *kv4_split(p, kRows, std::int64_t(head) * p.plan.tiles + tile0, s.seq) =
+                    {slot, to < count ? shares.slot_of(start + count - 1) - slot + 1 : 0};
         } else {
             if (seq >= p.b.seqs) break;
             s = uniform_sequence(p.b, seq);
@@ -750,10 +766,11 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
     }
 }
 
-// Adds the sums that several work-groups left of one sequence's tile of rows: W
-// waves for each row, which take the parts in turn. One does while sequences have
-// few parts on average (1820 rows of 4 parts: 4.8 us, with four waves a row 8.5);
-// with more of them four wait for a quarter each.
+// Adds the sums that several work-groups left of one sequence's tile of rows, as
+// the work-group that did the first part says: W waves for each row, which take the
+// parts in turn. One does while sequences have few parts on average (1820 rows of
+// 4 parts: 4.8 us, with four waves a row 8.5); with more of them four wait for a
+// quarter each.
 template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendProblem p)
 {
     constexpr int kAtOnce = 4, kRowsHere = kAttendWaves / W;
@@ -763,23 +780,16 @@ template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kerne
     const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all_waves % W;
     const int i = int(blockIdx.x % (Rows / kRowsHere)) * kRowsHere + all_waves / W;
     unsigned id = blockIdx.x / (Rows / kRowsHere);
-    const int tile = int(id % unsigned(p.plan.tiles));
-    id /= unsigned(p.plan.tiles);
-    const int head = int(id % unsigned(p.c.heads)), seq = int(id / unsigned(p.c.heads));
+    const int seq = int(id % unsigned(p.b.seqs));
+    id /= unsigned(p.b.seqs);
+    const int tile = int(id % unsigned(p.plan.tiles)), head = int(id / unsigned(p.plan.tiles));
+    const int *const split = reinterpret_cast<const int *>(kv4_split(p, Rows, id, seq));
+    const int slot = uniform_load(split, 0), parts = uniform_load(split, 1);  // not written where the sequence has no such rows
+    const Kv8Sequence s = uniform_sequence(p.b, seq);
     const std::int64_t row = std::int64_t(tile) * Rows + i;
-    const std::int64_t r_first = divide(std::int64_t(tile) * Rows, R), r_last = divide(std::int64_t(tile) * Rows + Rows - 1, R);
-    const Kv4Group g0 = kv4_group(p, 0, 0, r_first, r_last, shift, lane);
-    const Kv4Shares shares = kv4_shares(p, g0, r_first, r_last, shift, lane);
-    Kv4Group g = g0;
-    for (int first = 64; first <= seq; first += 64) g = kv4_group(p, first, broadcast(g.upto, 63), r_first, r_last, shift, lane);
-    const int own = seq & 63, turns = __builtin_amdgcn_readlane(g.turns, own);
-    const Kv8Sequence s = {seq, broadcast(g.s.len, own), broadcast(g.s.n, own), broadcast(g.s.row0, own)};
-    if (row >= s.n * R) return;
-    const std::int64_t start = broadcast(g.upto, own) - turns;
-    const int first = shares.slot_of(start), parts = shares.slot_of(start + turns - 1) - first + 1;
-    if (parts == 1) return;  // written by the work-group itself (with W > 1 this is the same for all waves)
+    if (row >= s.n * R || parts == 0) return;  // with W > 1 this is the same for all waves
     const std::int64_t pitch = std::int64_t(Rows) * (dim + 4);
-    const float *const part = p.ws + (((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + first + seq) * Rows + i) * (dim + 4);
+    const float *const part = p.ws + (((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + slot + seq) * Rows + i) * (dim + 4);
     float top = -__builtin_inff(), far = 0.0f, sum = 0.0f;
     f32x4 y = {0, 0, 0, 0};
     const float *const at = part + (4 * lane < dim ? 4 * lane : 0);

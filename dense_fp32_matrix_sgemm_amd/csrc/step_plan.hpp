@@ -24,6 +24,9 @@ struct Kv4Plan {
 // least, on average.
 constexpr int kKv4LeastTurns = 8;
 
+// What the workspace holds of each sequence and row tile besides parts (Kv4Split).
+constexpr int kKv4SplitBytes = 8;
+
 // Sequences whose turns are shared out together at most: each work-group adds
 // them all up.
 constexpr int kMostShared = 1024;
