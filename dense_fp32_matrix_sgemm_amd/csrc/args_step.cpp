@@ -198,27 +198,28 @@ Kv4Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int 
     const auto cut = [&](i64 tiles) { return int(tiles < most ? tiles : most); };
 
     Kv4Plan plan = {};
-    plan.copies = 1;
     plan.cus = cus;
     // Waves take row tiles of their own once that gives every compute unit a work-group.
-    const int most_mt = c.dim > 128 ? 1 : 2;  // longer heads have no registers for two
-    plan.rows = rows >= 64 * most_mt && (heads >= cus || tiles_of(64 * most_mt) * heads >= cus);
+    const int groups = c.dim > 128 ? 1 : 2;  // longer heads have no registers for two
+    plan.rows = rows >= 64 * groups && (heads >= cus || tiles_of(64 * groups) * heads >= cus);
     if (plan.rows) {
-        plan.mt = most_mt;
-        plan.tiles = cut(tiles_of(64 * most_mt));
+        plan.copies = 1;
+        plan.mt = groups;
+        plan.tiles = cut(tiles_of(64 * groups));
         return plan;
     }
-    // Two groups of 16 rows a wave halve the work on codes a row, once the
-    // device is full without them.
-    plan.mt = rows > 16 && tiles_of(16) * heads >= 2 * i64(cus) ? most_mt : 1;
-    if (plan.mt == 1) plan.copies = rows <= 4 ? 4 : rows <= 8 ? 2 : 1;
+    // Else they share one group of 16. Two would halve the work on codes a row, but
+    // leave registers for fewer waves: 32 sequences of 2000 tokens and 20 rows 45
+    // us, with two 39, but in float32 47 and 52, and 64 of 200 and 100 rows 51 and 54.
+    plan.mt = 1;
+    plan.copies = rows <= 4 ? 4 : rows <= 8 ? 2 : 1;
     plan.tiles = cut(tiles_of(plan.tile_rows()));
     // As many work-groups as the compute units hold at once share the tokens of
     // all sequences, each with at least 256 of those that the longest sequences
     // can have, unless there are many times as many sequences and heads in any case.
-    // (Three of them, or two with 16 rows of more than 64 components or more rows:
-    // 8 sequences of 4096 tokens and 16 rows 28 us, with three a unit 35.)
-    const int resident = c.dim > 128 || plan.mt > 1 || (plan.copies == 1 && c.dim > 64) ? 2 : 3;
+    // (Three of them, or two with more than 8 rows of more than 64 components: 8
+    // sequences of 4096 tokens and 16 rows 28 us, with three a unit 35.)
+    const int resident = c.dim > 128 || (plan.copies == 1 && c.dim > 64) ? 2 : 3;
     const i64 units = i64(plan.tiles) * c.heads;
     if (b.seqs > kMostShared || units * b.seqs >= 4 * resident * i64(cus)) return plan;
     i64 tokens = i64(b.table_ld) * c.block;

@@ -349,7 +349,7 @@ __device__ inline Kv4Shares kv4_shares(const Kv4AttendProblem &p, const Kv4Group
 // a sequence that others work on too is left in the workspace, and
 // kv4_join_kernel adds it.
 //
-// A tile has 16 MT rows, or 16 / P where there are no more: the columns of the
+// A tile has 16 rows, or 16 / P where there are no more: the columns of the
 // matrix instruction then hold each row P times over, every copy takes a P-th of
 // the tokens through the softmax, and the weights come back to the first copy
 // for the second product.
@@ -363,15 +363,14 @@ __device__ inline Kv4Shares kv4_shares(const Kv4AttendProblem &p, const Kv4Group
 // (0.21 GB): 45.6 us, 4.6 TB/s, and 4.9 for the join; with equal splits of each
 // sequence instead of equal shares, and no copies, 50.0 and 5.0. Bound by
 // memory: the loads alone take 42.
-template <class T, int DC, bool Full, int MT, int P>
+template <class T, int DC, bool Full, int P>
 __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4AttendProblem p)
 {
-    static_assert(P == 1 || MT == 1, "copies only of one group of rows");
-    constexpr int PD = 32 * DC, kCols = 16 / P, kRows = kCols * MT, kDTiles = 2 * DC, kLd = PD + 4, kVWords = (DC + 3) / 4, E = 8 / P;
+    constexpr int PD = 32 * DC, kRows = 16 / P, kDTiles = 2 * DC, kLd = PD + 4, kVWords = (DC + 3) / 4, E = 8 / P;
     __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows], sm_far[kAttendWaves][kRows];
     __shared__ __align__(16) float sm_o[kAttendWaves][kRows * kLd];
     typedef typename T::elem elem;
-    const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4, copy = c / kCols;
+    const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4, copy = c / kRows;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int dim = Full ? PD : p.c.dim, R = p.heads_q / p.c.heads;
     const int shift = 31 - __builtin_clz(unsigned(p.c.block)), block = 1 << shift;
@@ -404,19 +403,15 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
         const std::int64_t fresh0 = divide(row0, R);
         const int rest0 = int(row0 - fresh0 * R);  // row i of the tile: new row fresh0 + (rest0 + i) / R, its query head (rest0 + i) % R
 
-        // Each lane's rows: what they see, and their operands. Rows past the
-        // last repeat it; what they give is not stored.
-        int lo_t[MT], n_t[MT];  // first token seen, tokens seen
-        QueryPieces<T, DC> raw[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            int row = 16 * t + c % kCols;
-            row = rest0 + (row < rows ? row : rows - 1);
-            const int fresh = int(unsigned(row) / unsigned(R));
-            seen.by_new(fresh0 + fresh, lo_t[t], n_t[t]);
-            const elem *src = static_cast<const elem *>(p.Q) + (s.row0 + fresh0 + fresh) * p.ldq + (head * R + row - fresh * R) * p.hsq;
-            raw[t].load(src + kq * DC * 8, [&](int i) { return Full || (kq * DC + i) * 8 < dim; });
-        }
+        // Each lane's row: what it sees, and its operands. Rows past the last
+        // repeat it; what they give is not stored.
+        int lo_t, n_t;  // first token seen, tokens seen
+        QueryPieces<T, DC> raw;
+        const int row = rest0 + (c % kRows < rows ? c % kRows : rows - 1);
+        const int fresh = int(unsigned(row) / unsigned(R));
+        seen.by_new(fresh0 + fresh, lo_t, n_t);
+        const elem *src = static_cast<const elem *>(p.Q) + (s.row0 + fresh0 + fresh) * p.ldq + (head * R + row - fresh * R) * p.hsq;
+        raw.load(src + kq * DC * 8, [&](int i) { return Full || (kq * DC + i) * 8 < dim; });
         int first_lo, first_n, last_lo, last_n;
         seen.by_new(fresh0, first_lo, first_n);
         seen.by_new(fresh0 + unsigned(rest0 + rows - 1) / unsigned(R), last_lo, last_n);
@@ -426,14 +421,12 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
         const int inner = int((unsigned(last_lo) + 31u) >> 5), outer = (first_lo + first_n) >> 5;
         const int end = to < last - begin ? begin + to : last;
 
-        f32x4 o[MT][kDTiles] = {};
-        float m[MT], l[MT], far[MT];
-        bool is_far[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = far[t] = 0.0f, is_far[t] = false;
+        f32x4 o[kDTiles] = {};
+        float m = -__builtin_inff(), l = 0.0f, far = 0.0f;
+        bool is_far = false;
 
-        QOperand4<T> q[MT][DC];
-        float row_factor[MT];
+        QOperand4<T> q[DC];
+        float row_factor;
         // One turn's codes and scales, and whether its halves' pages may be read.
         std::uint32_t k[2][DC], v[8][kVWords];
         struct Scales {
@@ -500,15 +493,13 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
         auto work = [&](int turn, int next) {
             const bool cut = turn < inner || turn >= outer;  // some row does not see all of the turn
             const Place then = place_of(next);
-            f32x4 acc[2][MT];
+            f32x4 acc[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x) {
+                acc[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    acc[x][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int i = 0; i < DC; ++i) acc[x][t] = q[t][i].scores(k[x][i], acc[x][t]);
-                }
+                for (int i = 0; i < DC; ++i) acc[x] = q[i].scores(k[x][i], acc[x]);
+            }
             load_keys(then);
             // Byte x of even (odd): component 2 x (2 x + 1) of the word, of tokens 2 e and 2 e + 1.
             std::uint32_t even[kVWords][4], odd[kVWords][4];
@@ -540,84 +531,81 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
             }
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) exponents_of(own.v[i], ev[2 * i], ev[2 * i + 1]);
-            Frag ph[MT], pl[MT];
+            Frag ph, pl;
+            float z[E];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                float z[E];
+            for (int i = 0; i < E; ++i) {
+                if constexpr (P == 1) z[i] = acc[i / 4][i % 4];
+                else if constexpr (P == 2) z[i] = copy ? acc[1][i] : acc[0][i];
+                else {
+                    const float a = copy & 1 ? acc[0][2 + i] : acc[0][i], b = copy & 1 ? acc[1][2 + i] : acc[1][i];
+                    z[i] = copy & 2 ? b : a;
+                }
+                if (sizeof(elem) == 4) z[i] *= row_factor;
+            }
+            float y[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) y[i] = __builtin_fmaf(z[i], g[i], ev[i]);
+            unsigned sees = ~0u;  // bits of the tokens that the row sees
+            if (cut) {
+                sees = 0;
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    if constexpr (P == 1) z[i] = acc[i / 4][t][i % 4];
-                    else if constexpr (P == 2) z[i] = copy ? acc[1][t][i] : acc[0][t][i];
-                    else {
-                        const float a = copy & 1 ? acc[0][t][2 + i] : acc[0][t][i], b = copy & 1 ? acc[1][t][2 + i] : acc[1][t][i];
-                        z[i] = copy & 2 ? b : a;
+                    const int half = P == 1 ? i / 4 : copy * 2 / P, at = P == 1 ? i % 4 : copy * E % 4 + i;
+                    const bool yes = unsigned(32 * turn + 16 * half + 4 * kq + at - lo_t) < unsigned(n_t);
+                    y[i] = yes ? y[i] : -__builtin_inff();
+                    sees |= yes ? 1u << i : 0u;
+                }
+            }
+            float x[E], w[E], pe[E];
+            auto shrink = [&](float a) {
+                l *= a;
+#pragma unroll
+                for (int j = 0; j < kDTiles; ++j) o[j] *= a;
+            };
+            if (!is_far) {
+                float top = y[0];
+#pragma unroll
+                for (int i = 1; i < E; ++i) top = __builtin_fmaxf(top, y[i]);
+                top = column_max(copies_max<P>(top));
+                if (__ballot(top > m) != 0) {
+                    const float risen = __builtin_fmaxf(m, top);
+                    is_far = beyond_near(risen);
+                    if (!is_far) {
+                        const float a = rescale(m, risen);
+                        m = risen;
+                        shrink(a);
                     }
-                    if (sizeof(elem) == 4) z[i] *= row_factor[t];
                 }
-                float y[E];
+                const float base = m == -__builtin_inff() ? 0.0f : m - kTarget;
 #pragma unroll
-                for (int i = 0; i < E; ++i) y[i] = __builtin_fmaf(z[i], g[i], ev[i]);
-                unsigned sees = ~0u;  // bits of the tokens that the row sees
-                if (cut) {
-                    sees = 0;
+                for (int i = 0; i < E; ++i) x[i] = __builtin_fmaf(z[i], g[i], -base);
+            }
+            if (is_far) {
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const int half = P == 1 ? i / 4 : copy * 2 / P, at = P == 1 ? i % 4 : copy * E % 4 + i;
-                        const bool yes = unsigned(32 * turn + 16 * half + 4 * kq + at - lo_t[t]) < unsigned(n_t[t]);
-                        y[i] = yes ? y[i] : -__builtin_inff();
-                        sees |= yes ? 1u << i : 0u;
-                    }
-                }
-                float x[E], w[E], pe[E];
-                auto shrink = [&](float a) {
-                    l[t] *= a;
+                for (int i = 0; i < E; ++i) x[i] = sees >> i & 1 ? z[i] * g[i] : -__builtin_inff();
+                shrink(far_exponents<P>(x, ev, far, m));
+            }
 #pragma unroll
-                    for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
-                };
-                if (!is_far[t]) {
-                    float top = y[0];
+            for (int i = 0; i < E; ++i) {
+                pe[i] = __builtin_amdgcn_exp2f(x[i]);
+                // A scale that is not finite makes the whole row NaN, by w or by its parts.
+                w[i] = pe[i] * bits_f32(i & 1 ? own.v[i / 2] & 0xffff0000u : own.v[i / 2] << 16);
+            }
+            if (cut) {
 #pragma unroll
-                    for (int i = 1; i < E; ++i) top = __builtin_fmaxf(top, y[i]);
-                    top = column_max(copies_max<P>(top));
-                    if (__ballot(top > m[t]) != 0) {
-                        const float risen = __builtin_fmaxf(m[t], top);
-                        is_far[t] = beyond_near(risen);
-                        if (!is_far[t]) {
-                            const float a = rescale(m[t], risen);
-                            m[t] = risen;
-                            shrink(a);
-                        }
-                    }
-                    const float base = m[t] == -__builtin_inff() ? 0.0f : m[t] - kTarget;
+                for (int i = 0; i < E; ++i)
+                    if (!(sees >> i & 1)) pe[i] = w[i] = 0.0f;
+            }
 #pragma unroll
-                    for (int i = 0; i < E; ++i) x[i] = __builtin_fmaf(z[i], g[i], -base);
-                }
-                if (is_far[t]) {
+            for (int i = 0; i < E; ++i) l += pe[i];
+            std::uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
-                    for (int i = 0; i < E; ++i) x[i] = sees >> i & 1 ? z[i] * g[i] : -__builtin_inff();
-                    shrink(far_exponents<P>(x, ev, far[t], m[t]));
-                }
+            for (int i = 0; i < E / 2; ++i) split2(w[2 * i], w[2 * i + 1], hi[i], lo[i]);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    pe[i] = __builtin_amdgcn_exp2f(x[i]);
-                    // A scale that is not finite makes the whole row NaN, by w or by its parts.
-                    w[i] = pe[i] * bits_f32(i & 1 ? own.v[i / 2] & 0xffff0000u : own.v[i / 2] << 16);
-                }
-                if (cut) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        if (!(sees >> i & 1)) pe[i] = w[i] = 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < E; ++i) l[t] += pe[i];
-                std::uint32_t hi[E / 2], lo[E / 2];
-#pragma unroll
-                for (int i = 0; i < E / 2; ++i) split2(w[2 * i], w[2 * i + 1], hi[i], lo[i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    ph[t].v[e] = from_copy<P>(hi, e);
-                    pl[t].v[e] = from_copy<P>(lo, e);
-                }
+            for (int e = 0; e < 4; ++e) {
+                ph.v[e] = from_copy<P>(hi, e);
+                pl.v[e] = from_copy<P>(lo, e);
             }
 #pragma unroll
             for (int i = 0; i < kVWords; ++i) {
@@ -627,12 +615,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f[0].v[e] = fp4_f16<At>(even[i][e]), f[1].v[e] = fp4_f16<At>(odd[i][e]);
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            f32x4 &sum = o[t][8 * i + 2 * At + j];
-                            sum = mfma_f16(f[j], ph[t], mfma_f16(f[j], pl[t], sum));
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        f32x4 &sum = o[8 * i + 2 * At + j];
+                        sum = mfma_f16(f[j], ph, mfma_f16(f[j], pl, sum));
+                    }
                 };
                 byte(std::integral_constant<int, 0>{});
                 byte(std::integral_constant<int, 1>{});
@@ -649,8 +635,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
             load_keys(first);
             load_values(first);
             scales = load_scales(first);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) row_factor[t] = query_operands<T, DC>(raw[t], q[t]);
+            row_factor = query_operands<T, DC>(raw, q);
             for (; turn < end; turn += kAttendWaves) {
                 const int next = turn + kAttendWaves < end ? turn + kAttendWaves : turn;
                 work(turn, next);
@@ -658,19 +643,16 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
         }
 
         // The waves' sums, in LDS; then all onto the largest maximum.
+        // A row that sees no token is 0 / 1; one whose scores are all -inf is 0 / 0.
+        const float sum = column_sum(copies_sum<P>(l));
+        if (c < kRows) {
+            if (kq == 0) sm_m[wave][c] = m, sm_far[wave][c] = far, sm_l[wave][c] = n_t == 0 ? 1.0f : sum;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            // A row that sees no token is 0 / 1; one whose scores are all -inf is 0 / 0.
-            const float sum = column_sum(copies_sum<P>(l[t]));
-            if (c < kCols) {
-                if (kq == 0) sm_m[wave][16 * t + c] = m[t], sm_far[wave][16 * t + c] = far[t], sm_l[wave][16 * t + c] = n_t[t] == 0 ? 1.0f : sum;
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int j = 0; j < kDTiles; j += 4)
-                        *reinterpret_cast<f32x4 *>(&sm_o[wave][(16 * t + c) * kLd + (4 * kq + r) * kDTiles + j]) =
-                            f32x4{o[t][j][r], o[t][j + 1][r], o[t][j + 2][r], o[t][j + 3][r]};
-            }
+                for (int j = 0; j < kDTiles; j += 4)
+                    *reinterpret_cast<f32x4 *>(&sm_o[wave][c * kLd + (4 * kq + r) * kDTiles + j]) =
+                        f32x4{o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]};
         }
         __syncthreads();
         // A thread keeps one component quad of every 4 * 64 / (PD / 4)-th row.
@@ -1149,16 +1131,16 @@ template <class K> hipError_t launch_kv4_grid(K kernel, const Kv4AttendProblem &
     return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(groups), dim3(threads), args, 0, stream);
 }
 
-template <class T, int DC, bool Full, int MT, int P> hipError_t launch_kv4_few(const Kv4AttendProblem &p, hipStream_t stream)
+template <class T, int DC, bool Full, int P> hipError_t launch_kv4_few(const Kv4AttendProblem &p, hipStream_t stream)
 {
-    constexpr int kRows = 16 * MT / P;
+    constexpr int kRows = 16 / P;
     const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads;
     if (p.plan.slots == 0) {
         std::int64_t seqs = (std::int64_t(1) << 22) / per_seq;
         seqs = seqs < 1 ? 1 : seqs < p.b.seqs ? seqs : p.b.seqs;
-        return launch_kv4_grid(&kv4_few_kernel<T, DC, Full, MT, P>, p, unsigned(per_seq * seqs), 64 * kAttendWaves, stream);
+        return launch_kv4_grid(&kv4_few_kernel<T, DC, Full, P>, p, unsigned(per_seq * seqs), 64 * kAttendWaves, stream);
     }
-    const hipError_t e = launch_kv4_grid(&kv4_few_kernel<T, DC, Full, MT, P>, p, unsigned(per_seq * p.plan.slots), 64 * kAttendWaves, stream);
+    const hipError_t e = launch_kv4_grid(&kv4_few_kernel<T, DC, Full, P>, p, unsigned(per_seq * p.plan.slots), 64 * kAttendWaves, stream);
     if (e != hipSuccess) return e;
     if (p.plan.slots > 8 * p.b.seqs) return launch_kv4_grid(&kv4_join_kernel<kRows, 4>, p, unsigned(per_seq * p.b.seqs * kRows), 256, stream);
     return launch_kv4_grid(&kv4_join_kernel<kRows, 1>, p, unsigned(per_seq * p.b.seqs * (kRows / 4)), 256, stream);
@@ -1166,17 +1148,16 @@ template <class T, int DC, bool Full, int MT, int P> hipError_t launch_kv4_few(c
 
 template <class T, int DC, bool Full> hipError_t launch_kv4_shape(const Kv4AttendProblem &p, hipStream_t stream)
 {
-    constexpr int kMost = DC > 4 ? 1 : 2;  // plan_kv4_attend gives no more
     if (p.plan.rows) {
         const std::int64_t per_seq = std::int64_t(p.plan.tiles) * p.c.heads;
         std::int64_t seqs = (std::int64_t(1) << 22) / per_seq;
         seqs = seqs < 1 ? 1 : seqs < p.b.seqs ? seqs : p.b.seqs;
-        return launch_kv4_grid(&kv4_rows_kernel<T, DC, Full, kMost>, p, unsigned(per_seq * seqs), 64 * kAttendWaves, stream);
+        constexpr int kGroups = DC > 4 ? 1 : 2;  // of 16 rows a wave, as plan_kv4_attend has it
+        return launch_kv4_grid(&kv4_rows_kernel<T, DC, Full, kGroups>, p, unsigned(per_seq * seqs), 64 * kAttendWaves, stream);
     }
-    if (p.plan.mt > 1) return launch_kv4_few<T, DC, Full, kMost, 1>(p, stream);
-    return p.plan.copies == 4   ? launch_kv4_few<T, DC, Full, 1, 4>(p, stream)
-           : p.plan.copies == 2 ? launch_kv4_few<T, DC, Full, 1, 2>(p, stream)
-                                : launch_kv4_few<T, DC, Full, 1, 1>(p, stream);
+    return p.plan.copies == 4   ? launch_kv4_few<T, DC, Full, 4>(p, stream)
+           : p.plan.copies == 2 ? launch_kv4_few<T, DC, Full, 2>(p, stream)
+                                : launch_kv4_few<T, DC, Full, 1>(p, stream);
 }
 
 template <class T> hipError_t launch_kv4(const Kv4AttendProblem &p, hipStream_t stream)

@@ -11,8 +11,8 @@ namespace sgemm_impl {
 // the host knows, so that the workspace's size needs no device.
 struct Kv4Plan {
     int rows;    // 1: a work-group's waves take row tiles of their own; 0: the tokens of one row tile
-    int mt;      // groups of 16 rows a wave holds
-    int copies;  // mt == 1: how often the 16 columns of a group hold each row (4, 2 or 1)
+    int mt;      // groups of 16 rows a wave holds (one but for row tiles of its own)
+    int copies;  // how often the 16 columns of a group hold each row (4, 2 or 1)
     int tiles;   // row tiles (of one wave, or four when rows) per sequence and head the grid covers at once
     int slots;   // work-groups that share the tokens that a row tile of all sequences sees; 0: one for each sequence
     int parts;   // parts of sequences that they may leave in the workspace

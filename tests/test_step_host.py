@@ -129,7 +129,7 @@ def test_kv4_attend_shapes():
     # Few rows: copies in the columns of a tile, and the tokens of all sequences shared out.
     assert shape(32, 32, 1, 128)[:3] == (4, 1, 1) and shape(32, 32, 1, 128, heads_q=64)[:3] == (8, 1, 1)
     assert shape(32, 32, 1, 128, heads_q=72)[:3] == (16, 1, 1) and shape(31, 31, 1, 128, heads_q=160)[:3] == (16, 1, 2)
-    assert shape(200, 200, 1, 128, heads_q=160)[:3] == (32, 1, 1) and shape(200, 200, 1, 128, heads_q=160, dim=256)[:3] == (16, 1, 2)
+    assert shape(200, 200, 1, 128, heads_q=160)[:3] == (16, 1, 2) and shape(200, 200, 1, 128, heads_q=160, dim=256)[:3] == (16, 1, 2)
     assert shape(32, 32, 1, 128)[3] == 96 and shape(32, 32, 1, 128, dim=256)[3] == 64
     assert shape(1000, 1000, 1, 128)[3] == 0 and shape(1025, 1025, 1, 128, heads=1, heads_q=4)[3] == 0   # sequences enough
     assert shape(1, 1, 1, 1)[3] == 0 and shape(1, 1, 1, 128, window=64)[3] == 0                         # few tokens to see
