@@ -5,7 +5,15 @@
 // new token changes nothing that the cache holds, no row waits for another,
 // and nothing is atomic: a row of a head is a unit of its own, taken by as
 // many lanes as it has pieces of eight elements (rounded up to a power of
-// two), whose maximum goes round by lane exchanges.
+// two), whose maximum goes round by lane exchanges. A thread has four units in
+// flight: with two or eight, or 512 or 1024 threads, nothing was gained.
+//
+// 4 prompts of up to 4096 tokens, 8 heads of 128 in bf16: write 17.8 us for 61 MB
+// (3.4 TB/s), of which its vector instructions take a third, read 16.0 for 64 MB
+// (4.0); 64 sequences of one token: write 4.4 us, three round trips, and 128
+// tokens of each read into float32 17.5 for 76 MB (4.3). Loads and stores of a
+// row wait for its page, and that for the sequence: more units in flight did not
+// help, so what is left is the memory's turn from reading to writing.
 //
 // x / scale is needed to the last bit next to the midpoints of e2m1. The
 // quotient is formed as y = x r with r = 1 / scale, and corrected once by its

@@ -360,11 +360,12 @@ __device__ inline Kv4Shares kv4_shares(const Kv4AttendProblem &p, const Kv4Group
 // that may not be read are replaced by page 0 and their scores by NaN.
 //
 // 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 query heads each
-// (0.21 GB): 45.6 us, 4.6 TB/s, and 4.9 for the join; with equal splits of each
+// (0.21 GB): 45.9 us, 4.6 TB/s, and 4.7 for the join; with equal splits of each
 // sequence instead of equal shares, and no copies, 50.0 and 5.0. Bound by
 // memory: the loads alone take 42.
 template <class T, int DC, bool Full, int P>
-__global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4AttendProblem p)
+__global__ __launch_bounds__(64 * kAttendWaves, DC <= (P == 1 ? 2 : 4) ? 3 : 2)  // as many a compute unit as plan_kv4_attend counts on
+void kv4_few_kernel(Kv4AttendProblem p)
 {
     constexpr int PD = 32 * DC, kRows = 16 / P, kDTiles = 2 * DC, kLd = PD + 4, kVWords = (DC + 3) / 4, E = 8 / P;
     __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows], sm_far[kAttendWaves][kRows];
@@ -751,8 +752,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_few_kernel(Kv4Attend
 // Adds the sums that several work-groups left of one sequence's tile of rows, as
 // the work-group that did the first part says: W waves for each row, which take the
 // parts in turn. One does while sequences have few parts on average (1820 rows of
-// 4 parts: 4.8 us, with four waves a row 8.5); with more of them four wait for a
-// quarter each.
+// 4 parts: with four waves a row 8.5 us instead of 4.8); with more of them four
+// wait for a quarter each. Those 1820 rows now take 4.0, most of it the launch
+// and two round trips.
 template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendProblem p)
 {
     constexpr int kAtOnce = 4, kRowsHere = kAttendWaves / W;
@@ -845,8 +847,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
     unsigned id = blockIdx.x;
     // Later tiles see more tokens. Where a sequence's and head's work-groups are
     // the second ones that come to the compute units, they go the other way, so
-    // that each unit gets a long one and a short one (1 prompt of 2048 behind
-    // 3072: 236 us against 264, 2 of 1024 behind 4096 207 against 214).
+    // that each unit gets a long one and a short one (1 prompt of 2048
+    // rows of 5120 tokens: 236 us against 264, 2 of 1024 behind 4096 207 against 214).
     const unsigned tiles = unsigned(p.plan.tiles), number = id % tiles;
     const bool back = (id - number) / unsigned(p.plan.cus) & 1;
     const int tile0 = int(back ? tiles - 1 - number : number);

@@ -7,6 +7,10 @@
 // below 2^-28 and 2^-32) and a float32 argument costs at most 2^-25. All heads
 // of a row turn by the same angles: a work-group forms those of its rows once,
 // in LDS, and then walks over the rows' heads in pieces of eight pairs.
+//
+// Bound by memory: 4 prompts of up to 4096 rows, 32 and 8 heads of 128 in bf16
+// (240 MB), take 48 us, 5.0 TB/s, where nothing of them is in the caches, and 40
+// by themselves; 2 of up to 1021 rows of 96 components, float32 to bf16 (42 MB), 10.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -28,7 +28,7 @@ struct Kv4AttendProblem {
     sgemm_kv8_batch b;
     const void *Q;
     float *O;
-    float *ws;  // splits > 1
+    float *ws;  // plan.slots > 0
     std::int64_t ldq, hsq, ldo, hso;
     int heads_q;
     float scale;

@@ -835,7 +835,7 @@ typedef struct sgemm_kv_step {
  * negative), block (SGEMM_ERR_CACHE: not a power of two from 16 to 1024), NULL
  * pointers (of arrays that have elements), overlap of an output with another
  * array (but taken_after with taken). seqs == 0 still writes starts[0] and
- * *taken_after. One kernel is enqueued, two for more than 16384 rows.
+ * *taken_after. One kernel is enqueued, two for more than 8192 rows.
  */
 int sgemm_kv_tables(const sgemm_kv_step *step, void *stream);
 

@@ -74,6 +74,13 @@ def test_prompts(lens, new):
     check(lens, new, 16, 2500, pool[:700], taken=50, what="a pool that is too small")
 
 
+@pytest.mark.parametrize("lens,new", [([8192], [8192]), ([8191, 1], [8191, 1]), ([8192, 5000], [8192, 1]), ([4096, 4099], [4096, 4095])])
+def test_prompts_of_either_way(lens, new):
+    # Rows up to where one work-group places them all, and the next one.
+    print(f"[tables] {lens} {new}", flush=True)
+    check(lens, new, 32, -(-max(lens) // 32), np.random.default_rng(2).permutation(1000), taken=3, behind=2)
+
+
 def test_what_does_not_fit():
     # Pools that end before, between and after the call's pages, counters outside of them, tables without columns.
     lens, new, pool = [100, 37, 64, 5], [100, 1, 20, 5], np.arange(40, 60)
