@@ -9,8 +9,8 @@
 // flight: with two or eight, or 512 or 1024 threads, nothing was gained.
 //
 // 4 prompts of up to 4096 tokens, 8 heads of 128 in bf16: write 17.8 us for 61 MB
-// (3.4 TB/s), of which its vector instructions take a third, read 16.0 for 64 MB
-// (4.0); 64 sequences of one token: write 4.4 us, three round trips, and 128
+// (3.4 TB/s), of which its vector instructions take a third, read 13.3 for 64 MB
+// (4.8; 16.0 with outputs through the caches); 64 sequences of one token: write 4.4 us, three round trips, and 128
 // tokens of each read into float32 17.5 for 76 MB (4.3). Loads and stores of a
 // row wait for its page, and that for the sequence: more units in flight did not
 // help, so what is left is the memory's turn from reading to writing.
@@ -239,7 +239,11 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
     });
 }
 
-template <class T> __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4Problem p, Lay l)
+// Stream: outputs of 16 bits that are kept out of the caches. (Such a store has to
+// cover whole lines. A float32 lane's 32 bytes are two stores, 17.9 -> 27.2 us for
+// 64 sequences' 128 tokens; with the lanes' halves passed round, so that they do,
+// nothing was gained.)
+template <class T, bool Stream> __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4Problem p, Lay l)
 {
     typedef typename T::elem elem;
     const int dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block)), mask = p.c.block - 1;
@@ -274,7 +278,8 @@ template <class T> __global__ __launch_bounds__(kThreads) void kv4_read_kernel(K
             from_codes(v[i], x);
             Eight<T> out;
             rounded<T>(x, s, out);
-            __builtin_memcpy(dst + r * ld, &out, sizeof(out));
+            if constexpr (Stream) stream_store(dst + r * ld, __builtin_bit_cast(u32x4, out));
+            else __builtin_memcpy(dst + r * ld, &out, sizeof(out));
         }
     });
 }
@@ -297,7 +302,8 @@ hipError_t launch_kv4_write(const Kv4Problem &p, hipStream_t stream)
 
 hipError_t launch_kv4_read(const Kv4Problem &p, hipStream_t stream)
 {
-    return launch(p, &kv4_read_kernel<F32>, &kv4_read_kernel<BF16>, &kv4_read_kernel<F16>, stream);
+    if (p.stream()) return launch(p, &kv4_read_kernel<F32, false>, &kv4_read_kernel<BF16, true>, &kv4_read_kernel<F16, true>, stream);
+    return launch(p, &kv4_read_kernel<F32, false>, &kv4_read_kernel<BF16, false>, &kv4_read_kernel<F16, false>, stream);
 }
 
 }  // namespace sgemm_impl

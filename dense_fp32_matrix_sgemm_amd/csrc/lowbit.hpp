@@ -139,6 +139,11 @@ template <class V> __device__ inline V load_any(const void *p)
     return v;
 }
 
+// Eight 16-bit elements that are not to stay in the caches.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+__device__ inline u32x4 stream_load(const void *p) { return __builtin_nontemporal_load(static_cast<const u32x4_any *>(p)); }
+__device__ inline void stream_store(void *p, u32x4 v) { __builtin_nontemporal_store(v, static_cast<u32x4_any *>(p)); }
+
 // The upper halves of two float32, as a pair of bf16 (a in the low half):
 // truncation, so exact when the lower halves are zero.
 __device__ inline std::uint32_t pack_hi(float a, float b) { return __builtin_amdgcn_perm(f32_bits(b), f32_bits(a), 0x07060302u); }

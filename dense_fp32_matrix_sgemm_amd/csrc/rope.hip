@@ -9,8 +9,8 @@
 // in LDS, and then walks over the rows' heads in pieces of eight pairs.
 //
 // Bound by memory: 4 prompts of up to 4096 rows, 32 and 8 heads of 128 in bf16
-// (240 MB), take 48 us, 5.0 TB/s, where nothing of them is in the caches, and 40
-// by themselves; 2 of up to 1021 rows of 96 components, float32 to bf16 (42 MB), 10.
+// (240 MB), take 49 us in a graph, 4.9 TB/s, with inputs and outputs kept out of
+// the caches, 53 without; 2 of up to 1021 rows of 96 components, float32 to bf16 (42 MB), 10.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -45,8 +45,9 @@ template <class T, int N> struct Elems {
     typename T::elem x[N];
 };
 
-// Pairs held apart (i and i + rot / 2) or side by side.
-template <class T, class U, bool Side> __global__ __launch_bounds__(kThreads) void rope_kernel(RopeProblem p, int rows_at_once)
+// Side: pairs side by side, not apart (i and i + rot / 2). Stream: outputs of 16
+// bits, pairs apart, that are kept out of the caches.
+template <class T, class U, bool Side, bool Stream> __global__ __launch_bounds__(kThreads) void rope_kernel(RopeProblem p, int rows_at_once)
 {
     typedef typename T::elem in;
     typedef typename U::elem out;
@@ -90,26 +91,36 @@ template <class T, class U, bool Side> __global__ __launch_bounds__(kThreads) vo
                 if (Side) {
                     v = load_any<Elems<T, 16>>(x + 2 * i0);
                 } else {
-                    const Elems<T, 8> a = load_any<Elems<T, 8>>(x + i0), b = load_any<Elems<T, 8>>(x + pairs + i0);
+                    Elems<T, 8> a, b;
+                    if constexpr (Stream && sizeof(in) == 2) {
+                        a = __builtin_bit_cast(Elems<T, 8>, stream_load(x + i0)), b = __builtin_bit_cast(Elems<T, 8>, stream_load(x + pairs + i0));
+                    } else {
+                        a = load_any<Elems<T, 8>>(x + i0), b = load_any<Elems<T, 8>>(x + pairs + i0);
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v.x[2 * j] = a.x[j], v.x[2 * j + 1] = b.x[j];
                 }
-                out a[8], b[8];
+                Elems<U, 8> a, b;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float xa = to_f32<T>(v.x[2 * j]), xb = to_f32<T>(v.x[2 * j + 1]);
                     const Turn u = t[j];
-                    a[j] = from_f32<U>(__builtin_fmaf(xa, u.c, -(xb * u.s)));
-                    b[j] = from_f32<U>(__builtin_fmaf(xb, u.c, xa * u.s));
+                    a.x[j] = from_f32<U>(__builtin_fmaf(xa, u.c, -(xb * u.s)));
+                    b.x[j] = from_f32<U>(__builtin_fmaf(xb, u.c, xa * u.s));
                 }
                 if (Side) {
                     Elems<U, 16> w;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w.x[2 * j] = a[j], w.x[2 * j + 1] = b[j];
+                    for (int j = 0; j < 8; ++j) w.x[2 * j] = a.x[j], w.x[2 * j + 1] = b.x[j];
                     __builtin_memcpy(y + 2 * i0, &w, sizeof(w));
                 } else {
-                    __builtin_memcpy(y + i0, a, sizeof(a));
-                    __builtin_memcpy(y + pairs + i0, b, sizeof(b));
+                    if constexpr (Stream) {
+                        stream_store(y + i0, __builtin_bit_cast(u32x4, a));
+                        stream_store(y + pairs + i0, __builtin_bit_cast(u32x4, b));
+                    } else {
+                        __builtin_memcpy(y + i0, &a, sizeof(a));
+                        __builtin_memcpy(y + pairs + i0, &b, sizeof(b));
+                    }
                 }
             } else {
                 for (int j = 0; j < n; ++j) {
@@ -123,24 +134,29 @@ template <class T, class U, bool Side> __global__ __launch_bounds__(kThreads) vo
     }
 }
 
-template <class T, class U> const void *rope_kernel_of(bool side)
+template <class T, class U> const void *rope_kernel_of(bool side, bool stream)
 {
-    return side ? reinterpret_cast<const void *>(&rope_kernel<T, U, true>) : reinterpret_cast<const void *>(&rope_kernel<T, U, false>);
+    if (side) return reinterpret_cast<const void *>(&rope_kernel<T, U, true, false>);
+    if constexpr (sizeof(typename U::elem) == 2)
+        if (stream) return reinterpret_cast<const void *>(&rope_kernel<T, U, false, true>);
+    return reinterpret_cast<const void *>(&rope_kernel<T, U, false, false>);
 }
 
-template <class T> const void *rope_kernel_of(int otype, bool side)
+template <class T> const void *rope_kernel_of(int otype, bool side, bool stream)
 {
-    return otype == SGEMM_F32 ? rope_kernel_of<T, F32>(side) : otype == SGEMM_LP_BF16 ? rope_kernel_of<T, BF16>(side) : rope_kernel_of<T, F16>(side);
+    return otype == SGEMM_F32       ? rope_kernel_of<T, F32>(side, stream)
+           : otype == SGEMM_LP_BF16 ? rope_kernel_of<T, BF16>(side, stream)
+                                    : rope_kernel_of<T, F16>(side, stream);
 }
 
 }  // namespace
 
 hipError_t launch_rope(const RopeProblem &p, int cus, hipStream_t stream)
 {
-    const bool side = p.interleaved != 0;
-    const void *kernel = p.dtype == SGEMM_F32       ? rope_kernel_of<F32>(p.otype, side)
-                         : p.dtype == SGEMM_LP_BF16 ? rope_kernel_of<BF16>(p.otype, side)
-                                                    : rope_kernel_of<F16>(p.otype, side);
+    const bool side = p.interleaved != 0, large = p.stream();
+    const void *kernel = p.dtype == SGEMM_F32       ? rope_kernel_of<F32>(p.otype, side, large)
+                         : p.dtype == SGEMM_LP_BF16 ? rope_kernel_of<BF16>(p.otype, side, large)
+                                                    : rope_kernel_of<F16>(p.otype, side, large);
     // As many rows as give each thread an angle, but no more than leave every
     // compute unit a few work-groups.
     int rows_at_once = p.rot / 2 > 0 ? kThreads / (p.rot / 2) : 16;

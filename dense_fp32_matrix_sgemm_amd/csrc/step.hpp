@@ -19,6 +19,7 @@ struct Kv4Problem {
     void *K, *V;
     std::int64_t ldk, hsk, ldv, hsv;
     int dtype;
+    bool stream() const { return std::int64_t(b.rows) * c.heads * c.dim * 2 >= kStreamBytes; }  // 16-bit K, or V
 };
 hipError_t launch_kv4_write(const Kv4Problem &p, hipStream_t stream);
 hipError_t launch_kv4_read(const Kv4Problem &p, hipStream_t stream);
@@ -46,6 +47,7 @@ struct RopeProblem {
     sgemm_rope_rows x[2];  // x[1].heads == 0: one operand
     int dtype, otype, rows, dim, rot, interleaved, inverse;
     float amplitude;
+    bool stream() const { return std::int64_t(rows) * (x[0].heads + x[1].heads) * dim * 2 >= kStreamBytes; }  // 16-bit outputs
 };
 hipError_t launch_rope(const RopeProblem &p, int cus, hipStream_t stream);
 

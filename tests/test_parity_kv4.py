@@ -518,3 +518,24 @@ def test_many_sequences_share_their_tokens(heads, ratio, dim):
         attends(case, ratio, "bf16", max_new=max_new, what=f"max_new {max_new}")
         attends(case, ratio, "f32", max_new=max_new, window=900, what=f"window, max_new {max_new}")
     attends(case, ratio, "f16", causal=False, max_new=9, what="not causal")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim,layout", [(128, "packed"), (48, "padded"), (80, "heads")])
+def test_reading_back_more_than_the_caches_hold(dim, layout, dtype):
+    print(f"[kv4] large read dim={dim} {layout} {dtype}", flush=True)
+    lens = [5000, 3001, 17, 2500]
+    case = Case4(81, lens, [4990, 3001, 0, 2499], 6, 16, dim, before=2, behind=3)
+    assert case.rows * 6 * dim * 2 >= 4 << 20 or dim == 48
+    cache, args = case.device(), case.args()
+    outs = [views(torch.full((case.rows, 6, dim), 3.25).to(TYPES[dtype]), layout) for _ in range(2)]
+    if layout != "packed":  # rows that begin at an odd element
+        outs = [torch.full((case.rows, 7, dim + 1), 3.25, device="cuda").to(TYPES[dtype])[:, :6, 1:] for _ in range(2)]
+    sg.kv4_read(cache, *args, K=outs[0], V=outs[1])
+    for j in range(2):
+        got = outs[j].cpu().double().numpy()
+        for b in range(4):
+            n = int(case.new[b])
+            want = torch.from_numpy(case.ref.tokens(case.table, b, lens[b], j)[lens[b] - n:]).to(torch.float32).to(TYPES[dtype]).double().numpy()
+            assert np.array_equal(got[case.starts[b]:case.starts[b] + n], want), (b, j)
+        assert (got[:2] == 3.25).all() and (got[-3:] == 3.25).all()

@@ -96,6 +96,28 @@ def test_rows_and_the_place_they_go_to(rows, dtype):
     check(qkv[:, :heads], qkv[:, :0], positions.numpy(), freqs[:8].cpu().numpy(), (buf[:, :heads], buf[:, :0]), dtype)
 
 
+@pytest.mark.parametrize("dtype,otype", [("bf16", "bf16"), ("f16", "f16"), ("f32", "bf16"), ("bf16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("dim,rot", [(128, 128), (80, 48), (72, 40)])
+def test_more_rows_than_the_caches_hold(dim, rot, dtype, otype):
+    print(f"[rope] large dim={dim} rot={rot} {dtype} to {otype}", flush=True)
+    rows = 4099
+    Q, K = operands(dim, rows, 6, 3, dim, dtype)
+    positions = torch.randint(0, 100000, (rows,), generator=torch.Generator().manual_seed(dim), dtype=torch.int32)
+    freqs, _ = sg.rope_frequencies(rot)
+    got = sg.rope(Q.cuda(), K.cuda(), positions.cuda(), freqs, dtype=TYPES[otype])
+    check(Q, K, positions.numpy(), freqs.cpu().numpy(), got, otype)
+    # Rows that begin at an odd element, and in place.
+    wide = [torch.full((rows, t.shape[1] + 1, dim + 1), 3.25, device="cuda").to(TYPES[otype]) for t in (Q, K)]
+    outs = [w[:, :-1, 1:] for w in wide]
+    sg.rope(Q.cuda(), K.cuda(), positions.cuda(), freqs, out=outs)
+    assert all(torch.equal(a, b) for a, b in zip(outs, got))
+    assert all((w[:, -1] == 3.25).all() and (w[..., 0] == 3.25).all() for w in wide)
+    if dtype == otype:
+        q, k = Q.cuda(), K.cuda()
+        sg.rope(q, k, positions.cuda(), freqs, out=(q, k))
+        assert torch.equal(q, got[0]) and torch.equal(k, got[1])
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_positions_from_end_to_end(interleaved):
     # Angles of every quadrant and next to its borders, far positions, negative ones.
