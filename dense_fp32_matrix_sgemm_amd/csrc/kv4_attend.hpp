@@ -359,10 +359,15 @@ __device__ inline Kv4Shares kv4_shares(const Kv4AttendProblem &p, const Kv4Group
 // is loaded is looked at before its turn, so that no wait comes early. Pages
 // that may not be read are replaced by page 0 and their scores by NaN.
 //
+// Where a sequence's keys are read by one tile only and one load of a wave
+// covers whole lines (64 and 128 components), they are kept out of the caches:
+// 50.3 us instead of 55.4 in a graph for the batch below, 50.7 instead of 51.7
+// with 64 components. Values, whose lines take several loads, lost by it (51.7
+// with both), and so did keys of 80 components (34.8 -> 36.1), 192 and 256.
+//
 // 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 query heads each
-// (0.21 GB): 45.9 us, 4.6 TB/s, and 4.7 for the join; with equal splits of each
-// sequence instead of equal shares, and no copies, 50.0 and 5.0. Bound by
-// memory: the loads alone take 42.
+// (0.21 GB): 42.6 us, 5.0 TB/s, and 4.7 for the join; with equal splits of each
+// sequence instead of equal shares, and no copies, 10% more. Bound by memory.
 template <class T, int DC, bool Full, int P>
 __global__ __launch_bounds__(64 * kAttendWaves, DC <= (P == 1 ? 2 : 4) ? 3 : 2)  // as many a compute unit as plan_kv4_attend counts on
 void kv4_few_kernel(Kv4AttendProblem p)
@@ -453,7 +458,11 @@ void kv4_few_kernel(Kv4AttendProblem p)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const std::uint8_t *const at = codes_k + w.token[x] * (dim / 2);
-                if (Full) {
+                if constexpr (Full && P > 1 && DC <= 4) {
+                    typedef std::uint32_t words __attribute__((ext_vector_type(DC)));
+                    const words w = __builtin_nontemporal_load(reinterpret_cast<const words *>(at + k_at[0]));
+                    __builtin_memcpy(k[x], &w, sizeof(w));
+                } else if (Full) {
                     __builtin_memcpy(k[x], at + k_at[0], 4 * DC);
                 } else {
 #pragma unroll
