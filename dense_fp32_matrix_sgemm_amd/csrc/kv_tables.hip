@@ -45,18 +45,6 @@ __device__ inline i64 slot_of(i64 page, int position, int shift)
     return page < 0 ? -1 : (page << shift) + (position & ((1 << shift) - 1));
 }
 
-// The first of n ascending sums that is above x.
-template <class A> __device__ inline int above(const A *sums, int n, i64 x)
-{
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (i64(sums[mid]) > x) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
 __global__ __launch_bounds__(kThreads) void kv_tables_kernel(sgemm_kv_step t, int place_rows)
 {
     __shared__ i64 rows_to[kThreads], pages_to[kThreads], wave_rows[kWaves], wave_pages[kWaves];

@@ -2,6 +2,8 @@
 // positions, page tables (args_step.cpp). Pure C++ (no HIP header).
 #pragma once
 
+#include <cstdint>
+
 #include "lowbit_plan.hpp"
 #include "sgemm.h"
 
@@ -54,5 +56,17 @@ constexpr std::int64_t kStreamBytes = std::int64_t(4) << 20;
 // 8 prompts of up to 512, 1024 and 2048 tokens 5.4, 7.0 and 10.4 us, where the
 // second kernel makes it 7.2, 7.0 and 7.1 and a launch.
 constexpr int kTablesAlone = 8192;
+
+// The first of n ascending sums that is above x, or n.
+template <class A> constexpr int above(const A &sums, int n, std::int64_t x)
+{
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (std::int64_t(sums[mid]) > x) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
 
 }  // namespace sgemm_impl
