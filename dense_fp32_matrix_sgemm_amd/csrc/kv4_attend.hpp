@@ -749,7 +749,7 @@ void kv4_few_kernel(Kv4AttendProblem p)
             at = tile;
             tile += p.plan.tiles;
             if (at * kRows >= s.n * R) {
-                seq += step;
+                seq = next_sequence(seq, step, p.b.seqs);
                 tile = shared ? std::int64_t(tile0) + p.plan.tiles : tile0;
                 continue;
             }

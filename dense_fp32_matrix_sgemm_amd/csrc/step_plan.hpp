@@ -69,4 +69,7 @@ template <class A> constexpr int above(const A &sums, int n, std::int64_t x)
     return lo;
 }
 
+// The sequence `step` behind seq (< seqs), or seqs where there is none.
+constexpr int next_sequence(int seq, int step, int seqs) { return seq < seqs - step ? seq + step : seqs; }
+
 }  // namespace sgemm_impl

@@ -1,6 +1,7 @@
-// Which sequence a row falls to, at counts of sequences next to 2^31, for a
-// build under AddressSanitizer and UndefinedBehaviorSanitizer
-// (tests/test_step_search.py). The kernels search with the same function.
+// Which sequence a row falls to, and which a work-group takes next, at counts of
+// sequences next to 2^31, for a build under AddressSanitizer and
+// UndefinedBehaviorSanitizer (tests/test_step_search.py). The kernels walk
+// sequences with the same functions.
 #include <climits>
 #include <cstdint>
 #include <cstdio>
@@ -42,6 +43,13 @@ int main()
             if (x < 0) continue;
             expect(above(Sums{n}, n, x) == (x < n ? int(x) : n), "above", n, x, above(Sums{n}, n, x));
         }
+    for (int seqs : counts)
+        for (int step : {1, 2, 96, 4096, 1 << 22, INT_MAX})
+            for (std::int64_t seq : {std::int64_t(0), std::int64_t(seqs) - step, std::int64_t(seqs) - step - 1, std::int64_t(seqs) - 1}) {
+                if (seq < 0 || seq >= seqs) continue;
+                const std::int64_t next = seq + step;
+                expect(next_sequence(int(seq), step, seqs) == (next < seqs ? next : seqs), "next_sequence", seqs, step, seq);
+            }
     if (failures) return 1;
     std::printf("step search ok\n");
     return 0;

@@ -1,4 +1,4 @@
-"""Which sequence a row of a serving step falls to, at counts of
+"""Which sequence a row or a work-group of a serving step falls to, at counts of
 sequences next to 2^31 (no GPU needed)."""
 
 import os
