@@ -40,28 +40,51 @@ bool overlaps_kv4(Span x, const sgemm_kv4_cache *c)
     return false;
 }
 
-// Whether two rows x heads x dim operands (strides_ok) share a byte. Operands
-// of one row stride whose heads lie inside a row (parts of one buffer of
-// queries, keys and values, say) may be interleaved row by row.
+// A rows x heads x dim operand (strides_ok), in bytes.
 struct RowsOperand {
     const void *p;
     int rows, heads, dim, ld, hs, elem;
     Span span() const { return rows_span(p, rows, heads, dim, ld, hs, elem); }
-    i64 width() const { return (i64(heads - 1) * (heads > 1 ? hs : 0) + dim) * elem; }
+    i64 bytes() const { return i64(dim) * elem; }  // of a row of one head
+    i64 width() const { return heads > 1 ? i64(heads - 1) * hs * elem + bytes() : bytes(); }  // of a row
 };
 
+i64 floor_div(i64 a, i64 b) { return a / b - (a % b < 0 ? 1 : 0); }  // b > 0
+
+// Whether pieces of `a` bytes at every multiple of pitch lie apart from pieces
+// of `b` bytes at `at` and every multiple of pitch from there.
+bool apart_in(i64 pitch, i64 a, i64 b, i64 at)
+{
+    at -= floor_div(at, pitch) * pitch;
+    return at >= a && at + b <= pitch;
+}
+
+// Whether two operands of the same rows share a byte. Where the ranges that
+// they span meet and their strides are the same (of one row or one head there
+// is none), this is exact: rows and heads of the two may then be interleaved in
+// any way (queries, keys and values of each row, or of each head, in one
+// buffer). With other strides operands whose ranges meet count as sharing.
 bool share(const RowsOperand &a, const RowsOperand &b)
 {
     if (!overlap(a.span(), b.span())) return false;
-    const i64 pitch = i64(a.ld) * a.elem;
-    if (a.rows > 1 && pitch == i64(b.ld) * b.elem && a.width() <= pitch && b.width() <= pitch) {
-        // From the lower one on: a's width, then b's, within one pitch.
-        const std::uintptr_t pa = reinterpret_cast<std::uintptr_t>(a.p), pb = reinterpret_cast<std::uintptr_t>(b.p);
-        const RowsOperand &low = pa <= pb ? a : b, &high = pa <= pb ? b : a;
-        const i64 at = i64((pa <= pb ? pb - pa : pa - pb) % std::uintptr_t(pitch));
-        return !(at >= low.width() && at + high.width() <= pitch);
+    if (a.rows > 1 && i64(a.ld) * a.elem != i64(b.ld) * b.elem) return true;
+    if (a.heads > 1 && b.heads > 1 && i64(a.hs) * a.elem != i64(b.hs) * b.elem) return true;
+    const std::uintptr_t pa = reinterpret_cast<std::uintptr_t>(a.p), pb = reinterpret_cast<std::uintptr_t>(b.p);
+    if ((pa <= pb ? pb - pa : pa - pb) >> 60) return true;
+    const i64 pitch = a.rows > 1 ? i64(a.ld) * a.elem : 1, head = a.heads > 1 ? i64(a.hs) * a.elem : i64(b.hs) * b.elem;
+    const i64 apart = pa <= pb ? i64(pb - pa) : -i64(pa - pb);
+    // Side by side in each row, or in each head of each row: told without a walk over the heads.
+    if (a.rows > 1 && apart_in(pitch, a.width(), b.width(), apart)) return false;
+    if ((a.heads > 1 || b.heads > 1) && (a.rows == 1 || pitch % head == 0) && apart_in(head, a.bytes(), b.bytes(), apart)) return false;
+    // A row of b's head h + dh begins at x + dr pitch, dr rows on, where one of a's head h begins at 0.
+    for (i64 dh = 1 - a.heads; dh < b.heads; ++dh) {
+        const i64 x = apart + dh * head;
+        i64 first = -floor_div(x + b.bytes() - 1, pitch), last = floor_div(a.bytes() - 1 - x, pitch);  // of the rows that meet
+        if (first < 1 - a.rows) first = 1 - a.rows;
+        if (last > b.rows - 1) last = b.rows - 1;
+        if (first <= last) return true;
     }
-    return true;
+    return false;
 }
 
 }  // namespace

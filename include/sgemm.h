@@ -683,7 +683,8 @@ int sgemm_kv4_write(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, 
  * to dtype, into K and V (rows x heads x dim). A row whose page is not one of
  * the cache's reads NaN; a row before token 0 is left as it was. The checks of
  * sgemm_kv4_write() but for those of the cache's arrays; outputs that share
- * elements with each other or overlap the batch's arrays are refused as well. */
+ * elements with each other (as sgemm_rope_rows has it) or overlap the batch's
+ * arrays are refused as well. */
 int sgemm_kv4_read(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype,
                    void *K, int ldk, int hsk,
                    void *V, int ldv, int hsv,
@@ -745,7 +746,11 @@ int sgemm_kv4_attend_shape(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *
 
 /* Rows of `heads` heads that sgemm_rope turns: X is read and Y written, rows x
  * heads x dim with strides as for sgemm_kv8_write. Y may be X itself, with the
- * same strides and type; it must share no element with any other X or Y. */
+ * same strides and type; it must share no element with any other X or Y. Where
+ * the ranges of two operands meet they are told apart by equal strides (in
+ * bytes; one row or one head has none), as those of queries, keys and values
+ * that one buffer holds row by row or head by head; with other strides they
+ * count as sharing. */
 typedef struct sgemm_rope_rows {
     const void *X;
     void *Y;
