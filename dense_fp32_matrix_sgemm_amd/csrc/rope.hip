@@ -29,9 +29,11 @@ struct Turn {
 
 __device__ inline Turn turn_of(int position, double freq, float amplitude, bool inverse)
 {
-    const double quarters = double(position) * freq * 0.63661977236758134308;  // 2 / pi
-    const double whole = __builtin_rint(quarters);
-    const float x = float(quarters - whole) * 1.57079632679489661923f, y = x * x;
+    constexpr double kUp = 0.63661977236758134308, kLow = -3.9357353350364972e-17;  // 2 / pi
+    // Of the angle and of its product with 2 / pi what is rounded off is kept: up to 2^-24 each at 2^30 radians.
+    const double t = double(position) * freq, whole = __builtin_rint(t * kUp);
+    const double left = __builtin_fma(t, kUp, -whole) + __builtin_fma(t, kLow, __builtin_fma(double(position), freq, -t) * kUp);
+    const float x = float(left) * 1.57079632679489661923f, y = x * x;
     const float s = x * __builtin_fmaf(y, __builtin_fmaf(y, __builtin_fmaf(y, __builtin_fmaf(y, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
     const float c = __builtin_fmaf(
         y, __builtin_fmaf(y, __builtin_fmaf(y, __builtin_fmaf(y, __builtin_fmaf(y, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
