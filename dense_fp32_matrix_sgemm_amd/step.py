@@ -353,6 +353,48 @@ def _rope_rows(X, Y, dtype, name):
     return RopeRows(X.data_ptr() or None, Y.data_ptr() or None, heads, *x, *y), Y
 
 
+def _asks_gradient(x):
+    """Whether x, a tensor or a pair of tensors, requires a gradient."""
+    if isinstance(x, (tuple, list)):
+        return any(_asks_gradient(t) for t in x)
+    return getattr(x, "requires_grad", False)
+
+
+_ROPE = None
+
+
+def _rope_function():
+    """rope as a node of automatic differentiation: the gradient is turned back."""
+    global _ROPE
+    if _ROPE is None:
+        import torch
+
+        class Rope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, Q, K, positions, freqs, interleaved, amplitude, inverse, dtype):
+                ctx.save_for_backward(positions, freqs)
+                ctx.set_materialize_grads(False)
+                ctx.turn = {"interleaved": interleaved, "amplitude": amplitude, "inverse": not inverse, "dtype": Q.dtype}
+                out = rope(Q, K, positions, freqs, interleaved, amplitude, inverse, dtype)
+                if K is not None:
+                    ctx.mark_non_differentiable(*(y for y, needed in zip(out, ctx.needs_input_grad) if not needed))
+                return out
+
+            @staticmethod
+            def backward(ctx, dQ, dK=None):
+                # An expanded gradient is laid out; one without rows may be expanded and contiguous.
+                g = [None if d is None or not needed else d if d.is_contiguous() and d.stride(-1) == 1 else d.clone(memory_format=torch.contiguous_format)
+                     for d, needed in zip((dQ, dK), ctx.needs_input_grad)]
+                if g[0] is not None and g[1] is not None:
+                    g = rope(*g, *ctx.saved_tensors, **ctx.turn)
+                else:
+                    g = [None if d is None else rope(d, None, *ctx.saved_tensors, **ctx.turn) for d in g]
+                return (*g, None, None, None, None, None, None)
+
+        _ROPE = Rope
+    return _ROPE
+
+
 def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False, dtype=None, out=None):
     """Rotary positions: the pairs of components of each head of Q and K (rows
     x heads x dim: float32, bfloat16 or float16; K may be None) turned by
@@ -363,11 +405,13 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
     others are copied. Pairs are components i and i + len(freqs), or with
     ``interleaved`` 2 i and 2 i + 1. positions is an int32 tensor of the rows.
     ``inverse`` turns back, which is also the gradient's way: with dQ' the
-    gradient of what comes out, rope(dQ', ..., inverse=True) is Q's.
+    gradient of what comes out, rope(dQ', ..., inverse=True) is Q's. Where Q or
+    K require a gradient, automatic differentiation makes that call.
 
     Returns (Q', K'), or Q' alone without K, in ``dtype`` (the operands' type
     by default) or into ``out`` (likewise a pair or a tensor), which may be the
-    operands themselves.
+    operands themselves. There is no gradient through ``out``, nor with respect
+    to freqs: calls that ask for one are refused.
     """
     import torch
 
@@ -386,6 +430,10 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
         raise ValueError(f"positions must be {rows} contiguous elements (has {positions.shape[0]}), freqs contiguous")
     if 2 * pairs > dim:
         raise ValueError(f"{pairs} pairs do not fit heads of {dim} components")
+    if (Q.requires_grad or freqs.requires_grad or _asks_gradient(K) or _asks_gradient(out)) and torch.is_grad_enabled():
+        if out is not None or freqs.requires_grad:
+            raise ValueError("there is no gradient through out or with respect to freqs")
+        return _rope_function().apply(Q, K, positions, freqs, interleaved, amplitude, inverse, dtype)
     if out is None:
         outs = (None, None)
     elif K is None:
