@@ -437,13 +437,13 @@ def rope(Q, K, positions, freqs, interleaved=False, amplitude=1.0, inverse=False
     if out is None:
         outs = (None, None)
     elif K is None:
+        if not isinstance(out, torch.Tensor):
+            raise TypeError("out must be a tensor")
         outs = (out, None)
     else:
-        if not isinstance(out, (tuple, list)) or len(out) != 2:
+        if not isinstance(out, (tuple, list)) or len(out) != 2 or not all(isinstance(t, torch.Tensor) for t in out):
             raise TypeError("out must be a pair of tensors")
         outs = out
-        if outs[0] is None or outs[1] is None:
-            raise TypeError("out must be a pair of tensors")
     if dtype is None:
         dtype = Q.dtype if out is None else outs[0].dtype
     otype = code if dtype is Q.dtype else _type_code(dtype, "dtype")
