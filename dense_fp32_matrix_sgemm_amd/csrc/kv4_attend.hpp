@@ -16,23 +16,25 @@
 // * A code is always a finite number, so tokens that a row does not see need
 //   no care beyond a weight of zero.
 //
-// Codes are exact in f16, so the weights may be held in two parts of f16, 22
-// bits, where bf16 would need three for as many, and a matrix instruction of
-// four is saved. f16's range is made enough by a
-// common power of two for each row: the running maximum m is that of z +
-// exponent(V's scale) over the tokens seen, and weights are 2^(z - m + 14), so
-// that the largest product of a weight and a scale lies between 2^14 and 2^15
-// whatever the scales are (rows of scores beyond 2^14: far_exponents). The sum l counts weights of the same factor, which
-// the quotient drops. A product is held to 2^-22 of itself, or to 2^-39 of the
-// row's largest where that is more. Tokens that a row does not see take no part
-// in its maximum, so their scales do not cost it precision.
+// A weight is 2^(x - m), x the score and m a little above the row's largest so
+// far, so that the exponents of weights that count are small and float32 holds
+// them well, whatever the values' scales. Codes are exact in f16, so a weight's
+// product with its value's scale may be held in two parts of f16, 22 bits, where
+// bf16 would need three for as many, and a matrix instruction of four is saved.
+// f16's range is made enough by a power of two for each row, which the products
+// are multiplied by (unit_of). A product is held to 2^-22 of itself, or to 2^-38
+// of the row's largest where that is more. Tokens that a row does not see take
+// no part in its largest, so their scales do not cost it precision. (With the
+// exponent of a value's scale in m no factor is needed, but the exponential's
+// argument is as large as that exponent: weights at scales of 2^-80 were off by
+// 52 units of 2^-24, now by 5 at any scale.)
 //
 // While a wave feeds the matrix cores in a prompt its priority is raised: the
 // other wave of the SIMD then finds its vector instructions' turn while those
 // run.
 //
-// Both steps at 2 prompts of 1024 rows behind 4096 tokens, in f16: three parts
-// of bf16 259 us, two of f16 228, with the priority 216.
+// Both steps when they were taken, at 2 prompts of 1024 rows behind 4096 tokens, in
+// f16: three parts of bf16 259 us, two of f16 228, with the priority 216.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -84,10 +86,12 @@ template <> struct QOperand4<F32> {
     }
 };
 
-// Two float32 as two parts of f16, hi + lo, each rounded to nearest: 22 bits
-// and the sign, or down to 2^-24 for what lies below f16's normal numbers.
-__device__ inline void split2(float a, float b, std::uint32_t &hi, std::uint32_t &lo)
+// Two float32 times a power of two as two parts of f16, hi + lo, each rounded to
+// nearest: 22 bits and the sign, or down to 2^-24 for what lies below f16's normal
+// numbers.
+__device__ inline void split2(float a, float b, float power, std::uint32_t &hi, std::uint32_t &lo)
 {
+    a *= power, b *= power;
     hi = __builtin_bit_cast(std::uint32_t, f16x2{_Float16(a), _Float16(b)});
     float ra, rb;  // a - hi, b - hi: exact
     asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(ra) : "v"(hi), "v"(a));
@@ -137,7 +141,7 @@ template <class T, int DC> __device__ inline float query_operands(const QueryPie
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 std::uint32_t hi, lo;
-                split2(raw.r[i].x[2 * j] * up, raw.r[i].x[2 * j + 1] * up, hi, lo);
+                split2(raw.r[i].x[2 * j], raw.r[i].x[2 * j + 1], up, hi, lo);
                 q[i].hi.v[j] = hi;
                 q[i].lo.v[j] = lo;
             }
@@ -149,19 +153,6 @@ template <class T, int DC> __device__ inline float query_operands(const QueryPie
 __device__ inline float scale_of(u32x2 s, int r)
 {
     return bits_f32(r & 1 ? s[r / 2] & 0xffff0000u : s[r / 2] << 16);
-}
-
-// The exponents of the sizes of two scales (the lower half's and the upper
-// one's), in float32 and 127 too large. Scales below 2^-90 (and zeros) count as
-// 2^-90, so that a weight that such a scale is to bring back into range does
-// not overflow.
-__device__ inline void exponents_of(std::uint32_t s, float &lower, float &upper)
-{
-    typedef __attribute__((ext_vector_type(2))) std::uint16_t u16x2;
-    const u16x2 v = __builtin_elementwise_max(__builtin_bit_cast(u16x2, s << 1), u16x2{(127 - 90) << 8, (127 - 90) << 8});
-    const std::uint32_t u = __builtin_bit_cast(std::uint32_t, v);
-    lower = float((u >> 8) & 0xffu);
-    upper = float(u >> 24);
 }
 
 // The largest (sum) of a value over the P copies of a column's row.
@@ -183,48 +174,36 @@ template <int P> __device__ inline float copies_sum(float x)
     return x;
 }
 
-// What a row's weights are relative to: a token's weight is held as
-// 2^(x - far - m + kTarget), m being the largest x - far + ev over the tokens
-// seen, x a score and ev the exponent of its value's scale. `far` is 0 while m
-// lies within 2^14 of 0, and the score of the largest weight beyond, where m
-// would be rounded by more than 2^-10: differences of scores are formed before
-// an exponent is added to them, so that equal scores have equal weights however
-// large they are, and none leaves f16's range by a rounding.
-constexpr float kTarget = 127.0f + 14.0f;  // 127: the offset of exponents_of
-__device__ inline bool beyond_near(float m) { return __ballot(__builtin_fabsf(m) >= 16384.0f && m != -__builtin_inff()) != 0; }
+// How far above a row's largest score m is put when that rises beyond m, so that
+// it seldom does again. Weights are then at most 1 and that of the largest score at
+// least 2^-4, whose exponent float32 holds to 2^-23. Together with products that may
+// grow to twice what their unit was made for: 2 prompts of 1024 behind 4096 206 us,
+// with neither 219 to 229.
+constexpr float kAbove = 4.0f;
 
-// What is left of a row's sums where m is raised to `risen` and far moved to `to`.
-__device__ inline float rescale_far(float far, float m, float to, float risen) { return rescale(far - to + m, risen); }
-
-// The larger of two such places, for sums that are to be joined.
-__device__ inline void raise(float &far, float &m, float far2, float m2)
+// What a row's products of a weight and a scale are multiplied by, as the
+// exponent of a power of two, given the largest of them: it comes to lie between
+// 2^13 and 2^14, and has not to rise beyond 2^15. (Products below 2^-100 count as
+// that. One that is not finite makes its row NaN in any case.)
+__device__ inline int unit_of(float top)
 {
-    if (m2 == -__builtin_inff()) return;
-    const float to = m == -__builtin_inff() ? far2 : __builtin_fmaxf(far, far2);
-    m = __builtin_fmaxf(far - to + m, far2 - to + m2);
-    far = to;
+    const int e = int(f32_bits(top) >> 23);
+    return 127 + 13 - (e < 27 ? 27 : e);
 }
+__device__ inline float power(int e) { return bits_f32(std::uint32_t(127 + e) << 23); }  // 2^e, |e| < 127
 
-// N scores (-inf where a row does not see the token) and exponents of far rows:
-// raises far and m, turns each score into its weight's exponent, and returns
-// what is left of the sums.
-template <int P, int N> __device__ inline float far_exponents(float (&x)[N], const float (&ev)[N], float &far, float &m)
+// What sums of products that have the unit of largest product `from` are multiplied
+// by to have that of `to` (at least a * from), where a larger m makes them a times as
+// large: at most 2. One power of two, as of two factors one may overflow.
+__device__ inline float to_unit(float a, float from, float to) { return __builtin_ldexpf(a, unit_of(to) - unit_of(from)); }
+
+// Sums of products with the unit of largest product `top`, without it.
+__device__ inline f32x4 in_values(f32x4 x, float top)
 {
-    float score = x[0], top = -__builtin_inff();
+    const int e = -unit_of(top);
 #pragma unroll
-    for (int i = 1; i < N; ++i) score = __builtin_fmaxf(score, x[i]);
-    score = column_max(copies_max<P>(score));
-    // A row that has seen nothing stands nowhere yet.
-    const float to = m == -__builtin_inff() ? (score == -__builtin_inff() ? far : score) : __builtin_fmaxf(far, score);
-#pragma unroll
-    for (int i = 0; i < N; ++i) top = __builtin_fmaxf(top, x[i] - to + ev[i]);
-    const float risen = __builtin_fmaxf(far - to + m, column_max(copies_max<P>(top)));
-    const float a = rescale_far(far, m, to, risen), base = risen == -__builtin_inff() ? 0.0f : risen - kTarget;
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] - to - base;
-    far = to;
-    m = risen;
-    return a;
+    for (int j = 0; j < 4; ++j) x[j] = __builtin_ldexpf(x[j], e);
+    return x;
 }
 
 // Pair e of the four pairs of weights of a row that its P copies hold in order,
@@ -373,7 +352,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, DC <= (P == 1 ? 2 : 4) ? 3 : 2) 
 void kv4_few_kernel(Kv4AttendProblem p)
 {
     constexpr int PD = 32 * DC, kRows = 16 / P, kDTiles = 2 * DC, kLd = PD + 4, kVWords = (DC + 3) / 4, E = 8 / P;
-    __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows], sm_far[kAttendWaves][kRows];
+    __shared__ float sm_m[kAttendWaves][kRows], sm_l[kAttendWaves][kRows], sm_top[kAttendWaves][kRows];
     __shared__ __align__(16) float sm_o[kAttendWaves][kRows * kLd];
     typedef typename T::elem elem;
     const int lane = threadIdx.x & 63, c = lane & 15, kq = lane >> 4, copy = c / kRows;
@@ -428,8 +407,8 @@ void kv4_few_kernel(Kv4AttendProblem p)
         const int end = to < last - begin ? begin + to : last;
 
         f32x4 o[kDTiles] = {};
-        float m = -__builtin_inff(), l = 0.0f, far = 0.0f;
-        bool is_far = false;
+        float m = -__builtin_inff(), l = 0.0f;            // what scores are relative to; sum of the weights
+        float top_w = 0.0f, unit = power(unit_of(0.0f));  // largest product when the unit was made; what products are multiplied by
 
         QOperand4<T> q[DC];
         float row_factor;
@@ -525,7 +504,7 @@ void kv4_few_kernel(Kv4AttendProblem p)
             const Scales own = scales;
             scales = load_scales(then);
             // Token i of this lane: number 16 * half + 4 kq + i % 4 of the turn.
-            float g[E], ev[E];
+            float g[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 // x * 0 + x: a scale that is not finite becomes NaN.
@@ -539,8 +518,6 @@ void kv4_few_kernel(Kv4AttendProblem p)
                     if (!good) g[i] = __builtin_nanf("");
                 }
             }
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) exponents_of(own.v[i], ev[2 * i], ev[2 * i + 1]);
             Frag ph, pl;
             float z[E];
 #pragma unroll
@@ -553,65 +530,52 @@ void kv4_few_kernel(Kv4AttendProblem p)
                 }
                 if (sizeof(elem) == 4) z[i] *= row_factor;
             }
-            float y[E];
-#pragma unroll
-            for (int i = 0; i < E; ++i) y[i] = __builtin_fmaf(z[i], g[i], ev[i]);
             unsigned sees = ~0u;  // bits of the tokens that the row sees
+#pragma unroll
+            for (int i = 0; i < E; ++i) z[i] *= g[i];
             if (cut) {
                 sees = 0;
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     const int half = P == 1 ? i / 4 : copy * 2 / P, at = P == 1 ? i % 4 : copy * E % 4 + i;
                     const bool yes = unsigned(32 * turn + 16 * half + 4 * kq + at - lo_t) < unsigned(n_t);
-                    y[i] = yes ? y[i] : -__builtin_inff();
+                    z[i] = yes ? z[i] : -__builtin_inff();
                     sees |= yes ? 1u << i : 0u;
                 }
             }
-            float x[E], w[E], pe[E];
-            auto shrink = [&](float a) {
-                l *= a;
+            float w[E], top = z[0], a = 1.0f;
 #pragma unroll
-                for (int j = 0; j < kDTiles; ++j) o[j] *= a;
-            };
-            if (!is_far) {
-                float top = y[0];
-#pragma unroll
-                for (int i = 1; i < E; ++i) top = __builtin_fmaxf(top, y[i]);
+            for (int i = 1; i < E; ++i) top = __builtin_fmaxf(top, z[i]);
+            const bool risen = __ballot(top > m) != 0;
+            if (risen) {
                 top = column_max(copies_max<P>(top));
-                if (__ballot(top > m) != 0) {
-                    const float risen = __builtin_fmaxf(m, top);
-                    is_far = beyond_near(risen);
-                    if (!is_far) {
-                        const float a = rescale(m, risen);
-                        m = risen;
-                        shrink(a);
-                    }
-                }
-                const float base = m == -__builtin_inff() ? 0.0f : m - kTarget;
-#pragma unroll
-                for (int i = 0; i < E; ++i) x[i] = __builtin_fmaf(z[i], g[i], -base);
+                const float to = top > m ? top + kAbove : m;
+                a = rescale(m, to);
+                m = to;
+                l *= a;
             }
-            if (is_far) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) x[i] = sees >> i & 1 ? z[i] * g[i] : -__builtin_inff();
-                shrink(far_exponents<P>(x, ev, far, m));
-            }
+            const float base = __builtin_fmaxf(m, -3.402823466e38f);  // finite where a row has seen nothing
+            float largest = 0.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                pe[i] = __builtin_amdgcn_exp2f(x[i]);
+                float pe = __builtin_amdgcn_exp2f(z[i] - base);
                 // A scale that is not finite makes the whole row NaN, by w or by its parts.
-                w[i] = pe[i] * bits_f32(i & 1 ? own.v[i / 2] & 0xffff0000u : own.v[i / 2] << 16);
+                w[i] = pe * bits_f32(i & 1 ? own.v[i / 2] & 0xffff0000u : own.v[i / 2] << 16);
+                if (cut && !(sees >> i & 1)) pe = w[i] = 0.0f;
+                l += pe;
+                largest = __builtin_fmaxf(largest, __builtin_fabsf(w[i]));
             }
-            if (cut) {
+            if (risen || __ballot(0.5f * largest > top_w) != 0) {
+                const float to = __builtin_fmaxf(top_w * a, column_max(copies_max<P>(largest)));
+                const float b = to_unit(a, top_w, to);
 #pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (!(sees >> i & 1)) pe[i] = w[i] = 0.0f;
+                for (int j = 0; j < kDTiles; ++j) o[j] *= b;
+                top_w = to;
+                unit = power(unit_of(to));
             }
-#pragma unroll
-            for (int i = 0; i < E; ++i) l += pe[i];
             std::uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) split2(w[2 * i], w[2 * i + 1], hi[i], lo[i]);
+            for (int i = 0; i < E / 2; ++i) split2(w[2 * i], w[2 * i + 1], unit, hi[i], lo[i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 ph.v[e] = from_copy<P>(hi, e);
@@ -656,7 +620,7 @@ void kv4_few_kernel(Kv4AttendProblem p)
         // A row that sees no token is 0 / 1; one whose scores are all -inf is 0 / 0.
         const float sum = column_sum(copies_sum<P>(l));
         if (c < kRows) {
-            if (kq == 0) sm_m[wave][c] = m, sm_far[wave][c] = far, sm_l[wave][c] = n_t == 0 ? 1.0f : sum;
+            if (kq == 0) sm_m[wave][c] = m, sm_top[wave][c] = top_w, sm_l[wave][c] = n_t == 0 ? 1.0f : sum;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -669,26 +633,28 @@ void kv4_few_kernel(Kv4AttendProblem p)
         constexpr int kQuads = PD / 4, kStep = 64 * kAttendWaves / kQuads;
         const int d = int(threadIdx.x) % kQuads * 4;
         for (int i = int(threadIdx.x) / kQuads; i < rows; i += kStep) {
-            float far = sm_far[0][i], top = sm_m[0][i], sum = 0.0f;
+            float m = sm_m[0][i], top = 0.0f, sum = 0.0f;
 #pragma unroll
-            for (int w = 1; w < kAttendWaves; ++w) raise(far, top, sm_far[w][i], sm_m[w][i]);
+            for (int w = 1; w < kAttendWaves; ++w) m = __builtin_fmaxf(m, sm_m[w][i]);
+#pragma unroll
+            for (int w = 0; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, sm_top[w][i] * rescale(sm_m[w][i], m));
             f32x4 x = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < kAttendWaves; ++w) {
-                const float a = rescale_far(sm_far[w][i], sm_m[w][i], far, top);
+                const float a = rescale(sm_m[w][i], m);
                 sum += sm_l[w][i] * a;
-                x += *reinterpret_cast<const f32x4 *>(&sm_o[w][i * kLd + d]) * a;
+                x += *reinterpret_cast<const f32x4 *>(&sm_o[w][i * kLd + d]) * to_unit(a, sm_top[w][i], top);
             }
             if (!Full && d >= dim) continue;
             if (part < 0) {
                 const int fresh = int(unsigned(rest0 + i) / unsigned(R));
-                x = x / sum;
+                x = in_values(x / sum, top);
                 if (seen.beyond_new(fresh0 + fresh)) x = x * __builtin_nanf("");
                 __builtin_memcpy(p.O + (s.row0 + fresh0 + fresh) * p.ldo + (head * R + rest0 + i - fresh * R) * p.hso + d, &x, sizeof(x));
             } else {
                 const std::int64_t at = ((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + part) * kRows + i;
                 *reinterpret_cast<f32x4 *>(p.ws + at * (dim + 4) + d) = x;
-                if (d == 0) p.ws[at * (dim + 4) + dim] = top, p.ws[at * (dim + 4) + dim + 1] = sum, p.ws[at * (dim + 4) + dim + 2] = far;
+                if (d == 0) p.ws[at * (dim + 4) + dim] = m, p.ws[at * (dim + 4) + dim + 1] = sum, p.ws[at * (dim + 4) + dim + 2] = top;
             }
         }
         __syncthreads();
@@ -767,7 +733,7 @@ void kv4_few_kernel(Kv4AttendProblem p)
 template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendProblem p)
 {
     constexpr int kAtOnce = 4, kRowsHere = kAttendWaves / W;
-    __shared__ float sm_top[kAttendWaves], sm_sum[kAttendWaves], sm_far[kAttendWaves];
+    __shared__ float sm_m[kAttendWaves], sm_top[kAttendWaves], sm_sum[kAttendWaves];
     __shared__ __align__(16) float sm_x[W > 1 ? kAttendWaves : 1][256];
     const int lane = threadIdx.x & 63, R = p.heads_q / p.c.heads, dim = p.c.dim, shift = 31 - __builtin_clz(unsigned(p.c.block));
     const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = all_waves % W;
@@ -783,12 +749,12 @@ template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kerne
     if (row >= s.n * R || parts == 0) return;  // with W > 1 this is the same for all waves
     const std::int64_t pitch = std::int64_t(Rows) * (dim + 4);
     const float *const part = p.ws + (((std::int64_t(head) * p.plan.tiles + tile) * p.plan.parts + slot + seq) * Rows + i) * (dim + 4);
-    float top = -__builtin_inff(), far = 0.0f, sum = 0.0f;
+    float m = -__builtin_inff(), top = 0.0f, sum = 0.0f;
     f32x4 y = {0, 0, 0, 0};
     const float *const at = part + (4 * lane < dim ? 4 * lane : 0);
     for (int x0 = wave; x0 < parts; x0 += W * kAtOnce) {
         f32x4 v[kAtOnce];
-        f32x4 stand[kAtOnce];  // m, sum and far
+        f32x4 stand[kAtOnce];  // m, sum and largest product
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int x = x0 + W * j < parts ? x0 + W * j : x0;
@@ -799,30 +765,33 @@ template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kerne
         for (int j = 0; j < kAtOnce; ++j) {
             if (x0 + W * j >= parts) continue;
             // A part that saw nothing of its row weighs nothing: its sums are zeros.
-            const float from = far, m = top;
-            raise(far, top, stand[j][2], stand[j][0]);
-            const float a = rescale_far(from, m, far, top), b = rescale_far(stand[j][2], stand[j][0], far, top);
+            const float to = __builtin_fmaxf(m, stand[j][0]), a = rescale(m, to), b = rescale(stand[j][0], to);
+            const float largest = __builtin_fmaxf(top * a, stand[j][2] * b);
             sum = sum * a + stand[j][1] * b;
-            y = y * a + v[j] * b;
+            y = y * to_unit(a, top, largest) + v[j] * to_unit(b, stand[j][2], largest);
+            m = to;
+            top = largest;
         }
     }
     if constexpr (W > 1) {
-        if (lane == 0) sm_top[wave] = top, sm_sum[wave] = sum, sm_far[wave] = far;
+        if (lane == 0) sm_m[wave] = m, sm_top[wave] = top, sm_sum[wave] = sum;
         if (4 * lane < dim) *reinterpret_cast<f32x4 *>(&sm_x[wave][4 * lane]) = y;
         __syncthreads();
         if (wave != 0) return;
-        for (int w = 1; w < W; ++w) raise(far, top, sm_far[w], sm_top[w]);
+        for (int w = 1; w < W; ++w) m = __builtin_fmaxf(m, sm_m[w]);
+        top = 0.0f;
+        for (int w = 0; w < W; ++w) top = __builtin_fmaxf(top, sm_top[w] * rescale(sm_m[w], m));
         sum = 0.0f;
         y = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float a = rescale_far(sm_far[w], sm_top[w], far, top);
+            const float a = rescale(sm_m[w], m);
             sum += sm_sum[w] * a;
-            if (4 * lane < dim) y += *reinterpret_cast<const f32x4 *>(&sm_x[w][4 * lane]) * a;
+            if (4 * lane < dim) y += *reinterpret_cast<const f32x4 *>(&sm_x[w][4 * lane]) * to_unit(a, sm_top[w], top);
         }
     }
     if (4 * lane >= dim) return;
-    y = y / sum;
+    y = in_values(y / sum, top);
     const std::int64_t fresh = divide(row, R);
     const KvSeen seen{s.len - s.n, s.len, std::int64_t(p.b.table_ld) << shift, 1, p.causal, p.window};
     if (seen.beyond_new(fresh)) y = y * __builtin_nanf("");
@@ -833,16 +802,14 @@ template <int Rows, int W> __global__ __launch_bounds__(256) void kv4_join_kerne
 // and values pass through the compute unit's cache for all four. A wave keeps 32
 // rows, so that a code is converted once for them.
 //
-// 2 prompts of 1024 rows behind 4096 tokens in f16: 211 us, 564 TFLOP/s, bound by
-// the SIMDs: vector instructions take 75% of the cycles a compute unit is busy,
-// matrix instructions 37%, two of three of those for the second part of the
-// weights and the first. Codes converted once for the four waves and laid in LDS
-// need a quarter fewer vector instructions, but their barriers and reads cost
-// more than that: 233 to 246 us, with four waves or eight and two to four a SIMD.
-//
-// Rows that are far are found when m rises, and a tile that had one is done once
-// more with care for them: within the loop that care costs every tile 7%, the
-// look at m 1.5%.
+// 2 prompts of 1024 rows behind 4096 tokens in f16: 206 us, 577 TFLOP/s. As it
+// is, a SIMD is busy issuing: of its cycles vector instructions take 62% (the
+// exponentials' longer turn not counted) and matrix instructions 40%, two of three
+// of those for the second part of the weights and the first. Codes converted once
+// for the four waves and laid in LDS need a quarter fewer vector instructions, but
+// their barriers and reads cost more than that: 233 to 246 us when the rest took
+// 216, with four waves or eight and two to four a SIMD. More than 32 rows a wave were
+// not tried.
 template <class T, int DC, bool Full, int MT>
 __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4AttendProblem p)
 {
@@ -906,10 +873,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
             const int inner = int((unsigned(last_lo) + 31u) >> 5), outer = (first_lo + first_n) >> 5;
 
             f32x4 o[MT][kDTiles] = {};
-            float m[MT], l[MT], far[MT];
-            bool far_off = false;  // some row has gone where it ought to be far
+            float m[MT], l[MT];         // what scores are relative to; sum of the weights
+            float top_w[MT], unit[MT];  // largest product when the unit was made; what products are multiplied by
 #pragma unroll
-            for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = far[t] = 0.0f;
+            for (int t = 0; t < MT; ++t) m[t] = -__builtin_inff(), l[t] = top_w[t] = 0.0f, unit[t] = power(unit_of(0.0f));
 
             // The page of a half turn, and where its first token lies; `good`: it may be read.
             struct Half {
@@ -953,10 +920,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                 }
             };
 
-            // Turns from .. to; Cut: some row does not see all of a turn; Far: some
-            // row is far.
-            auto turns = [&](int from, int to, auto cut_, auto far_) {
-                constexpr bool Cut = decltype(cut_)::value, Far = decltype(far_)::value;
+            // Turns from .. to; Cut: some row does not see all of a turn.
+            auto turns = [&](int from, int to, auto cut_) {
+                constexpr bool Cut = decltype(cut_)::value;
                 int turn = from;
                 if (turn >= to) return;
                 bool good[2];  // of this turn's halves
@@ -970,7 +936,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                     const int t0 = 32 * turn, tn = turn + 1 < to ? t0 + 32 : t0;
                     const Half next[2] = {half_at(tn), half_at(tn + 16)};
                     f32x4 acc[2][MT];
-                    float g[8], ev[8];
+                    float g[8];
                     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -991,70 +957,79 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
 #pragma unroll
                             for (int r = 0; r < 4; ++r) g[4 * x + r] = __builtin_nanf("");
                         }
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) exponents_of(vs[x][r], ev[4 * x + 2 * r], ev[4 * x + 2 * r + 1]);
                     }
                     __builtin_amdgcn_s_setprio(0);
                     load_keys(next);
                     good[0] = next[0].good, good[1] = next[1].good;
+                    // Both groups of rows go side by side, with one look at all largest scores and
+                    // one at all largest products (one after the other: 211 us instead of 206).
                     Frag ph[MT], pl[MT];
+                    float z[MT][8], w[MT][8], a[MT];
+                    unsigned sees[MT];  // bits of the tokens that the row sees
+                    bool rises = false;
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
-                        unsigned sees = 0;  // bits of the tokens that the row sees
-                        float x[8], w[8];
-                        auto shrink = [&](float a) {
-                            l[t] *= a;
-#pragma unroll
-                            for (int j = 0; j < kDTiles; ++j) o[t][j] *= a;
-                        };
-                        auto sees_token = [&](int e) { return unsigned(t0 + 16 * (e / 4) + 4 * kq + e % 4 - lo_t[t]) < unsigned(n_t[t]); };
-                        if constexpr (!Far) {
-                            float top = -__builtin_inff();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float y = __builtin_fmaf(acc[e / 4][t][e % 4], g[e], ev[e]);
-                                if (Cut) {
-                                    const bool yes = sees_token(e);
-                                    y = yes ? y : -__builtin_inff();
-                                    sees |= yes ? 1u << e : 0u;
-                                }
-                                top = __builtin_fmaxf(top, y);
-                            }
-                            top = column_max(top);
-                            if (__ballot(top > m[t]) != 0) {
-                                const float risen = __builtin_fmaxf(m[t], top), a = rescale(m[t], risen);
-                                far_off |= beyond_near(risen);
-                                m[t] = risen;
-                                shrink(a);
-                            }
-                            const float base = m[t] == -__builtin_inff() ? 0.0f : m[t] - kTarget;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(acc[e / 4][t][e % 4], g[e], -base);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const bool yes = !Cut || sees_token(e);
-                                x[e] = yes ? acc[e / 4][t][e % 4] * g[e] : -__builtin_inff();
-                                sees |= yes ? 1u << e : 0u;
-                            }
-                            shrink(far_exponents<1>(x, ev, far[t], m[t]));
-                        }
+                        float top = -__builtin_inff();
+                        sees[t] = 0;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            float pe = __builtin_amdgcn_exp2f(x[e]);
-                            // A scale that is not finite makes the whole row NaN, by w or by its parts.
-                            w[e] = pe * scale_of(vs[e / 4], e % 4);
-                            if (Cut && !(sees >> e & 1)) pe = w[e] = 0.0f;
-                            l[t] += pe;
+                            z[t][e] = acc[e / 4][t][e % 4] * g[e];
+                            if (Cut) {
+                                const bool yes = unsigned(t0 + 16 * (e / 4) + 4 * kq + e % 4 - lo_t[t]) < unsigned(n_t[t]);
+                                z[t][e] = yes ? z[t][e] : -__builtin_inff();
+                                sees[t] |= yes ? 1u << e : 0u;
+                            }
+                            top = __builtin_fmaxf(top, z[t][e]);
                         }
+                        a[t] = top;
+                        rises |= top > m[t];
+                    }
+                    const bool risen = __ballot(rises) != 0;
+                    if (__builtin_expect(risen, 0)) {
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            const float top = column_max(a[t]), to = top > m[t] ? top + kAbove : m[t];
+                            a[t] = rescale(m[t], to);
+                            m[t] = to;
+                            l[t] *= a[t];
+                        }
+                    }
+                    float largest[MT];
+                    rises = risen;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const float base = __builtin_fmaxf(m[t], -3.402823466e38f);  // finite where a row has seen nothing
+                        largest[t] = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float pe = __builtin_amdgcn_exp2f(z[t][e] - base);
+                            // A scale that is not finite makes the whole row NaN, by w or by its parts.
+                            w[t][e] = pe * scale_of(vs[e / 4], e % 4);
+                            if (Cut && !(sees[t] >> e & 1)) pe = w[t][e] = 0.0f;
+                            l[t] += pe;
+                            largest[t] = __builtin_fmaxf(largest[t], __builtin_fabsf(w[t][e]));
+                        }
+                        rises |= 0.5f * largest[t] > top_w[t];
+                    }
+                    if (__builtin_expect(__ballot(rises) != 0, 0)) {
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            const float by = risen ? a[t] : 1.0f, to = __builtin_fmaxf(top_w[t] * by, column_max(largest[t])), b = to_unit(by, top_w[t], to);
+#pragma unroll
+                            for (int j = 0; j < kDTiles; ++j) o[t][j] *= b;
+                            top_w[t] = to;
+                            unit[t] = power(unit_of(to));
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             std::uint32_t hi, lo;
-                            split2(w[2 * e], w[2 * e + 1], hi, lo);
+                            split2(w[t][2 * e], w[t][2 * e + 1], unit[t], hi, lo);
                             ph[t].v[e] = hi;
                             pl[t].v[e] = lo;
                         }
-                    }
                     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                     for (int i = 0; i < kVWords; ++i) {
@@ -1092,21 +1067,11 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
             };
             if (inner < outer) {
                 const int a = inner < end ? (inner > begin ? inner : begin) : end, b = outer < end ? (outer > a ? outer : a) : end;
-                turns(begin, a, std::true_type{}, std::false_type{});
-                turns(a, b, std::false_type{}, std::false_type{});
-                turns(b, end, std::true_type{}, std::false_type{});
+                turns(begin, a, std::true_type{});
+                turns(a, b, std::false_type{});
+                turns(b, end, std::true_type{});
             } else {
-                turns(begin, end, std::true_type{}, std::false_type{});
-            }
-            if (far_off) {
-                // Seldom: once more from the start.
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    m[t] = -__builtin_inff(), l[t] = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < kDTiles; ++j) o[t][j] = f32x4{0, 0, 0, 0};
-                }
-                turns(begin, end, std::true_type{}, std::true_type{});
+                turns(begin, end, std::true_type{});
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
@@ -1128,6 +1093,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
                     f32x4 y;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) y[j] = o[t][(x + j) % kDTiles][x / kDTiles] * inverse;
+                    y = in_values(y, top_w[t]);
                     __builtin_memcpy(dst + x, &y, sizeof(y));
                 }
             }

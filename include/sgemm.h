@@ -707,9 +707,11 @@ int sgemm_kv4_check_args(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *ba
  *
  * Scores are <Q, code> in float32 times scale * log2(e) * K's scale, and have to
  * stay within float32's normal numbers, as has a value itself. float32 queries
- * are held to 2^-22 of a component or 2^-39 of the row's largest, products of a
- * weight and a value's scale to 2^-22 of themselves or 2^-39 of the row's
- * largest, whichever is more; scales of V below 2^-90 count as 2^-90 there.
+ * are held to 2^-22 of a component or 2^-39 of the row's largest. Weights are
+ * exponentials in float32, good to 2^-22 besides what their scores are off by;
+ * those below 2^-122 of the row's largest are 0. Their products with a value's
+ * scale are held to 2^-22 of themselves or 2^-38 of the row's largest, whichever
+ * is more, with products below 2^-100 counted as that.
  */
 int sgemm_kv4_attend(const sgemm_kv4_cache *cache, const sgemm_kv8_batch *batch, int dtype, int heads_q,
                      const void *Q, int ldq, int hsq,
