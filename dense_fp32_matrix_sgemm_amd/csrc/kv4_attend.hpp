@@ -339,13 +339,18 @@ __device__ inline Kv4Shares kv4_shares(const Kv4AttendProblem &p, const Kv4Group
 // that may not be read are replaced by page 0 and their scores by NaN.
 //
 // Where a sequence's keys are read by one tile only and one load of a wave
-// covers whole lines (64 and 128 components), they are kept out of the caches:
-// 50.3 us instead of 55.4 in a graph for the batch below, 50.7 instead of 51.7
-// with 64 components. Values, whose lines take several loads, lost by it (51.7
-// with both), and so did keys of 80 components (34.8 -> 36.1), 192 and 256.
+// covers whole lines (64 and 128 components), they are kept out of the caches. In a
+// graph of three batches in turn, 32 x 8192 tokens of 128 components 50.0 us
+// instead of 55.4, 64 x 4096 50.8 instead of 56.3, 32 x 4096 33.9 instead of 35.3, of 64
+// components 38.6, 38.6 and 29.1 instead of 39.2, 39.9 and 28.7; up to 32 x 2000 no
+// difference beyond 3% either way. One batch alone, again and again, that the chip's
+// caches hold whole loses up to 2% (32 x 8192 47.9 instead of 47.3, 32 x 2000 26.3
+// instead of 26.9). So the rule has no size in it. Values, whose lines take several
+// loads, lost by it (51.7 with both when keys alone took 50.3), and so did keys of 80
+// components (34.8 -> 36.1), 192 and 256.
 //
 // 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 query heads each
-// (0.21 GB): 42.6 us, 5.0 TB/s, and 4.7 for the join; with equal splits of each
+// (0.21 GB): 41.8 us, 5.0 TB/s, and 4.8 for the join; with equal splits of each
 // sequence instead of equal shares, and no copies, 10% more. Bound by memory.
 template <class T, int DC, bool Full, int P>
 __global__ __launch_bounds__(64 * kAttendWaves, DC <= (P == 1 ? 2 : 4) ? 3 : 2)  // as many a compute unit as plan_kv4_attend counts on
