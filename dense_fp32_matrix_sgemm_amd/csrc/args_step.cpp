@@ -249,7 +249,10 @@ Kv4Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int 
     if (window > 0 && tokens > window + new_rows) tokens = window + new_rows;
     i64 slots = resident * i64(cus) / units, room = i64(b.seqs) * (tokens / (32 * kKv4LeastTurns));
     if (slots > room) slots = room;
-    if (slots > 64 * i64(b.seqs)) slots = 64 * i64(b.seqs);
+    // 64 for each sequence at most, on average, as the join has to add what they leave:
+    // 1 sequence of 131072 tokens and 1, 2, 4 and 8 cache heads 31, 32, 33 and 39 us,
+    // with 192 at most 34, 37, 41 and 42, with all that fit 57, 51, 40 and 42.
+    if (slots > kMostParts * i64(b.seqs)) slots = kMostParts * i64(b.seqs);
     if (slots <= b.seqs && room <= b.seqs) return plan;  // no sequence long enough to be shared
     if (slots < 1) return plan;
     // A whole number for each sequence, if that leaves out few: sequences of one

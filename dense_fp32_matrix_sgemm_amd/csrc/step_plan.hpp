@@ -33,6 +33,9 @@ constexpr int kKv4SplitBytes = 8;
 // them all up.
 constexpr int kMostShared = 1024;
 
+// Work-groups that share the tokens of a tile's sequences at most, for each sequence.
+constexpr int kMostParts = 64;
+
 Kv4Plan plan_kv4_attend(const sgemm_kv4_cache &c, const sgemm_kv8_batch &b, int heads_q, int window, int cus);
 
 // Whether sgemm_kv4_write's arrays overlap one another or the batch's.
