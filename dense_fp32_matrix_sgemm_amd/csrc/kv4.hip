@@ -8,12 +8,15 @@
 // two), whose maximum goes round by lane exchanges. A thread has four units in
 // flight: with two or eight, or 512 or 1024 threads, nothing was gained.
 //
-// 4 prompts of up to 4096 tokens, 8 heads of 128 in bf16: write 17.8 us for 61 MB
-// (3.4 TB/s), of which its vector instructions take a third, read 13.3 for 64 MB
-// (4.8; 16.0 with outputs through the caches); 64 sequences of one token: write 4.4 us, three round trips, and 128
-// tokens of each read into float32 17.5 for 76 MB (4.3). Loads and stores of a
-// row wait for its page, and that for the sequence: more units in flight did not
-// help, so what is left is the memory's turn from reading to writing.
+// 4 prompts of up to 4096 tokens, 8 heads of 128 in bf16: write 17.5 us for 61 MB
+// (3.5 TB/s), of which its vector instructions take a third, read 13.3 for 64 MB
+// (4.8; 16.0 with outputs through the caches); 64 sequences of one token: write 3.8 us, three round trips, and 128
+// tokens of each read into float32 17.6 for 76 MB (4.3). When rows are written
+// they are loaded first, as soon as their sequence is known, and only the stores
+// wait for their pages; when rows are read back, the loads do. More units in flight
+// did not help either. What keeps the write from a copy's rate was not found out: a
+// wave stores pieces of 64 bytes for each of four heads, and each scale apart,
+// 2 bytes in a line of its own; another order was not tried.
 //
 // x / scale is needed to the last bit next to the midpoints of e2m1. The
 // quotient is formed as y = x r with r = 1 / scale, and corrected once by its

@@ -344,8 +344,8 @@ __device__ inline Kv4Shares kv4_shares(const Kv4AttendProblem &p, const Kv4Group
 // instead of 55.4, 64 x 4096 50.8 instead of 56.3, 32 x 4096 33.9 instead of 35.3, of 64
 // components 38.6, 38.6 and 29.1 instead of 39.2, 39.9 and 28.7; up to 32 x 2000 no
 // difference beyond 3% either way. One batch alone, again and again, that the chip's
-// caches hold whole loses up to 2% (32 x 8192 47.9 instead of 47.3, 32 x 2000 26.3
-// instead of 26.9). So the rule has no size in it. Values, whose lines take several
+// caches hold whole loses up to 3% (32 x 8192 47.9 instead of 47.3, 64 x 4096 of 64
+// components 38.6 instead of 37.7). So the rule has no size in it. Values, whose lines take several
 // loads, lost by it (51.7 with both when keys alone took 50.3), and so did keys of 80
 // components (34.8 -> 36.1), 192 and 256.
 //
