@@ -5,10 +5,10 @@ helpers.
 
 Like the rest of the binding it only marshals arguments: the kernels are
 enqueued on the current stream of the operands' device, nothing waits, and a
-refused argument raises. The raw entry points take the C ABI's arguments in
-its order; ``cache``, ``batch`` and ``step`` are :class:`KV4Cache`,
-``KV8Batch`` and :class:`KVStep` structures, ``first`` and ``second``
-:class:`RopeRows`.
+refused argument raises. Of the helpers :func:`rope` alone has a gradient.
+The raw entry points take the C ABI's arguments in its order; ``cache``,
+``batch`` and ``step`` are :class:`KV4Cache`, ``KV8Batch`` and
+:class:`KVStep` structures, ``first`` and ``second`` :class:`RopeRows`.
 """
 
 from __future__ import annotations

@@ -176,3 +176,33 @@ def test_the_largest_product_changes_with_the_largest_score(layout, dtype):
         Q[..., 0] = sign * 100.0  # scores up to 12.5 log2(e) = 18 binary digits apart
         Q[:, :, 1] = 4.0
         held(case, Q, dtype, True, 0, max(new), f"{layout} {sign} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_powers_of_two_pass_through(layout, dtype):
+    # Values' scales times 2^k give the same rows times 2^k, to the bit: products are
+    # held relative to their row's largest, and weights do not know of the scales.
+    lens, new, heads = LAYOUTS[layout]
+    case = Case4(41, lens, new, heads, 16, 96)
+    Q = case.normal(3 * heads, dtype).cuda()
+    s = case.ref.scales[1].copy()
+    want = sg.kv4_attend(Q, case.device(), *case.args(), max_new=max(new))
+    for k in (-80, -30, 1, 30, 90, 124):
+        case.ref.scales[1] = s * 2.0**k
+        got = sg.kv4_attend(Q, case.device(), *case.args(), max_new=max(new))
+        assert torch.equal(got.double() * 2.0**-k, want.double()), (layout, dtype, k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_one_token_is_read_as_it_is(dtype):
+    # A window of one: the weight is its own normaliser, up to a rounding of each of product, parts and quotient.
+    for layout in LAYOUTS:
+        lens, new, heads = LAYOUTS[layout]
+        case = Case4(43, lens, new, heads, 16, 64)
+        Q = case.normal(heads, dtype).cuda()
+        got = sg.kv4_attend(Q, case.device(), *case.args(), window=1, max_new=max(new)).cpu().double().numpy()
+        for b, l in enumerate(lens):
+            v = case.ref.tokens(case.table, b, l, 1)[l - new[b]:]
+            o = got[case.starts[b]:case.starts[b + 1]]
+            assert (np.abs(o - v) <= 6 * U * np.abs(v)).all(), (layout, b)
