@@ -485,6 +485,7 @@ void kv4_few_kernel(Kv4AttendProblem p)
         };
 
         auto work = [&](int turn, int next) {
+#pragma clang fp contract(off)  // a score is rounded before m is taken off it: equal scores are then equal to the bit, and none is above m
             const bool cut = turn < inner || turn >= outer;  // some row does not see all of the turn
             const Place then = place_of(next);
             f32x4 acc[2];
@@ -927,6 +928,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, 2) void kv4_rows_kernel(Kv4Atten
 
             // Turns from .. to; Cut: some row does not see all of a turn.
             auto turns = [&](int from, int to, auto cut_) {
+#pragma clang fp contract(off)  // as for few rows
                 constexpr bool Cut = decltype(cut_)::value;
                 int turn = from;
                 if (turn >= to) return;
